@@ -102,9 +102,16 @@ enum {
   KVQ_DEVERR_CONTEXT_RANGE = 1u << 2, /* context_len < 0 or > max_blocks_per_seq * bs
                                          or > max_context_len                             */
   KVQ_DEVERR_TIMEOUT = 1u << 3,       /* a bounded wait on an mbarrier ran out           */
-  KVQ_DEVERR_CHANNEL_RUN = 1u << 4    /* per-channel K: a run of tokens into a block does
+  KVQ_DEVERR_CHANNEL_RUN = 1u << 4,   /* per-channel K: a run of tokens into a block does
                                          not fill the block's rows from row 0 in order
                                          (see kvq_quantize_write)                         */
+  KVQ_DEVERR_CAPACITY = 1u << 5,      /* kvq_assign_blocks: too few free blocks, or more
+                                         new tokens than max_tokens                       */
+  KVQ_DEVERR_POOL_STATE = 1u << 6,    /* block pool: a free count or free block out of
+                                         range, a block given back more often than held,
+                                         an append into a block that other rows share      */
+  KVQ_DEVERR_GROUP_RANGE = 1u << 7    /* kvq_prefix_decode: group_starts out of order or
+                                         outside [0, batch]                               */
 };
 
 /* Layout of one layer's paged cache.  Supported combinations:
@@ -303,6 +310,127 @@ int kvq_prefetch_blocks(const kvq_format *fmt, kvq_caches host_caches, kvq_scale
                         int64_t host_num_blocks, const int32_t *src_blocks,
                         const int32_t *dst_blocks, int32_t num_pairs, kvq_caches caches,
                         kvq_scales scales, kvq_stream_t stream);
+
+/*
+ * kvq_assign_blocks / kvq_release_blocks -- block tables and slot mappings
+ * made on the device from request lengths, and blocks given back ("Quantized
+ * KV caches in production", PagedAttention: a sequence's blocks are found
+ * through its table; the allocator is this library's).
+ *
+ * The pool holds the blocks that no row uses as a stack, and how many rows
+ * use each block (rows share blocks of a common prefix).  It starts with
+ * every block free: free_list any permutation of [0, num_blocks), free_count
+ * num_blocks, ref_counts 0.
+ */
+typedef struct {
+  int32_t *free_list;  /* [num_blocks], entries [0, free_count) free, the last one goes next */
+  int32_t *free_count; /* [1]                                                              */
+  int32_t *ref_counts; /* [num_blocks] rows that use the block                             */
+  int64_t num_blocks;
+} kvq_block_pool;
+
+/*
+ * kvq_assign_blocks -- room for new_lens[r] more tokens of every row r.
+ *
+ *   new_lens       [num_rows] int32, >= 0
+ *   context_lens   [num_rows] int32, tokens the row holds (updated)
+ *   block_tables   [num_rows, max_blocks_per_seq] int32 (updated)
+ *   pool           updated
+ *   prefix_rows, prefix_blocks  [num_rows] int32, or both NULL: row r with
+ *                  prefix_rows[r] = s >= 0 starts with the first
+ *                  prefix_blocks[r] blocks of row s, shared, not copied
+ *                  (context_lens[r] must be 0, and row s must hold those
+ *                  blocks in full before the call)
+ *   max_tokens     host-side size of the token outputs
+ *   token_offsets  [num_rows + 1] int32: row r's new tokens are entries
+ *                  [token_offsets[r], token_offsets[r + 1]) (written)
+ *   slot_mapping   [max_tokens] int64: the tokens' slots, for
+ *                  kvq_quantize_write; -1 (skip) past the last token, so that
+ *                  a captured step of fixed size can be replayed (written)
+ *   positions      [max_tokens] int32: the tokens' positions in their rows,
+ *                  -1 past the last token (written), or NULL
+ *
+ * The result is that of the loop
+ *   for r = 0, 1, ...: take the shared blocks (their counts go up by 1), set
+ *     context_lens[r] = 16 prefix_blocks[r];
+ *     for every block that [context_lens[r], context_lens[r] + new_lens[r])
+ *       enters: pop one from free_list, its count is 1;
+ *     context_lens[r] += new_lens[r].
+ * All or nothing: with an argument out of range (KVQ_DEVERR_CONTEXT_RANGE,
+ * KVQ_DEVERR_BLOCK_RANGE), too few free blocks or too many tokens
+ * (KVQ_DEVERR_CAPACITY), or a row that would append into a block whose count
+ * is not 1 (KVQ_DEVERR_POOL_STATE), the bit is set, no row, table or pool
+ * entry changes, token_offsets are 0 and the slots are -1.
+ *
+ * kvq_release_blocks -- every row keeps its first keep_lens[r] tokens (0: it
+ * is done; context_lens[r] or more: nothing changes) and gives back the
+ * blocks past them: table entries become -1, counts go down by 1, and blocks
+ * that nobody uses are pushed, as the loop over r and the row's blocks from
+ * last to first would.  A release back to the lengths before an assign leaves
+ * the pool as it was before the assign.  A negative keep_lens or a context out of
+ * range sets KVQ_DEVERR_CONTEXT_RANGE and leaves the row alone; a table entry
+ * outside [0, num_blocks) sets KVQ_DEVERR_BLOCK_RANGE and is only cleared.
+ *
+ * Each is one launch; it may be captured and replayed.  The pool, tables and
+ * lengths are read and written by one call at a time (order calls on streams).
+ * num_rows <= 8192, num_rows * max_blocks_per_seq < 2^31.  Pointers of int32
+ * arrays need 4-byte, of slot_mapping 8-byte alignment.
+ */
+int kvq_assign_blocks(const int32_t *new_lens, int32_t num_rows, int32_t *context_lens,
+                      int32_t *block_tables, int32_t max_blocks_per_seq, kvq_block_pool pool,
+                      const int32_t *prefix_rows, const int32_t *prefix_blocks,
+                      int32_t max_tokens, int32_t *token_offsets, int64_t *slot_mapping,
+                      int32_t *positions, kvq_stream_t stream);
+int kvq_release_blocks(const int32_t *keep_lens, int32_t num_rows, int32_t *context_lens,
+                       int32_t *block_tables, int32_t max_blocks_per_seq, kvq_block_pool pool,
+                       kvq_stream_t stream);
+
+/*
+ * kvq_prefix_decode -- kvq_paged_decode for a batch whose sequences share
+ * prefixes: each shared block is read once per group of sequences, and the
+ * rows of a group are multiplied with it together on the tensor cores.
+ *
+ *   q_bf16, fmt, caches, scales, block_tables, context_lens, max_context_len
+ *                 as kvq_paged_decode; tables and contexts describe whole
+ *                 sequences, prefix included
+ *   group_starts  [num_groups + 1] int32, non-decreasing, in [0, batch]: group
+ *                 g is the sequences [group_starts[g], group_starts[g + 1]).
+ *                 Sequences outside every group share nothing
+ *   prefix_lens   [num_groups] int32: the first 16 floor(prefix_lens[g] / 16)
+ *                 positions of the group's sequences lie in the same physical
+ *                 blocks: their tables agree there, each as far as its context
+ *                 goes (a shorter sequence attends to its own part of them)
+ *   max_prefix_len  host-side upper bound of prefix_lens
+ *   res_k_bf16, res_v_bf16  the full-precision tail of a per-channel K cache,
+ *                 as kvq_kivi_decode, or both NULL
+ *   out_bf16      [batch, num_q_heads, head_dim] BF16 (written)
+ *   workspace     device buffer of at least kvq_prefix_decode_workspace_size()
+ *                 bytes, 256-byte aligned; two calls that may overlap on the
+ *                 GPU (streams, captured graphs) need two
+ *
+ * The result is kvq_paged_decode's (kvq_kivi_decode's with a tail) but for
+ * the prefix's operands: queries, probabilities and scaled codes enter the
+ * matrix products as f16, rounded once (a relative 2^-12 each, with the row's
+ * or tile's power of two taken out; codes alone are exact); products,
+ * softmax statistics and partial outputs are FP32, and the output is rounded
+ * once to BF16, which is coarser.
+ * A group of fewer than two sequences shares nothing and costs what
+ * kvq_paged_decode costs.  A prefix_lens entry outside [0, max_prefix_len]
+ * (KVQ_DEVERR_CONTEXT_RANGE) and groups out of order
+ * (KVQ_DEVERR_GROUP_RANGE) are decoded without sharing; other errors as
+ * kvq_paged_decode.  num_groups <= 8192 (0: group_starts, prefix_lens may be
+ * NULL); batch == 0 is a no-op.
+ */
+int kvq_prefix_decode_workspace_size(const kvq_format *fmt, int32_t batch, int32_t num_q_heads,
+                                     int32_t max_context_len, int32_t num_groups, size_t *bytes);
+int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads,
+                      const kvq_format *fmt, kvq_caches caches, kvq_scales scales,
+                      const int32_t *block_tables, int32_t max_blocks_per_seq,
+                      const int32_t *context_lens, int32_t max_context_len,
+                      const int32_t *group_starts, const int32_t *prefix_lens,
+                      int32_t num_groups, int32_t max_prefix_len, const void *res_k_bf16,
+                      const void *res_v_bf16, void *out_bf16, void *workspace,
+                      size_t workspace_bytes, kvq_stream_t stream);
 
 /*
  * kvq_device_errors -- synchronize `stream`, then return the sticky device

@@ -38,11 +38,15 @@ DEVERR_BLOCK_RANGE = 1 << 1
 DEVERR_CONTEXT_RANGE = 1 << 2
 DEVERR_TIMEOUT = 1 << 3
 DEVERR_CHANNEL_RUN = 1 << 4
+DEVERR_CAPACITY = 1 << 5
+DEVERR_POOL_STATE = 1 << 6
+DEVERR_GROUP_RANGE = 1 << 7
 
 EXPORTED_SYMBOLS = (
     "kvq_quantize_write", "kvq_decode_workspace_size", "kvq_paged_decode",
     "kvq_device_errors", "kvq_status_string", "kvq_version", "kvq_paged_decode_noalloc",
     "kvq_write_decode", "kvq_prefetch_blocks", "kvq_kivi_append", "kvq_kivi_decode", "kvq_build_id",
+    "kvq_assign_blocks", "kvq_release_blocks", "kvq_prefix_decode", "kvq_prefix_decode_workspace_size",
 )
 
 # size of the static scratch of kvq_paged_decode_noalloc (include/kvq.h)
@@ -72,6 +76,11 @@ class _Caches(ctypes.Structure):
 
 class _Scales(ctypes.Structure):
     _fields_ = [("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class _BlockPool(ctypes.Structure):
+    _fields_ = [("free_list", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
+                ("ref_counts", ctypes.c_void_p), ("num_blocks", ctypes.c_int64)]
 
 
 _lib = None
@@ -111,6 +120,15 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.kvq_prefetch_blocks.restype = ctypes.c_int
         lib.kvq_paged_decode_noalloc.argtypes = [vp, i32, i32, fmtp, _Caches, _Scales, vp, i32, vp, i32, vp, vp]
         lib.kvq_paged_decode_noalloc.restype = ctypes.c_int
+        lib.kvq_assign_blocks.argtypes = [vp, i32, vp, vp, i32, _BlockPool, vp, vp, i32, vp, vp, vp, vp]
+        lib.kvq_assign_blocks.restype = ctypes.c_int
+        lib.kvq_release_blocks.argtypes = [vp, i32, vp, vp, i32, _BlockPool, vp]
+        lib.kvq_release_blocks.restype = ctypes.c_int
+        lib.kvq_prefix_decode_workspace_size.argtypes = [fmtp, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
+        lib.kvq_prefix_decode_workspace_size.restype = ctypes.c_int
+        lib.kvq_prefix_decode.argtypes = [vp, i32, i32, fmtp, _Caches, _Scales, vp, i32, vp, i32, vp, vp, i32, i32,
+                                          vp, vp, vp, vp, ctypes.c_size_t, vp]
+        lib.kvq_prefix_decode.restype = ctypes.c_int
         lib.kvq_device_errors.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32, vp]
         lib.kvq_device_errors.restype = ctypes.c_int
         lib.kvq_status_string.argtypes = [i32]
@@ -438,6 +456,135 @@ def kvq_prefetch_blocks(host_pool: dict, src_blocks: torch.Tensor, dst_blocks: t
         raise KvqError(st, "kvq_prefetch_blocks")
 
 
+def allocate_pool(num_blocks: int, device="cuda") -> dict:
+    """A block pool with every block free, block 0 first in line: free_list
+    int32 [num_blocks], free_count int32 [1], ref_counts int32 [num_blocks]."""
+    return {"free_list": torch.arange(num_blocks - 1, -1, -1, dtype=torch.int32, device=device),
+            "free_count": torch.full((1,), num_blocks, dtype=torch.int32, device=device),
+            "ref_counts": torch.zeros(num_blocks, dtype=torch.int32, device=device)}
+
+
+def _pool(pool: dict) -> _BlockPool:
+    fl, fc, rc = pool["free_list"], pool["free_count"], pool["ref_counts"]
+    n = int(fl.numel())
+    if int(rc.numel()) != n or int(fc.numel()) != 1:
+        raise ValueError("a pool is free_list [n], free_count [1] and ref_counts [n]")
+    return _BlockPool(_ptr(fl, torch.int32, "free_list"), _ptr(fc, torch.int32, "free_count"),
+                      _ptr(rc, torch.int32, "ref_counts"), n)
+
+
+def kvq_assign_blocks(new_lens: torch.Tensor, context_lens: torch.Tensor, block_tables: torch.Tensor, pool: dict,
+                      max_tokens: int, prefix_rows: Optional[torch.Tensor] = None,
+                      prefix_blocks: Optional[torch.Tensor] = None, token_offsets: Optional[torch.Tensor] = None,
+                      slot_mapping: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                      stream=None) -> tuple:
+    """Room for new_lens[r] more tokens of every row (int32 [R]): context_lens
+    [R], block_tables [R, max_blocks] and the pool are updated in place;
+    returns (token_offsets int32 [R + 1], slot_mapping int64 [max_tokens],
+    positions int32 [max_tokens]), -1 past the last token.  Row r with
+    prefix_rows[r] >= 0 starts with that row's first prefix_blocks[r] blocks."""
+    lib = load_library()
+    rows, dev = int(new_lens.shape[0]), block_tables.device
+    if context_lens.shape != (rows,) or block_tables.dim() != 2 or block_tables.shape[0] != rows:
+        raise ValueError("new_lens and context_lens must be [R] and block_tables [R, max_blocks]")
+    for t, what in ((prefix_rows, "prefix_rows"), (prefix_blocks, "prefix_blocks")):
+        if t is not None and t.shape != (rows,):
+            raise ValueError(f"{what} must be [R]")
+    if token_offsets is None:
+        token_offsets = torch.empty(rows + 1, dtype=torch.int32, device=dev)
+    if slot_mapping is None:
+        slot_mapping = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+    if token_offsets.shape != (rows + 1,) or slot_mapping.shape != (max_tokens,) or positions.shape != (max_tokens,):
+        raise ValueError("token_offsets must be [R + 1], slot_mapping and positions [max_tokens]")
+    st = lib.kvq_assign_blocks(_ptr(new_lens, torch.int32, "new_lens"), rows,
+                               _ptr(context_lens, torch.int32, "context_lens"),
+                               _ptr(block_tables, torch.int32, "block_tables"), int(block_tables.shape[1]), _pool(pool),
+                               None if prefix_rows is None else _ptr(prefix_rows, torch.int32, "prefix_rows"),
+                               None if prefix_blocks is None else _ptr(prefix_blocks, torch.int32, "prefix_blocks"),
+                               int(max_tokens), _ptr(token_offsets, torch.int32, "token_offsets"),
+                               _ptr(slot_mapping, torch.int64, "slot_mapping"),
+                               _ptr(positions, torch.int32, "positions"), _stream(stream))
+    if st != KVQ_OK:
+        raise KvqError(st, "kvq_assign_blocks")
+    return token_offsets, slot_mapping, positions
+
+
+def kvq_release_blocks(keep_lens: torch.Tensor, context_lens: torch.Tensor, block_tables: torch.Tensor, pool: dict,
+                       stream=None) -> None:
+    """Every row keeps its first keep_lens[r] tokens (int32 [R]) and gives the
+    blocks past them back to the pool; context_lens, block_tables and the pool
+    are updated in place."""
+    lib = load_library()
+    rows = int(keep_lens.shape[0])
+    if context_lens.shape != (rows,) or block_tables.dim() != 2 or block_tables.shape[0] != rows:
+        raise ValueError("keep_lens and context_lens must be [R] and block_tables [R, max_blocks]")
+    st = lib.kvq_release_blocks(_ptr(keep_lens, torch.int32, "keep_lens"), rows,
+                                _ptr(context_lens, torch.int32, "context_lens"),
+                                _ptr(block_tables, torch.int32, "block_tables"), int(block_tables.shape[1]),
+                                _pool(pool), _stream(stream))
+    if st != KVQ_OK:
+        raise KvqError(st, "kvq_release_blocks")
+
+
+def kvq_prefix_decode_workspace_size(fmt: CacheFormat, batch: int, num_q_heads: int, max_context_len: int,
+                                     num_groups: int) -> int:
+    lib = load_library()
+    out = ctypes.c_size_t(0)
+    cf = fmt.as_c()
+    st = lib.kvq_prefix_decode_workspace_size(ctypes.byref(cf), int(batch), int(num_q_heads), int(max_context_len),
+                                              int(num_groups), ctypes.byref(out))
+    if st != KVQ_OK:
+        raise KvqError(st, "kvq_prefix_decode_workspace_size")
+    return int(out.value)
+
+
+def kvq_prefix_decode(q: torch.Tensor, fmt: CacheFormat, cache: dict, block_tables: torch.Tensor,
+                      context_lens: torch.Tensor, max_context_len: int, group_starts: torch.Tensor,
+                      prefix_lens: torch.Tensor, max_prefix_len: int, residual: Optional[dict] = None,
+                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """One decode step over prefixes that groups of sequences share: group g is
+    the sequences [group_starts[g], group_starts[g + 1]), whose tables agree on
+    the first prefix_lens[g] // 16 blocks.  q BF16 [B, H_q, d] -> out BF16
+    [B, H_q, d]; `residual` is the tail of a per-channel K cache."""
+    lib = load_library()
+    bsz, hq, d = (int(x) for x in q.shape)
+    if d != fmt.head_dim:
+        raise ValueError("q head_dim does not match the cache format")
+    if block_tables.dim() != 2 or block_tables.shape[0] != bsz or context_lens.shape != (bsz,):
+        raise ValueError("block_tables must be [B, max_blocks] and context_lens [B]")
+    groups = int(prefix_lens.shape[0])
+    if prefix_lens.dim() != 1 or group_starts.shape != (groups + 1,):
+        raise ValueError("prefix_lens must be [num_groups] and group_starts [num_groups + 1]")
+    rk = rv = None
+    if residual is not None:
+        want = (bsz, fmt.block_size, fmt.num_kv_heads, d)
+        if tuple(residual["k"].shape) != want or tuple(residual["v"].shape) != want:
+            raise ValueError(f"residual k and v must be {list(want)}")
+        rk, rv = _ptr(residual["k"], torch.bfloat16, "residual k"), _ptr(residual["v"], torch.bfloat16, "residual v")
+    if out is None:
+        out = torch.empty((bsz, hq, d), dtype=torch.bfloat16, device=q.device)
+    elif tuple(out.shape) != (bsz, hq, d):
+        raise ValueError("out must have the shape of q")
+    if workspace is None:
+        nbytes = kvq_prefix_decode_workspace_size(fmt, bsz, hq, max_context_len, groups)
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+    cf = fmt.as_c()
+    caches, scales = _caches(cache)
+    st = lib.kvq_prefix_decode(_ptr(q, torch.bfloat16, "q"), bsz, hq, ctypes.byref(cf), caches, scales,
+                               _ptr(block_tables, torch.int32, "block_tables"), int(block_tables.shape[1]),
+                               _ptr(context_lens, torch.int32, "context_lens"), int(max_context_len),
+                               _ptr(group_starts, torch.int32, "group_starts"),
+                               _ptr(prefix_lens, torch.int32, "prefix_lens"), groups, int(max_prefix_len), rk, rv,
+                               _ptr(out, torch.bfloat16, "out"), _ptr(workspace, torch.uint8, "workspace"),
+                               int(workspace.numel()), _stream(stream))
+    if st != KVQ_OK:
+        raise KvqError(st, "kvq_prefix_decode")
+    return out
+
+
 def kvq_device_errors(clear: bool = True, stream=None) -> int:
     """Synchronize the stream and return the sticky device error bits."""
     lib = load_library()
@@ -449,5 +596,6 @@ def kvq_device_errors(clear: bool = True, stream=None) -> int:
 
 
 __all__ = [n for n in dir() if n.startswith("kvq_")] + [
-    "CacheFormat", "cache_format", "allocate_cache", "allocate_host_pool", "allocate_residual", "load_library", "KvqError", "LIB_PATH",
+    "CacheFormat", "cache_format", "allocate_cache", "allocate_host_pool", "allocate_residual",
+    "allocate_pool", "load_library", "KvqError", "LIB_PATH",
     "EXPORTED_SYMBOLS"]

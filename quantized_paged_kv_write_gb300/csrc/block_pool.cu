@@ -1,0 +1,400 @@
+// Block tables and slot mappings made on the GPU, and blocks given back.
+//
+// What it computes: the paged cache's bookkeeping ("Quantized KV caches in
+// production", PagedAttention: fixed-size blocks found through a per-sequence
+// table) from the requests' lengths.  The order is that of a loop over the
+// rows (assign: row 0 first; release: the last row first, its last block
+// first), so results do not depend on scheduling and a release that undoes an
+// assign leaves the free list as it was.
+//
+// What bounds it: latency.  A decode step of 256 rows moves 7 KB.  So each
+// call is one launch of one thread-block cluster: every CTA scans all rows
+// into its own shared memory (two running sums), the CTAs share the writing,
+// and a cluster barrier orders the in-place updates after everybody's reads,
+// where a second launch or a counter in memory would cost more than the work.
+#include <limits.h>
+
+#include "common.cuh"
+#include "kvq_internal.h"
+
+namespace kvq {
+namespace {
+
+constexpr int kPoolThreads = 1024;
+constexpr int kPoolWarps = kPoolThreads / 32;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();  // the aligned form wants the warp together
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int ld_cluster_s32(const int *smem, uint32_t rank) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(smem)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kBlockSize - 1) / kBlockSize; }
+
+// Exclusive sums over the CTA's threads of x (64-bit) and y; the totals go to
+// tx and ty.  wsum holds two values per warp; the caller may call again at
+// once.
+__device__ __forceinline__ void scan2(long long x, int y, long long *wx, int *wy, long long &ex, int &ey,
+                                      long long &tx, int &ty) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long ix = x;
+  int iy = y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, ix, o);
+    const int b = __shfl_up_sync(0xffffffffu, iy, o);
+    if (lane >= o) {
+      ix += a;
+      iy += b;
+    }
+  }
+  if (lane == 31) {
+    wx[warp] = ix;
+    wy[warp] = iy;
+  }
+  __syncthreads();
+  long long bx = 0, sx = 0;
+  int by = 0, sy = 0;
+  for (int w = 0; w < kPoolWarps; ++w) {
+    if (w == warp) {
+      bx = sx;
+      by = sy;
+    }
+    sx += wx[w];
+    sy += wy[w];
+  }
+  __syncthreads();
+  ex = bx + ix - x;
+  ey = by + iy - y;
+  tx = sx;
+  ty = sy;
+}
+
+// Last row r with off[r] <= i (off non-decreasing, off[0] = 0, i < off[rows]).
+__device__ __forceinline__ int row_of(const int *off, int rows, int i) {
+  int lo = 0, hi = rows;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------------------
+// assign
+// ---------------------------------------------------------------------------
+// Shared: tok[rows + 1], blk[rows + 1], ctx[rows] (contexts after sharing).
+__global__ void __launch_bounds__(kPoolThreads) assign_blocks_kernel(const AssignArgs a) {
+  extern __shared__ int sm[];
+  __shared__ long long wx[kPoolWarps];
+  __shared__ int wy[kPoolWarps];
+  const int B = a.rows, M = a.max_blocks;
+  int *tok = sm, *blk = sm + B + 1, *ctx = sm + 2 * (B + 1);
+  const uint32_t rank = cluster_rank(), nct = cluster_size();
+  const int f = __ldg(a.free_count);
+
+  // ---- check the rows and sum tokens and blocks
+  unsigned int bad = 0;
+  long long ctok = 0;  // running totals of the rows so far
+  int cblk = 0;
+  for (int base = 0; base < B; base += kPoolThreads) {
+    const int b = base + threadIdx.x;
+    int n = 0, c = 0, need = 0;
+    if (b < B) {
+      n = __ldg(a.new_lens + b);
+      c = __ldcg(a.ctx + b);
+      if (n < 0 || c < 0) bad |= KVQ_DEVERR_CONTEXT_RANGE;
+      if (a.prefix_rows != nullptr) {
+        const int s = __ldg(a.prefix_rows + b);
+        if (s >= 0) {
+          const int k = __ldg(a.prefix_blocks + b);
+          // the source row must hold the shared blocks already, all full
+          if (s >= B || s == b || c != 0 || k < 0 || k > M ||
+              static_cast<long long>(k) * kBlockSize > __ldcg(a.ctx + (s < B ? s : 0)))
+            bad |= KVQ_DEVERR_CONTEXT_RANGE;
+          else
+            c = k * kBlockSize;
+        }
+      }
+      if (!bad && static_cast<long long>(c) + n > static_cast<long long>(M) * kBlockSize) bad |= KVQ_DEVERR_CONTEXT_RANGE;
+      if (!bad && n > 0 && c % kBlockSize != 0) {
+        // the row continues a block of its own: never one that others read
+        const int id = __ldcg(a.tables + static_cast<int64_t>(b) * M + c / kBlockSize);
+        if (id < 0 || id >= a.num_blocks) bad |= KVQ_DEVERR_BLOCK_RANGE;
+        else if (__ldcg(a.ref_counts + id) != 1) bad |= KVQ_DEVERR_POOL_STATE;
+      }
+      if (bad) n = 0;
+      need = bad ? 0 : blocks_of(c + n) - blocks_of(c);
+    }
+    long long et, tt;
+    int eb, tb;
+    scan2(n, need, wx, wy, et, eb, tt, tb);
+    if (b < B) {
+      const long long t = ctok + et;
+      tok[b] = t > INT_MAX ? INT_MAX : static_cast<int>(t);
+      blk[b] = cblk + eb;
+      ctx[b] = c;
+    }
+    ctok += tt;
+    cblk += tb;
+  }
+  if (f < 0 || f > a.num_blocks) bad |= KVQ_DEVERR_POOL_STATE;
+  else if (cblk > f || ctok > a.max_tokens) bad |= KVQ_DEVERR_CAPACITY;
+  if (bad && rank == 0) set_error(a.err, bad);
+  const bool ok = !__syncthreads_or(bad != 0);
+  const int ntok = ok ? static_cast<int>(ctok) : 0, nblk = ok ? cblk : 0;
+  if (threadIdx.x == 0) {
+    tok[B] = ntok;
+    blk[B] = nblk;
+  }
+  __syncthreads();
+  cluster_arrive();  // this CTA has read what the call updates in place
+
+  const int tid = rank * kPoolThreads + threadIdx.x, nth = nct * kPoolThreads;
+  // ---- offsets, slots and positions
+  for (int b = tid; b <= B; b += nth) a.token_offsets[b] = ok ? tok[b] : 0;
+  for (int64_t t = tid; t < a.max_tokens; t += nth) {
+    int64_t slot = -1;
+    int pos = -1;
+    if (t < ntok) {
+      const int b = row_of(tok, B, static_cast<int>(t));
+      const int c = ctx[b], have = blocks_of(c);
+      pos = c + static_cast<int>(t) - tok[b];
+      const int j = pos / kBlockSize;
+      const int id = j < have ? __ldcg(a.tables + static_cast<int64_t>(b) * M + j)
+                              : __ldg(a.free_list + (f - 1 - (blk[b] + j - have)));
+      if (id >= 0 && id < a.num_blocks) slot = static_cast<int64_t>(id) * kBlockSize + pos % kBlockSize;
+    }
+    a.slots[t] = slot;
+    if (a.positions != nullptr) a.positions[t] = pos;
+  }
+  if (ok) {
+    // ---- shared blocks, then new ones
+    if (a.prefix_rows != nullptr) {
+      for (int b = rank; b < B; b += nct) {
+        const int s = __ldg(a.prefix_rows + b);
+        if (s < 0) continue;
+        const int k = ctx[b] / kBlockSize;
+        for (int i = threadIdx.x; i < k; i += kPoolThreads) {
+          const int id = __ldcg(a.tables + static_cast<int64_t>(s) * M + i);
+          a.tables[static_cast<int64_t>(b) * M + i] = id;
+          if (id >= 0 && id < a.num_blocks) atomicAdd(a.ref_counts + id, 1);
+          else set_error(a.err, KVQ_DEVERR_BLOCK_RANGE);
+        }
+      }
+    }
+    for (int i = tid; i < nblk; i += nth) {
+      const int b = row_of(blk, B, i);
+      const int id = __ldg(a.free_list + (f - 1 - i));
+      const bool in = id >= 0 && id < a.num_blocks;
+      if (!in) set_error(a.err, KVQ_DEVERR_POOL_STATE);
+      a.tables[static_cast<int64_t>(b) * M + blocks_of(ctx[b]) + i - blk[b]] = in ? id : -1;
+      if (in) a.ref_counts[id] = 1;
+    }
+  }
+  cluster_wait();
+  if (ok) {
+    for (int b = tid; b < B; b += nth) a.ctx[b] = ctx[b] + tok[b + 1] - tok[b];
+    if (tid == 0) *a.free_count = f - nblk;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// release
+// ---------------------------------------------------------------------------
+// Items are the released table entries in (row, block) order.  A block that
+// several rows give back in one call is pushed by the first of its items (the
+// last one of the descending loop): after all counts are taken down, every
+// item of a block whose count is 0 offers INT_MIN + item to an atomic minimum
+// on the count itself, and the item that finds its own code pushes.
+__global__ void __launch_bounds__(kPoolThreads) release_blocks_kernel(const ReleaseArgs a) {
+  extern __shared__ int sm[];
+  __shared__ long long wx[kPoolWarps];
+  __shared__ int wy[kPoolWarps];
+  __shared__ int pushes;
+  const int B = a.rows, M = a.max_blocks;
+  int *off = sm, *first = sm + B + 1;  // first released block of the row
+  const uint32_t rank = cluster_rank(), nct = cluster_size();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int f = __ldg(a.free_count);
+  const bool pool_ok = f >= 0 && f <= a.num_blocks;
+  if (!pool_ok && rank == 0 && threadIdx.x == 0) set_error(a.err, KVQ_DEVERR_POOL_STATE);
+
+  int n = 0;
+  for (int base = 0; base < B; base += kPoolThreads) {
+    const int b = base + threadIdx.x;
+    int cnt = 0, i0 = 0;
+    if (b < B) {
+      const int c = __ldcg(a.ctx + b), keep = __ldg(a.keep + b);
+      if (c < 0 || static_cast<long long>(c) > static_cast<long long>(M) * kBlockSize || keep < 0) {
+        if (rank == 0) set_error(a.err, KVQ_DEVERR_CONTEXT_RANGE);
+        i0 = -1;  // the row stays as it is
+      } else {
+        i0 = blocks_of(keep < c ? keep : c);
+        cnt = pool_ok ? blocks_of(c) - i0 : 0;
+      }
+    }
+    long long e0, t0;
+    int eb, tb;
+    scan2(0, cnt, wx, wy, e0, eb, t0, tb);
+    if (b < B) {
+      off[b] = n + eb;
+      first[b] = i0;
+    }
+    n += tb;
+  }
+  if (threadIdx.x == 0) {
+    off[B] = n;
+    pushes = 0;
+  }
+  __syncthreads();
+
+  // each warp owns a contiguous run of items
+  const int64_t w = static_cast<int64_t>(rank) * kPoolWarps + warp, nw = static_cast<int64_t>(nct) * kPoolWarps;
+  const int lo = static_cast<int>(w * n / nw), hi = static_cast<int>((w + 1) * n / nw);
+  auto entry = [&](int i) -> int32_t * {
+    const int b = row_of(off, B, i);
+    return a.tables + static_cast<int64_t>(b) * M + first[b] + (i - off[b]);
+  };
+  for (int i = lo + lane; i < hi; i += 32) {
+    int32_t *e = entry(i);
+    const int id = __ldcg(e);
+    if (id < 0 || id >= a.num_blocks) {
+      set_error(a.err, KVQ_DEVERR_BLOCK_RANGE);
+      *e = -1;
+      continue;
+    }
+    if (atomicSub(a.ref_counts + id, 1) <= 0) {  // given back more often than held
+      atomicAdd(a.ref_counts + id, 1);
+      set_error(a.err, KVQ_DEVERR_POOL_STATE);
+      *e = -1;
+    }
+  }
+  cluster_arrive();
+  cluster_wait();
+  for (int i = lo + lane; i < hi; i += 32) {
+    const int id = __ldcg(entry(i));
+    if (id >= 0 && __ldcg(a.ref_counts + id) <= 0) atomicMin(a.ref_counts + id, INT_MIN + i);
+  }
+  cluster_arrive();
+  cluster_wait();
+  int mine = 0;  // pushes of this warp
+  for (int i = lo + lane; i < hi; i += 32) {
+    const int id = __ldcg(entry(i));
+    mine += id >= 0 && __ldcg(a.ref_counts + id) == INT_MIN + i;
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) wy[warp] = mine;
+  __syncthreads();
+  int before = 0;  // pushes of the CTA's earlier warps
+  for (int k = 0; k < warp; ++k) before += wy[k];
+  if (threadIdx.x == kPoolThreads - 1) pushes = before + mine;
+  cluster_arrive();
+  cluster_wait();
+  int total = 0;
+  for (uint32_t r = 0; r < nct; ++r) {
+    const int p = ld_cluster_s32(&pushes, r);
+    if (r < rank) before += p;
+    total += p;
+  }
+  // the descending loop pushes the last item first
+  int done = before;
+  for (int base = lo; base < hi; base += 32) {
+    const int i = base + lane;
+    bool push = false;
+    int id = -1;
+    if (i < hi) {
+      int32_t *e = entry(i);
+      id = __ldcg(e);
+      push = id >= 0 && __ldcg(a.ref_counts + id) == INT_MIN + i;
+      *e = -1;
+    }
+    const unsigned int votes = __ballot_sync(0xffffffffu, push);
+    if (push) {
+      const int64_t at = static_cast<int64_t>(f) + total - 1 - (done + __popc(votes & ((1u << lane) - 1)));
+      if (at < a.num_blocks) a.free_list[at] = id;
+      else set_error(a.err, KVQ_DEVERR_POOL_STATE);
+      a.ref_counts[id] = 0;
+    }
+    done += __popc(votes);
+  }
+  const int tid = rank * kPoolThreads + threadIdx.x, nth = nct * kPoolThreads;
+  for (int b = tid; b < B; b += nth) {
+    if (!pool_ok || first[b] < 0) continue;
+    const int c = a.ctx[b], keep = __ldg(a.keep + b);
+    if (keep < c) a.ctx[b] = keep;
+  }
+  if (tid == 0 && total > 0) {
+    const int64_t v = static_cast<int64_t>(f) + total;
+    *a.free_count = v < a.num_blocks ? static_cast<int>(v) : static_cast<int>(a.num_blocks);
+  }
+  cluster_arrive();  // no CTA exits while another may still read its pushes
+  cluster_wait();
+}
+
+template <typename Args>
+cudaError_t launch_cluster(void (*kern)(const Args), const Args &a, int ctas, size_t smem, cudaStream_t stream) {
+  // above the default 48 KB only with many rows; the attribute is per device
+  // and idempotent
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kPoolThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+// Portable cluster sizes, one CTA per 4096 items of work.
+int cluster_for(int64_t items) {
+  int c = 1;
+  while (c < 8 && static_cast<int64_t>(c) * 4096 < items) c *= 2;
+  return c;
+}
+
+}  // namespace
+
+cudaError_t launch_assign_blocks(const AssignArgs &a, cudaStream_t stream) {
+  int64_t items = a.max_tokens;
+  if (a.prefix_rows != nullptr) items += static_cast<int64_t>(a.rows) * a.max_blocks;
+  const size_t smem = (3 * static_cast<size_t>(a.rows) + 2) * sizeof(int);
+  return launch_cluster(assign_blocks_kernel, a, cluster_for(items), smem, stream);
+}
+
+cudaError_t launch_release_blocks(const ReleaseArgs &a, cudaStream_t stream) {
+  const size_t smem = (2 * static_cast<size_t>(a.rows) + 1) * sizeof(int);
+  return launch_cluster(release_blocks_kernel, a, cluster_for(static_cast<int64_t>(a.rows) * a.max_blocks), smem,
+                        stream);
+}
+
+}  // namespace kvq

@@ -66,6 +66,7 @@ cudaError_t launch_one(const DecodeArgs &a, const DecodePlan &plan, const Decode
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
+  if (a.split_only) return cudaSuccess;
   const int warps = a.B * a.Hq;
   decode_reduce_kernel<D><<<(warps + 7) / 8, 256, 0, stream>>>(a, a.ws_cum);
   return cudaGetLastError();

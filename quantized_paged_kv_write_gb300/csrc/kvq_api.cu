@@ -581,6 +581,226 @@ int kvq_prefetch_blocks(const kvq_format *fmt, kvq_caches host_caches, kvq_scale
   return launch_prefetch(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static int check_pool(int32_t num_rows, const int32_t *lens, const int32_t *context_lens, const int32_t *block_tables,
+                      int32_t max_blocks, const kvq_block_pool &pool) {
+  if (num_rows < 0 || max_blocks < 1 || pool.num_blocks < 0) return KVQ_ERR_INVALID_ARG;
+  if (num_rows > 8192 || static_cast<int64_t>(num_rows) * max_blocks >= (int64_t(1) << 31) ||
+      pool.num_blocks >= (int64_t(1) << 31))
+    return KVQ_ERR_UNSUPPORTED;
+  if (num_rows > 0 && (!lens || !context_lens || !block_tables)) return KVQ_ERR_INVALID_ARG;
+  if (!pool.free_count || (pool.num_blocks > 0 && (!pool.free_list || !pool.ref_counts))) return KVQ_ERR_INVALID_ARG;
+  if (!aligned4(lens) || !aligned4(context_lens) || !aligned4(block_tables) || !aligned4(pool.free_list) ||
+      !aligned4(pool.free_count) || !aligned4(pool.ref_counts))
+    return KVQ_ERR_INVALID_ARG;
+  return KVQ_OK;
+}
+
+int kvq_assign_blocks(const int32_t *new_lens, int32_t num_rows, int32_t *context_lens, int32_t *block_tables,
+                      int32_t max_blocks_per_seq, kvq_block_pool pool, const int32_t *prefix_rows,
+                      const int32_t *prefix_blocks, int32_t max_tokens, int32_t *token_offsets,
+                      int64_t *slot_mapping, int32_t *positions, kvq_stream_t stream) {
+  const int st = check_pool(num_rows, new_lens, context_lens, block_tables, max_blocks_per_seq, pool);
+  if (st != KVQ_OK) return st;
+  if (max_tokens < 0 || !token_offsets || (max_tokens > 0 && !slot_mapping)) return KVQ_ERR_INVALID_ARG;
+  if ((prefix_rows == nullptr) != (prefix_blocks == nullptr)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned4(prefix_rows) || !aligned4(prefix_blocks) || !aligned4(token_offsets) || !aligned4(positions) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return KVQ_ERR_INVALID_ARG;
+  AssignArgs a;
+  if (error_word(&a.err) != cudaSuccess) return KVQ_ERR_CUDA;
+  a.new_lens = new_lens;
+  a.ctx = context_lens;
+  a.tables = block_tables;
+  a.free_list = pool.free_list;
+  a.free_count = pool.free_count;
+  a.ref_counts = pool.ref_counts;
+  a.prefix_rows = prefix_rows;
+  a.prefix_blocks = prefix_blocks;
+  a.token_offsets = token_offsets;
+  a.slots = slot_mapping;
+  a.positions = positions;
+  a.num_blocks = pool.num_blocks;
+  a.rows = num_rows;
+  a.max_blocks = max_blocks_per_seq;
+  a.max_tokens = max_tokens;
+  return launch_assign_blocks(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+int kvq_release_blocks(const int32_t *keep_lens, int32_t num_rows, int32_t *context_lens, int32_t *block_tables,
+                       int32_t max_blocks_per_seq, kvq_block_pool pool, kvq_stream_t stream) {
+  const int st = check_pool(num_rows, keep_lens, context_lens, block_tables, max_blocks_per_seq, pool);
+  if (st != KVQ_OK) return st;
+  if (num_rows == 0) return KVQ_OK;
+  ReleaseArgs a;
+  if (error_word(&a.err) != cudaSuccess) return KVQ_ERR_CUDA;
+  a.keep = keep_lens;
+  a.ctx = context_lens;
+  a.tables = block_tables;
+  a.free_list = pool.free_list;
+  a.free_count = pool.free_count;
+  a.ref_counts = pool.ref_counts;
+  a.num_blocks = pool.num_blocks;
+  a.rows = num_rows;
+  a.max_blocks = max_blocks_per_seq;
+  return launch_release_blocks(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+// Workspace of the shared-prefix decode: the suffix's split decode, then the
+// plan and the prefix partials, each 256-aligned.
+struct PrefixWs {
+  WsLayout sfx;
+  size_t groups, seqs, o, ml, total;
+};
+
+static PrefixWs prefix_ws(int B, int Hq, int H, int D, int groups, int sfx_ctas, int ctas) {
+  auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
+  PrefixWs w;
+  w.sfx = ws_layout(B, H, D, sfx_ctas);
+  const size_t rows = 2 * static_cast<size_t>(B) * Hq + static_cast<size_t>(kPrefixRows) * ctas;
+  w.groups = al(w.sfx.total);
+  w.seqs = w.groups + al((static_cast<size_t>(groups) + 1) * sizeof(PrefixGroup));
+  w.o = w.seqs + al(4 * static_cast<size_t>(B) * sizeof(int));
+  w.ml = w.o + al(rows * D * sizeof(float));
+  w.total = w.ml + al(rows * 2 * sizeof(float));
+  return w;
+}
+
+// CTAs of the prefix kernel: one per SM.
+static int prefix_plan(const kvq_format *fmt, int32_t batch, int32_t num_q_heads, int32_t num_groups, int *kf, int *vf,
+                       DecodePlan *plan, int *sms) {
+  int st = check_decode_shape(fmt, batch, num_q_heads, kf, vf);
+  if (st != KVQ_OK) return st;
+  if (num_groups < 0) return KVQ_ERR_INVALID_ARG;
+  if (num_groups > 8192) return KVQ_ERR_UNSUPPORTED;
+  if (batch == 0) return KVQ_OK;
+  if (plan_decode(fmt->head_dim, *kf, *vf, fmt->num_kv_heads, num_q_heads / fmt->num_kv_heads, batch,
+                  fmt->rotation != 0, plan) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  return sm_count(sms);
+}
+
+int kvq_prefix_decode_workspace_size(const kvq_format *fmt, int32_t batch, int32_t num_q_heads,
+                                     int32_t max_context_len, int32_t num_groups, size_t *bytes) {
+  int kf = 0, vf = 0, sms = 0;
+  DecodePlan plan;
+  const int st = prefix_plan(fmt, batch, num_q_heads, num_groups, &kf, &vf, &plan, &sms);
+  if (st != KVQ_OK) return st;
+  if (!bytes || max_context_len < 0) return KVQ_ERR_INVALID_ARG;
+  *bytes = prefix_ws(batch, num_q_heads, fmt->num_kv_heads, fmt->head_dim, num_groups, plan.max_ctas, sms).total;
+  return KVQ_OK;
+}
+
+int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, const kvq_format *fmt,
+                      kvq_caches caches, kvq_scales scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                      const int32_t *context_lens, int32_t max_context_len, const int32_t *group_starts,
+                      const int32_t *prefix_lens, int32_t num_groups, int32_t max_prefix_len, const void *res_k_bf16,
+                      const void *res_v_bf16, void *out_bf16, void *workspace, size_t workspace_bytes,
+                      kvq_stream_t stream) {
+  int kf = 0, vf = 0, sms = 0;
+  DecodePlan plan;
+  int st = prefix_plan(fmt, batch, num_q_heads, num_groups, &kf, &vf, &plan, &sms);
+  if (st != KVQ_OK) return st;
+  const bool tail = res_k_bf16 != nullptr || res_v_bf16 != nullptr;
+  if (tail) {
+    if (kf != K_INT8_CHAN && kf != K_INT2_CHAN) return KVQ_ERR_UNSUPPORTED;  // the tail belongs to per-channel K
+    if (!res_k_bf16 || !res_v_bf16 || !aligned16(res_k_bf16) || !aligned16(res_v_bf16)) return KVQ_ERR_INVALID_ARG;
+  }
+  if (max_blocks_per_seq < 1 || max_context_len < 0 || max_prefix_len < 0) return KVQ_ERR_INVALID_ARG;
+  if (batch == 0) return KVQ_OK;
+  if (!q_bf16 || !caches.k_cache || !caches.v_cache || !scales.k_scale || !scales.v_scale || !block_tables ||
+      !context_lens || !out_bf16 || !workspace || (num_groups > 0 && (!group_starts || !prefix_lens)))
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q_bf16) || !aligned16(caches.k_cache) || !aligned16(caches.v_cache) || !aligned16(scales.k_scale) ||
+      !aligned16(scales.v_scale) || !aligned16(out_bf16) || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      !aligned4(block_tables) || !aligned4(context_lens) || !aligned4(group_starts) || !aligned4(prefix_lens))
+    return KVQ_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(batch) * max_blocks_per_seq >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  if (fmt->num_blocks < 1 || fmt->num_blocks >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  const int H = fmt->num_kv_heads, D = fmt->head_dim, G = num_q_heads / H;
+  const PrefixWs wl = prefix_ws(batch, num_q_heads, H, D, num_groups, plan.max_ctas, sms);
+  if (workspace_bytes < wl.total) return KVQ_ERR_WORKSPACE;
+  unsigned int *err = nullptr;
+  if (error_word(&err) != cudaSuccess) return KVQ_ERR_CUDA;
+  DecodeMaps maps;
+  if ((st = encode_decode_maps(&maps, caches, scales, fmt->num_blocks, H, D, kf, vf)) != KVQ_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+
+  PrefixArgs p;
+  p.q = static_cast<const uint16_t *>(q_bf16);
+  p.kc = static_cast<const uint8_t *>(caches.k_cache);
+  p.vc = static_cast<const uint8_t *>(caches.v_cache);
+  p.ks = scales.k_scale;
+  p.vs = scales.v_scale;
+  p.tables = block_tables;
+  p.ctx = context_lens;
+  p.group_starts = group_starts;
+  p.prefix_lens = prefix_lens;
+  p.res_k = static_cast<const uint16_t *>(res_k_bf16);
+  p.res_v = static_cast<const uint16_t *>(res_v_bf16);
+  p.ws_groups = reinterpret_cast<PrefixGroup *>(ws + wl.groups);
+  p.ws_limit = reinterpret_cast<int *>(ws + wl.seqs);
+  p.ws_ctx = p.ws_limit + batch;
+  p.ws_off = p.ws_ctx + batch;
+  p.ws_group = p.ws_off + batch;
+  p.ws_o = reinterpret_cast<float *>(ws + wl.o);
+  p.ws_ml = reinterpret_cast<float *>(ws + wl.ml);
+  p.sfx_o = reinterpret_cast<float *>(ws + wl.sfx.o_off);
+  p.sfx_ml = reinterpret_cast<float *>(ws + wl.sfx.ml_off);
+  p.sfx_cum = reinterpret_cast<int *>(ws + wl.sfx.cum_off);
+  p.out = static_cast<uint16_t *>(out_bf16);
+  p.err = err;
+  p.num_blocks = fmt->num_blocks;
+  p.B = batch;
+  p.Hq = num_q_heads;
+  p.H = H;
+  p.G = G;
+  p.groups = num_groups;
+  p.max_blocks = max_blocks_per_seq;
+  p.max_ctx = max_context_len;
+  p.max_prefix = max_prefix_len;
+  p.nctas = sms;
+  p.sfx_nctas = plan.max_ctas;
+  p.sfx_blocks_per_cta = 4;
+  p.rot = fmt->rotation;
+  for (int w = 0; w < 4; ++w) p.rot_signs[w] = fmt->rotation_signs[w];
+
+  DecodeArgs a;
+  a.q = p.q;
+  a.ks = scales.k_scale;
+  a.vs = scales.v_scale;
+  a.tables = block_tables;
+  a.ctx = p.ws_ctx;
+  a.ws_o = reinterpret_cast<float *>(ws + wl.sfx.o_off);
+  a.ws_ml = reinterpret_cast<float *>(ws + wl.sfx.ml_off);
+  a.ws_cum = reinterpret_cast<int *>(ws + wl.sfx.cum_off);
+  a.out = nullptr;
+  a.err = err;
+  a.num_blocks = fmt->num_blocks;
+  a.B = batch;
+  a.Hq = num_q_heads;
+  a.H = H;
+  a.G = G;
+  a.max_blocks = max_blocks_per_seq;
+  a.max_ctx = max_context_len;
+  a.nctas = plan.max_ctas;
+  a.rot = fmt->rotation;
+  for (int w = 0; w < 4; ++w) a.rot_signs[w] = fmt->rotation_signs[w];
+  a.res_k = p.res_k;
+  a.res_v = p.res_v;
+  a.tab_off = p.ws_off;
+  a.blocks_per_cta = p.sfx_blocks_per_cta;
+  a.split_only = true;
+
+  if (launch_prefix_plan(p, s) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (num_groups > 0 && max_prefix_len >= kBlockSize && launch_prefix_attend(D, kf, vf, p, s) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  if (launch_decode(D, kf, vf, a, plan, maps, s) != cudaSuccess) return KVQ_ERR_CUDA;
+  return launch_prefix_merge(D, p, s) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
 int kvq_device_errors(uint32_t *bits_out, int32_t clear, kvq_stream_t stream) {
   if (!bits_out) return KVQ_ERR_INVALID_ARG;
   unsigned int *err = nullptr;

@@ -52,6 +52,13 @@ struct DecodeArgs {
   const uint16_t *res_k = nullptr, *res_v = nullptr;
   uint8_t *kc_w = nullptr, *vc_w = nullptr;  // code caches (written)
   float *ks_w = nullptr, *vs_w = nullptr;    // scales (written)
+  // Suffix of a shared-prefix decode (kvq_prefix_decode): ctx then holds the
+  // suffix lengths, sequence b's blocks start at entry tab_off[b] of its table
+  // row, fewer than blocks_per_cta blocks per CTA leave CTAs idle (the host
+  // does not know the suffix lengths), and the caller merges the partials.
+  const int32_t *tab_off = nullptr;
+  int blocks_per_cta = 0;
+  bool split_only = false;
 };
 
 // Launch plan of the split kernel for one shape on the current device.
@@ -101,6 +108,79 @@ struct KiviAppendArgs {
 cudaError_t launch_kivi_append(int head_dim, int kf, int vf, const KiviAppendArgs &a, cudaStream_t stream);
 
 // (dispatch lives in kvq_api.cu)
+
+// Block bookkeeping on the device (block_pool.cu).
+struct AssignArgs {
+  const int32_t *new_lens;                     // [rows]
+  int32_t *ctx;                                // [rows], updated
+  int32_t *tables;                             // [rows, max_blocks], updated
+  const int32_t *free_list;                    // [num_blocks] stack
+  int32_t *free_count, *ref_counts;            // [1], [num_blocks], updated
+  const int32_t *prefix_rows, *prefix_blocks;  // [rows] or null
+  int32_t *token_offsets;                      // [rows + 1]
+  int64_t *slots;                              // [max_tokens]
+  int32_t *positions;                          // [max_tokens] or null
+  unsigned int *err;
+  int64_t num_blocks;
+  int rows, max_blocks, max_tokens;
+};
+struct ReleaseArgs {
+  const int32_t *keep;                         // [rows]
+  int32_t *ctx, *tables, *free_list, *free_count, *ref_counts;
+  unsigned int *err;
+  int64_t num_blocks;
+  int rows, max_blocks;
+};
+cudaError_t launch_assign_blocks(const AssignArgs &a, cudaStream_t stream);
+cudaError_t launch_release_blocks(const ReleaseArgs &a, cudaStream_t stream);
+
+// Decode over a prefix that the sequences of a group share (prefix_decode.cu).
+//
+// Work: a unit is (group, row block, kv head); its rows are the (sequence,
+// query head) pairs of the group that read the kv head, cut evenly into row
+// blocks of at most kPrefixRows; it has ceil(shared / kPrefixTile) tiles.  The
+// units' tiles form one list, of which CTA c of P = min(nctas, T) takes
+// [c T / P, (c + 1) T / P), at least one tile.  Unit u's partial softmax state in CTA c lies at row
+// (row slots of the units before u) + kPrefixRows c of ws_o and ws_ml, which
+// never collides: from one (unit, CTA) pair to the next in order, either the
+// CTA grows by one or the unit does.
+constexpr int kPrefixRows = 256;
+constexpr int kPrefixTile = 128;
+struct PrefixGroup {
+  int start, nseq;       // sequences [start, start + nseq); nseq 0: no sharing
+  int shared;            // shared positions, a multiple of the block size
+  int lead;              // the sequence whose table holds all shared blocks
+  int row_blocks, rows;  // row blocks, and rows in each (the last may have fewer)
+  int tiles, slots;      // tiles of a unit, and its row slots
+  int64_t tile0;         // tiles of the groups before
+  int64_t row0;          // row slots of the groups before
+};
+struct PrefixArgs {
+  const uint16_t *q;             // BF16 [B, Hq, D]
+  const uint8_t *kc, *vc;        // codes
+  const float *ks, *vs;          // scales
+  const int32_t *tables, *ctx;   // [B, max_blocks], [B]
+  const int32_t *group_starts, *prefix_lens;  // [groups + 1], [groups]
+  const uint16_t *res_k, *res_v; // full-precision tail or null
+  PrefixGroup *ws_groups;        // [groups + 1]; entry `groups` holds tile0 = T and tiles = P
+  int *ws_limit;                 // [B] shared positions that the sequence attends to
+  int *ws_ctx, *ws_off;          // [B] suffix length, first suffix block
+  int *ws_group;                 // [B] group or -1
+  float *ws_o, *ws_ml;           // prefix partials: [rows, D], [rows, 2]
+  const float *sfx_o, *sfx_ml;   // suffix partials (DecodeArgs::ws_o, ws_ml)
+  const int *sfx_cum;            // suffix block counts, prefix sums
+  uint16_t *out;                 // BF16 [B, Hq, D]
+  unsigned int *err;
+  int64_t num_blocks;
+  int B, Hq, H, G, groups, max_blocks, max_ctx, max_prefix;
+  int nctas;                     // CTAs of the prefix kernel
+  int sfx_nctas, sfx_blocks_per_cta;
+  int rot;
+  uint32_t rot_signs[4];
+};
+cudaError_t launch_prefix_plan(const PrefixArgs &a, cudaStream_t stream);
+cudaError_t launch_prefix_attend(int head_dim, int kf, int vf, const PrefixArgs &a, cudaStream_t stream);
+cudaError_t launch_prefix_merge(int head_dim, const PrefixArgs &a, cudaStream_t stream);
 
 // Per-format entry points defined in the decode_k*.cu translation units.
 template <int KF>

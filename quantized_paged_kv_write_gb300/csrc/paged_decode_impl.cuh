@@ -364,8 +364,10 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
   __syncthreads();
 
   const int total = cum[B];
-  const int P = a.nctas;
   const int c = blockIdx.x;
+  int P = a.nctas;
+  if (a.blocks_per_cta > 0) P = min(P, max(1, (total + a.blocks_per_cta - 1) / a.blocks_per_cta));
+  if (c >= P) return;
   const int g0 = static_cast<int>((static_cast<int64_t>(c) * total) / P);
   const int g1 = static_cast<int>((static_cast<int64_t>(c + 1) * total) / P);
   if (c == 0) {
@@ -397,7 +399,8 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
       int phys = -1;
       if (gl < g1) {
         const int bl = seq_of(cum, B, gl);
-        phys = __ldg(a.tables + static_cast<int64_t>(bl) * a.max_blocks + (gl - cum[bl]));
+        const int skip = a.tab_off != nullptr ? __ldg(a.tab_off + bl) : 0;
+        phys = __ldg(a.tables + static_cast<int64_t>(bl) * a.max_blocks + skip + (gl - cum[bl]));
       }
       const int n = min(32, g1 - base);
       for (int k = 0; k < n; ++k) {
