@@ -12,13 +12,12 @@
 //
 // Three steps around the suffix's split decode: the plan (what is shared, and
 // the list of work), the prefix attention, and the merge.
-#include "common.cuh"
-#include "kvq_internal.h"
+#include <atomic>
+
+#include "prefix_attend.cuh"
 
 namespace kvq {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
 
 // ---------------------------------------------------------------------------
 // plan
@@ -171,120 +170,6 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
 }
 
 // ---------------------------------------------------------------------------
-// prefix attention
-// ---------------------------------------------------------------------------
-struct Cell {  // formats as run-time values
-  int kf, vf, krow, vrow;
-};
-
-__device__ __forceinline__ float code_value(const uint8_t *row, int ch, int bits, bool fp8) {
-  if (fp8) return f16lo_to_f32(e4m3x2_to_f16x2(row[ch]));
-  if (bits == 8) return static_cast<float>(static_cast<int8_t>(row[ch]));
-  if (bits == 4) {
-    const int n = (row[ch >> 1] >> (4 * (ch & 1))) & 15;
-    return static_cast<float>((n ^ 8) - 8);
-  }
-  const int n = (row[ch >> 2] >> (2 * (ch & 3))) & 3;
-  return static_cast<float>((n ^ 2) - 2);
-}
-
-// One thread per row; a block of 16 keys at a time is dequantized to FP32 in
-// shared memory.
-template <int D>
-__global__ void __launch_bounds__(kPrefixRows) prefix_attend_kernel(const PrefixArgs a, const Cell f) {
-  extern __shared__ float sh[];
-  float *qs = sh;                       // [D][rows]
-  float *ks = qs + D * kPrefixRows;     // [16][D]
-  float *vs = ks + kBlockSize * D;      // [16][D]
-  const int r = threadIdx.x;
-  const int64_t T = a.ws_groups[a.groups].tile0;
-  const int c = blockIdx.x, P = a.ws_groups[a.groups].tiles;
-  if (c >= P) return;
-  const int64_t x1 = (c + 1) * T / P;
-  int64_t x = c * T / P;
-  while (x < x1) {
-    int lo = 0, hi = a.groups;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.ws_groups[mid].tile0 <= x) lo = mid; else hi = mid;
-    }
-    const PrefixGroup g = a.ws_groups[lo];
-    const int u = static_cast<int>((x - g.tile0) / g.tiles);
-    const int t0 = static_cast<int>((x - g.tile0) % g.tiles);
-    const int t1 = static_cast<int>(min(static_cast<int64_t>(g.tiles), t0 + (x1 - x)));
-    const int h = u % a.H, rb = u / a.H;
-    const int R = g.nseq * a.G;
-    const int row = rb * g.rows + r;
-    const bool live = r < g.rows && row < R;
-    const int b = g.start + (live ? row / a.G : 0), gq = live ? row % a.G : 0;
-    const int limit = live ? a.ws_limit[b] : 0;
-    __syncthreads();
-    const uint16_t *q = a.q + (static_cast<int64_t>(b) * a.Hq + h * a.G + gq) * D;
-    for (int i = 0; i < D; ++i) {
-      float v = bf16lo_to_f32(q[i]);
-      if (a.rot && ((a.rot_signs[i >> 5] >> (i & 31)) & 1)) v = -v;
-      qs[i * kPrefixRows + r] = v;
-    }
-    if (a.rot) {
-      for (int s = 1; s < D; s <<= 1)
-        for (int i = 0; i < D; ++i)
-          if (!(i & s)) {
-            const float y = qs[i * kPrefixRows + r], w = qs[(i + s) * kPrefixRows + r];
-            qs[i * kPrefixRows + r] = y + w;
-            qs[(i + s) * kPrefixRows + r] = y - w;
-          }
-      for (int i = 0; i < D; ++i) qs[i * kPrefixRows + r] *= 1.f / D;
-    }
-    const float zs = rsqrtf(static_cast<float>(D)) * kLog2e;
-    float o[D], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < D; ++i) o[i] = 0.f;
-    const int j1 = min(t1 * (kPrefixTile / kBlockSize), g.shared / kBlockSize);
-    for (int j = t0 * (kPrefixTile / kBlockSize); j < j1; ++j) {
-      const int64_t id = a.tables[static_cast<int64_t>(g.lead) * a.max_blocks + j];
-      if (id < 0 || id >= a.num_blocks) {
-        if (r == 0) set_error(a.err, KVQ_DEVERR_BLOCK_RANGE);
-        continue;
-      }
-      __syncthreads();
-      for (int i = r; i < kBlockSize * D; i += kPrefixRows) {
-        const int t = i / D, ch = i % D;
-        const int64_t tok = (id * kBlockSize + t) * a.H + h;
-        const float kv = code_value(a.kc + tok * f.krow, ch, f.krow * 8 / D, f.kf == K_FP8_TOK);
-        const float vv = code_value(a.vc + tok * f.vrow, ch, f.vrow * 8 / D, f.vf == V_FP8_TOK);
-        const bool chan = f.kf == K_INT8_CHAN || f.kf == K_INT2_CHAN;
-        const bool grp = f.vf == V_INT4_G32 || f.vf == V_INT2_G32;
-        ks[i] = kv * (chan ? a.ks[(id * a.H + h) * D + ch] : a.ks[tok]);
-        vs[i] = vv * (grp ? a.vs[tok * (D / 32) + ch / 32] : a.vs[tok]);
-      }
-      __syncthreads();
-      const int n = min(kBlockSize, limit - j * kBlockSize);
-      for (int t = 0; t < n; ++t) {
-        float s = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < D; ++i) s += qs[i * kPrefixRows + r] * ks[t * D + i];
-        const float z = s * zs;
-        const float mn = fmaxf(m, z);
-        const float keep = exp2f(m - mn), p = exp2f(z - mn);
-        l = l * keep + p;
-#pragma unroll
-        for (int i = 0; i < D; ++i) o[i] = o[i] * keep + p * vs[t * D + i];
-        m = mn;
-      }
-    }
-    if (live) {
-      const int64_t at = g.row0 + static_cast<int64_t>(u) * g.slots + static_cast<int64_t>(c) * kPrefixRows + r;
-#pragma unroll
-      for (int i = 0; i < D; ++i) a.ws_o[at * D + i] = o[i];
-      a.ws_ml[at * 2] = m;
-      a.ws_ml[at * 2 + 1] = l;
-      if (g.slots > g.rows) a.ws_ml[(at + g.rows) * 2] = -INFINITY;
-    }
-    x += t1 - t0;
-  }
-}
-
-// ---------------------------------------------------------------------------
 // merge: one warp per (sequence, query head)
 // ---------------------------------------------------------------------------
 template <int D>
@@ -426,15 +311,26 @@ cudaError_t launch_prefix_plan(const PrefixArgs &a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_prefix_attend(int head_dim, int kf, int vf, const PrefixArgs &a, cudaStream_t stream) {
-  const auto row = [&](bool four, bool two) { return four ? head_dim / 2 : two ? head_dim / 4 : head_dim; };
-  const Cell f = {kf, vf, row(kf == K_INT4_TOK, kf == K_INT2_CHAN), row(vf == V_INT4_G32, vf == V_INT2_G32)};
-  const size_t smem = static_cast<size_t>(head_dim) * (kPrefixRows + 2 * kBlockSize) * sizeof(float);
-  auto kern = head_dim == 128 ? prefix_attend_kernel<128> : prefix_attend_kernel<64>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+template <int D>
+static cudaError_t attend(int kf, int vf, const PrefixArgs &a, cudaStream_t stream) {
+  auto kern = prefix::prefix_attend_kernel<D>;
+  constexpr size_t smem = prefix::Smem<D>::bytes + 1024;  // alignment slack
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  kern<<<a.nctas, kPrefixRows, smem, stream>>>(a, f);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  static std::atomic<unsigned long long> done{0};  // devices whose limit is raised
+  if (!((done.load(std::memory_order_acquire) >> dev) & 1ull)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) != cudaSuccess)
+      return e;
+    done.fetch_or(1ull << dev, std::memory_order_acq_rel);
+  }
+  kern<<<a.nctas, prefix::kThreads, smem, stream>>>(a, kf, vf);
   return cudaGetLastError();
+}
+
+cudaError_t launch_prefix_attend(int head_dim, int kf, int vf, const PrefixArgs &a, cudaStream_t stream) {
+  return head_dim == 128 ? attend<128>(kf, vf, a, stream) : attend<64>(kf, vf, a, stream);
 }
 
 cudaError_t launch_prefix_merge(int head_dim, const PrefixArgs &a, cudaStream_t stream) {
