@@ -795,7 +795,7 @@ int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
   a.split_only = true;
 
   if (launch_prefix_plan(p, s) != cudaSuccess) return KVQ_ERR_CUDA;
-  if (num_groups > 0 && max_prefix_len >= kBlockSize && launch_prefix_attend(D, kf, vf, p, s) != cudaSuccess)
+  if (num_groups > 0 && max_prefix_len >= kBlockSize && launch_prefix_attend(D, kf, vf, p, maps, s) != cudaSuccess)
     return KVQ_ERR_CUDA;
   if (launch_decode(D, kf, vf, a, plan, maps, s) != cudaSuccess) return KVQ_ERR_CUDA;
   return launch_prefix_merge(D, p, s) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;

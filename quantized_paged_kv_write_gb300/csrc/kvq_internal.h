@@ -179,7 +179,8 @@ struct PrefixArgs {
   uint32_t rot_signs[4];
 };
 cudaError_t launch_prefix_plan(const PrefixArgs &a, cudaStream_t stream);
-cudaError_t launch_prefix_attend(int head_dim, int kf, int vf, const PrefixArgs &a, cudaStream_t stream);
+cudaError_t launch_prefix_attend(int head_dim, int kf, int vf, const PrefixArgs &a, const DecodeMaps &maps,
+                                 cudaStream_t stream);
 cudaError_t launch_prefix_merge(int head_dim, const PrefixArgs &a, cudaStream_t stream);
 
 // Per-format entry points defined in the decode_k*.cu translation units.

@@ -312,25 +312,31 @@ cudaError_t launch_prefix_plan(const PrefixArgs &a, cudaStream_t stream) {
 }
 
 template <int D>
-static cudaError_t attend(int kf, int vf, const PrefixArgs &a, cudaStream_t stream) {
+static cudaError_t attend(int kf, int vf, const PrefixArgs &a, const DecodeMaps &m, cudaStream_t stream) {
   auto kern = prefix::prefix_attend_kernel<D>;
-  constexpr size_t smem = prefix::Smem<D>::bytes + 1024;  // alignment slack
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   static std::atomic<unsigned long long> done{0};  // devices whose limit is raised
   if (!((done.load(std::memory_order_acquire) >> dev) & 1ull)) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) != cudaSuccess)
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, prefix::kMaxSmem)) != cudaSuccess)
       return e;
     done.fetch_or(1ull << dev, std::memory_order_acq_rel);
   }
-  kern<<<a.nctas, prefix::kThreads, smem, stream>>>(a, kf, vf);
+  // a batch that cannot fill more than one row tile gives the other one's
+  // place to the ring of codes
+  const int krow = kf == K_INT4_TOK ? D / 2 : kf == K_INT2_CHAN ? D / 4 : D;
+  const int vrow = vf == V_INT4_G32 ? D / 2 : vf == V_INT2_G32 ? D / 4 : D;
+  const prefix::Layout y = prefix::layout_of<D>(kf == K_INT8_CHAN || kf == K_INT2_CHAN, vf == V_INT4_G32 || vf == V_INT2_G32,
+                                                a.B * a.G > kPrefixRows / 2, krow, vrow);
+  kern<<<a.nctas, prefix::kThreads, y.bytes, stream>>>(m.k, m.v, a, y, kf, vf, krow, vrow);
   return cudaGetLastError();
 }
 
-cudaError_t launch_prefix_attend(int head_dim, int kf, int vf, const PrefixArgs &a, cudaStream_t stream) {
-  return head_dim == 128 ? attend<128>(kf, vf, a, stream) : attend<64>(kf, vf, a, stream);
+cudaError_t launch_prefix_attend(int head_dim, int kf, int vf, const PrefixArgs &a, const DecodeMaps &m,
+                                 cudaStream_t stream) {
+  return head_dim == 128 ? attend<128>(kf, vf, a, m, stream) : attend<64>(kf, vf, a, m, stream);
 }
 
 cudaError_t launch_prefix_merge(int head_dim, const PrefixArgs &a, cudaStream_t stream) {
