@@ -166,7 +166,7 @@ struct PrefixArgs {
   int *ws_limit;                 // [B] shared positions that the sequence attends to
   int *ws_ctx, *ws_off;          // [B] suffix length, first suffix block
   int *ws_group;                 // [B] group or -1
-  float *ws_o, *ws_ml;           // prefix partials: [rows, D], [rows, 2]
+  float *ws_o, *ws_ml;           // prefix partials: by (unit, CTA, stream) [D / 4][rows][4], and [rows, 2]
   const float *sfx_o, *sfx_ml;   // suffix partials (DecodeArgs::ws_o, ws_ml)
   const int *sfx_cum;            // suffix block counts, prefix sums
   uint16_t *out;                 // BF16 [B, Hq, D]

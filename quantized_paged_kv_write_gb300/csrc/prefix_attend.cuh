@@ -79,8 +79,9 @@ struct Smem {
   static constexpr uint32_t info = vs + kMeta * kTile * 4;         // [kMeta] {F, block mask}
   static constexpr uint32_t bars = info + kMeta * 8;    // mbarriers
   static constexpr uint32_t tmem = bars + 56 * 8;       // tensor memory address, then the abort flag
-  static constexpr uint32_t scales = tmem + 16;         // [2] channel scales (high, low parts) and group scales
-  static_assert(scales % 16 == 0 && scales <= 5 * 1024, "small arrays");
+  static constexpr uint32_t factors = tmem + 16;        // [128] row factors
+  static constexpr uint32_t scales = factors + 512;     // [2] channel scales (high, low parts) and group scales
+  static_assert(scales % 16 == 0 && scales <= 5 * 1024 + 512, "small arrays");
 };
 
 // What depends on the formats and on whether any unit has two row tiles.
@@ -746,53 +747,51 @@ __device__ __noinline__ void rotate_row(const PrefixArgs &a, float (&y)[D / 32],
 }
 
 // The warp's 32 rows of Q' into their tile; `from` is the lane's row of q, -1
-// for none.  Returns this lane's row factor c.
+// for none.  Returns this lane's row factor c.  The BF16 rows are copied to the
+// places of the f16 rows (all copies in flight at once) and converted there.
 template <int D>
-__device__ __noinline__ float stage_queries(const PrefixArgs &a, int from, uint32_t tile, int row0, int lane, bool store) {
+__device__ __noinline__ float stage_queries(const PrefixArgs &a, int from, uint32_t tile, int row0, int lane) {
   constexpr int CPL = D / 32;  // channels per lane
-  constexpr int U = 4;
   const uint16_t *const q = a.q + lane * CPL;
   const int ch = lane * CPL;
-  const uint32_t at = tile + (ch >> 6) * Smem<D>::HALF + (ch & 7) * 2;
+  const uint32_t at = tile + (ch >> 6) * Smem<D>::HALF + (ch & 7) * 2 + row0 * 128;
+  const uint32_t chunk = (ch & 63) >> 3;
   float c = 0.f;
 #pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += U) {
-    uint32_t w[U][CPL / 2];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int row = __shfl_sync(0xffffffffu, from, r0 + u);
-      const uint32_t *p = reinterpret_cast<const uint32_t *>(q + static_cast<int64_t>(max(row, 0)) * D);
-#pragma unroll
-      for (int e = 0; e < CPL / 2; ++e) w[u][e] = row < 0 ? 0u : __ldg(p + e);
+  for (int r = 0; r < 32; ++r) {
+    const int row = __shfl_sync(0xffffffffu, from, r);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at + r * 128 + ((chunk ^ (r & 7)) << 4)),
+                 "l"(q + static_cast<int64_t>(max(row, 0)) * D), "n"(CPL * 2), "r"(row < 0 ? 0 : CPL * 2)
+                 : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+#pragma unroll 4
+  for (int r = 0; r < 32; ++r) {
+    const uint32_t to = at + r * 128 + ((chunk ^ (r & 7)) << 4);
+    float y[CPL];
+    if constexpr (CPL == 4) {
+      const uint2 w = lds64(to);
+      y[0] = bf16lo_to_f32(w.x); y[1] = bf16hi_to_f32(w.x); y[2] = bf16lo_to_f32(w.y); y[3] = bf16hi_to_f32(w.y);
+    } else {
+      const uint32_t w = lds32(to);
+      y[0] = bf16lo_to_f32(w); y[1] = bf16hi_to_f32(w);
     }
+    if (a.rot) rotate_row<D>(a, y, lane);
+    float m = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float y[CPL];
+    for (int e = 0; e < CPL; ++e) m = fmaxf(m, fabsf(y[e]));
+    m = __uint_as_float(warp_max_u32(__float_as_uint(m)));
+    // 2^er brings m into [2^14, 2^15).  Below 2^-86 the scores vanish anyway:
+    // er <= 100 keeps 2^er and c normal floats.
+    const int er = m > 0.f ? min(14 - ilog2f(m), 100) : 0;
+    const float f = pow2i(er);
+    if (lane == r) c = pow2i(-er);
+    uint32_t h[CPL / 2];
 #pragma unroll
-      for (int e = 0; e < CPL / 2; ++e) {
-        y[2 * e] = bf16lo_to_f32(w[u][e]);
-        y[2 * e + 1] = bf16hi_to_f32(w[u][e]);
-      }
-      if (a.rot) rotate_row<D>(a, y, lane);
-      float m = 0.f;
-#pragma unroll
-      for (int e = 0; e < CPL; ++e) m = fmaxf(m, fabsf(y[e]));
-      m = __uint_as_float(warp_max_u32(__float_as_uint(m)));
-      // 2^er brings m into [2^14, 2^15).  Below 2^-86 the scores vanish anyway:
-      // er <= 100 keeps 2^er and c normal floats.
-      const int er = m > 0.f ? min(14 - ilog2f(m), 100) : 0;
-      const float f = pow2i(er);
-      if (lane == r0 + u) c = pow2i(-er);
-      uint32_t h[CPL / 2];
-#pragma unroll
-      for (int e = 0; e < CPL / 2; ++e) h[e] = f32x2_to_f16x2(y[2 * e] * f, y[2 * e + 1] * f);
-      const int rr = row0 + r0 + u;
-      const uint32_t to = at + rr * 128 + ((((ch & 63) >> 3) ^ (rr & 7)) << 4);
-      if (store) {
-        if constexpr (CPL == 4) sts64(to, h[0], h[1]);
-        else sts32(to, h[0]);
-      }
-    }
+    for (int e = 0; e < CPL / 2; ++e) h[e] = f32x2_to_f16x2(y[2 * e] * f, y[2 * e + 1] * f);
+    if constexpr (CPL == 4) sts64(to, h[0], h[1]);
+    else sts32(to, h[0]);
   }
   return c * rsqrtf(static_cast<float>(D)) * kLog2e * (a.rot ? 1.f / D : 1.f);
 }
@@ -817,11 +816,22 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
     const bool live = r < s.g.rows && row < R;
     // ---- queries
     const int b = s.g.start + row / a.G;
-    const float c = stage_queries<D>(a, live ? b * a.Hq + s.h * a.G + row % a.G : -1, base + L::q + (s.two ? wg : 0) * L::TILE,
-                                     32 * warp, lane, s.two || wg == 0);
-    fence_proxy_async_shared();
+    float c = 0.f;
+    if (s.two || wg == 0) {
+      c = stage_queries<D>(a, live ? b * a.Hq + s.h * a.G + row % a.G : -1, base + L::q + (s.two ? wg : 0) * L::TILE,
+                           32 * warp, lane);
+      fence_proxy_async_shared();
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&wait.bars[B_Q]);
+    if (!s.two) {
+      // both warpgroups have the same rows: the factors go through shared memory
+      float *const f = reinterpret_cast<float *>(smem + y0.small + L::factors);
+      if (wg == 0) f[32 * warp + lane] = c;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      c = f[32 * warp + lane];
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
     const int limit = live ? __ldg(a.ws_limit + b) : s.g.shared;
     const int nearest = __reduce_min_sync(0xffffffffu, limit);
 
@@ -967,9 +977,10 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
       __syncwarp();
       if (lane == 0) mbar_arrive(&wait.bars[B_P + wg]);
     }
-    // ---- the unit's partial state
-    const int64_t at = s.g.row0 + static_cast<int64_t>(s.u) * s.g.slots + static_cast<int64_t>(blockIdx.x) * kPrefixRows +
-                       (s.two ? r : wg * s.g.rows + r);
+    // ---- the unit's partial state: ml by row, O as [D / 4][rows][4], so that the
+    // lanes' 16-byte stores are consecutive
+    const int64_t slot0 = s.g.row0 + static_cast<int64_t>(s.u) * s.g.slots + static_cast<int64_t>(blockIdx.x) * kPrefixRows +
+                          (s.two ? 0 : wg * s.g.rows);
     if (begun) {
       wait(B_O + wg, no & 1);
       __syncwarp();
@@ -983,10 +994,10 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
         tmem_ld16(O + 16 * cc, w);
         tmem_wait_ld(w);
         if (live) {
-          float4 *o = reinterpret_cast<float4 *>(a.ws_o + at * D + 16 * cc);
+          float4 *o = reinterpret_cast<float4 *>(a.ws_o + slot0 * D) + 4 * cc * s.g.rows + r;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            o[e] = make_float4(__uint_as_float(w[4 * e]) * back, __uint_as_float(w[4 * e + 1]) * back,
+            o[e * s.g.rows] = make_float4(__uint_as_float(w[4 * e]) * back, __uint_as_float(w[4 * e + 1]) * back,
                                __uint_as_float(w[4 * e + 2]) * back, __uint_as_float(w[4 * e + 3]) * back);
         }
       }
@@ -997,7 +1008,7 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
       wait(B_O, seg & 1);
       __syncwarp();
     }
-    if (live) *reinterpret_cast<float2 *>(a.ws_ml + at * 2) = make_float2(m == -INFINITY ? m : m * c, l);
+    if (live) *reinterpret_cast<float2 *>(a.ws_ml + (slot0 + r) * 2) = make_float2(m == -INFINITY ? m : m * c, l);
     x += tiles;
     n0 += tiles;
   }

@@ -170,137 +170,175 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
 }
 
 // ---------------------------------------------------------------------------
-// merge: one warp per (sequence, query head)
+// merge
 // ---------------------------------------------------------------------------
+// A CTA merges kMergeRows rows of one kv head (row = sequence * G + query head
+// of the group, as the units count them); a thread has 4 channels of a row, so
+// the rows' 16-byte pieces of a partial are consecutive in memory.  Bound by the
+// latency of the partials in L2 (up to ~40 of them for a row): eight are in
+// flight at a time.
+constexpr int kMergeRows = 8;
+
 template <int D>
-__global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixArgs a) {
-  constexpr int CPL = D / 32;  // channels per lane
-  const int id = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (id >= a.B * a.Hq) return;
-  const int b = id / a.Hq, hq = id % a.Hq, h = hq / a.G, gq = hq % a.G;
-  float acc[CPL], L = 0.f, mx = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < CPL; ++k) acc[k] = 0.f;
+__global__ void __launch_bounds__(kMergeRows *D / 4) prefix_merge_kernel(const PrefixArgs a) {
+  constexpr int CG = D / 4;  // channel groups
+  constexpr int U = 8;
+  __shared__ float sh[kMergeRows][D + 4];
+  const int rl = threadIdx.x % kMergeRows, cg = threadIdx.x / kMergeRows;
+  const int h = blockIdx.x % a.H, row = blockIdx.x / a.H * kMergeRows + rl;
+  const bool live = row < a.B * a.G;
+  const int b = live ? row / a.G : 0, gq = live ? row % a.G : 0;
 
-  // one more partial state with its output in o[0 .. CPL)
-  auto add = [&](float m, float l, const float (&o)[CPL]) {
-    if (m == -INFINITY) return;
-    const float mn = fmaxf(mx, m);
-    const float keep = exp2f(mx - mn), w = exp2f(m - mn);
-    L = L * keep + w * l;
-#pragma unroll
-    for (int k = 0; k < CPL; ++k) acc[k] = acc[k] * keep + w * o[k];
-    mx = mn;
-  };
-  auto load = [&](const float *p, float (&o)[CPL]) {
-#pragma unroll
-    for (int k = 0; k < CPL; ++k) o[k] = p[lane * CPL + k];
-  };
-
-  // ---- prefix
-  const int gi = a.ws_group[b];
+  // ---- where the row's partials are: prefix (CTA c of its unit, one or two
+  // streams), then suffix (the split decode's)
+  int n0 = 0, streams = 1, prows = 0, n1 = 0;
+  int64_t pslot = 0, srec = 0;
+  const int gi = live ? a.ws_group[b] : -1;
   if (gi >= 0) {
     const PrefixGroup g = a.ws_groups[gi];
-    const int row = (b - g.start) * a.G + gq;
-    const int rb = row / g.rows, r = row % g.rows, u = rb * a.H + h;
-    const int64_t T = a.ws_groups[a.groups].tile0;
-    const int64_t x0 = g.tile0 + static_cast<int64_t>(u) * g.tiles;
+    const int r = (b - g.start) * a.G + gq, rb = r / g.rows, u = rb * a.H + h;
+    const int T = static_cast<int>(a.ws_groups[a.groups].tile0), P = a.ws_groups[a.groups].tiles;
+    const int x0 = static_cast<int>(g.tile0) + u * g.tiles;
     // the CTA that holds tile x of the list
-    const int P = a.ws_groups[a.groups].tiles;
-    auto cta_of = [&](int64_t x) { return static_cast<int>(min(static_cast<int64_t>(P - 1), ((x + 1) * P - 1) / T)); };
+    auto cta_of = [&](int x) { return min(P - 1, static_cast<int>(((static_cast<int64_t>(x) + 1) * P - 1) / T)); };
     const int c0 = cta_of(x0), c1 = cta_of(x0 + g.tiles - 1);
-    for (int c = c0; c <= c1; ++c) {
-      for (int s = 0; s < (g.slots > g.rows ? 2 : 1); ++s) {
-        const int64_t at = g.row0 + static_cast<int64_t>(u) * g.slots + static_cast<int64_t>(c) * kPrefixRows + s * g.rows + r;
-        const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + at * 2);
-        if (ml.x == -INFINITY) continue;
-        float o[CPL];
-        load(a.ws_o + at * D, o);
-        add(ml.x, ml.y, o);
-      }
+    streams = g.slots > g.rows ? 2 : 1;
+    prows = g.rows;
+    n0 = (c1 - c0 + 1) * streams;
+    pslot = g.row0 + static_cast<int64_t>(u) * g.slots + static_cast<int64_t>(c0) * kPrefixRows;
+    srec = r % g.rows;  // (the row in its block, for now)
+  }
+  const int prow = static_cast<int>(srec);
+  const bool packed = 2 * a.G <= 8;  // suffix columns g (high) and g + G (low)
+  if (live) {
+    const int s0 = a.sfx_cum[b], s1 = a.sfx_cum[b + 1];
+    if (s1 > s0) {
+      const int total = a.sfx_cum[a.B];
+      const int P = min(a.sfx_nctas, max(1, (total + a.sfx_blocks_per_cta - 1) / a.sfx_blocks_per_cta));
+      auto cta_of = [&](int x) { return min(P - 1, static_cast<int>(((static_cast<int64_t>(x) + 1) * P - 1) / total)); };
+      const int c0 = cta_of(s0);
+      n1 = cta_of(s1 - 1) - c0 + 1;
+      srec = ((static_cast<int64_t>(b) + c0) * a.H + h) * 8 + gq;
     }
   }
-  // ---- suffix: the split decode's partials
-  const int s0 = a.sfx_cum[b], s1 = a.sfx_cum[b + 1];
-  if (s1 > s0) {
-    const int total = a.sfx_cum[a.B];
-    const int P = min(a.sfx_nctas, max(1, (total + a.sfx_blocks_per_cta - 1) / a.sfx_blocks_per_cta));
-    auto cta_of = [&](int x) {
-      const int64_t v = ((static_cast<int64_t>(x) + 1) * P - 1) / total;
-      return static_cast<int>(v < P - 1 ? v : P - 1);
-    };
-    const bool packed = 2 * a.G <= 8;  // columns g (high) and g + G (low)
-    for (int c = cta_of(s0); c <= cta_of(s1 - 1); ++c) {
-      const int64_t rec = (static_cast<int64_t>(b) + c) * a.H + h;
-      const float2 ml = *reinterpret_cast<const float2 *>(a.sfx_ml + (rec * 8 + gq) * 2);
-      if (ml.x == -INFINITY) continue;
-      float o[CPL];
-      load(a.sfx_o + (rec * 8 + gq) * D, o);
-      if (packed) {
-        float y[CPL];
-        load(a.sfx_o + (rec * 8 + gq + a.G) * D, y);
+  auto ml_of = [&](int i) -> float2 {
+    if (i < n0) {
+      const int64_t at = pslot + static_cast<int64_t>(i / streams) * kPrefixRows + (i % streams) * prows + prow;
+      return *reinterpret_cast<const float2 *>(a.ws_ml + at * 2);
+    }
+    return *reinterpret_cast<const float2 *>(a.sfx_ml + (srec + static_cast<int64_t>(i - n0) * a.H * 8) * 2);
+  };
+  auto o_of = [&](int i) -> float4 {
+    if (i < n0) {
+      const int64_t at = pslot + static_cast<int64_t>(i / streams) * kPrefixRows + (i % streams) * prows;
+      return reinterpret_cast<const float4 *>(a.ws_o + at * D)[cg * prows + prow];
+    }
+    const float *p = a.sfx_o + (srec + static_cast<int64_t>(i - n0) * a.H * 8) * D + 4 * cg;
+    float4 v = *reinterpret_cast<const float4 *>(p);
+    if (packed) {
+      const float4 y = *reinterpret_cast<const float4 *>(p + a.G * D);
+      v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+    }
+    return v;
+  };
+  const int n = n0 + n1;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float L = 0.f, mx = -INFINITY;
+  for (int i = 0; i < n; i += U) {
+    // a batch's largest m, then its weighted sum; partials without weight (a
+    // warpgroup that had no tile, a row masked there) hold no O
+    float2 ml[U];
 #pragma unroll
-        for (int k = 0; k < CPL; ++k) o[k] += y[k];
-      }
-      add(ml.x, ml.y, o);
+    for (int k = 0; k < U; ++k) ml[k] = i + k < n ? ml_of(i + k) : make_float2(-INFINITY, 0.f);
+    float4 v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) v[k] = i + k < n ? o_of(i + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float mn = mx;
+#pragma unroll
+    for (int k = 0; k < U; ++k) mn = fmaxf(mn, ml[k].x);
+    if (mn == -INFINITY) continue;
+    const float keep = exp2f(mx - mn);
+    mx = mn;
+    L *= keep;
+    acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (ml[k].x == -INFINITY) continue;
+      const float w = exp2f(ml[k].x - mn);
+      L = fmaf(w, ml[k].y, L);
+      acc.x = fmaf(w, v[k].x, acc.x);
+      acc.y = fmaf(w, v[k].y, acc.y);
+      acc.z = fmaf(w, v[k].z, acc.z);
+      acc.w = fmaf(w, v[k].w, acc.w);
     }
   }
-  // ---- the full-precision tail of a per-channel K cache
+  // ---- the full-precision tail of a per-channel K cache (products summed over
+  // the row's threads in shared memory)
   if (a.res_k != nullptr) {
-    const int nt = a.ws_ctx[b] % kBlockSize;
-    const uint16_t *q = a.q + static_cast<int64_t>(id) * D + lane * CPL;
+    const int nt = live ? a.ws_ctx[b] % kBlockSize : 0;
+    const uint2 qw = live ? *reinterpret_cast<const uint2 *>(a.q + (static_cast<int64_t>(b) * a.Hq + h * a.G + gq) * D + 4 * cg)
+                          : make_uint2(0u, 0u);
     const float zs = rsqrtf(static_cast<float>(D)) * kLog2e;
-    for (int t = 0; t < nt; ++t) {
-      const int64_t at = ((static_cast<int64_t>(b) * kBlockSize + t) * a.H + h) * D + lane * CPL;
-      float dot = 0.f, o[CPL];
-#pragma unroll
-      for (int k = 0; k < CPL; ++k) {
-        dot += bf16lo_to_f32(q[k]) * bf16lo_to_f32(a.res_k[at + k]);
-        o[k] = bf16lo_to_f32(a.res_v[at + k]);
+    for (int t = 0; t < kBlockSize; ++t) {
+      const bool in = t < nt;
+      const int64_t at = ((static_cast<int64_t>(b) * kBlockSize + t) * a.H + h) * D + 4 * cg;
+      float dot = 0.f;
+      if (in) {
+        const uint2 k = *reinterpret_cast<const uint2 *>(a.res_k + at);
+        dot = bf16lo_to_f32(qw.x) * bf16lo_to_f32(k.x) + bf16hi_to_f32(qw.x) * bf16hi_to_f32(k.x) +
+              bf16lo_to_f32(qw.y) * bf16lo_to_f32(k.y) + bf16hi_to_f32(qw.y) * bf16hi_to_f32(k.y);
       }
+      // lanes rl, rl + 8, .. of a warp share a row; then the warps
 #pragma unroll
-      for (int s = 16; s >= 1; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-      add(dot * zs, 1.f, o);
+      for (int o = kMergeRows; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      __syncthreads();
+      if ((threadIdx.x & 31) < kMergeRows) sh[rl][threadIdx.x >> 5] = dot;
+      __syncthreads();
+      if (in) {
+        float z = 0.f;
+        for (int w = 0; w < kMergeRows * CG / 32; ++w) z += sh[rl][w];
+        z *= zs;
+        const uint2 v = *reinterpret_cast<const uint2 *>(a.res_v + at);
+        const float mn = fmaxf(mx, z), keep = exp2f(mx - mn), p = exp2f(z - mn);
+        mx = mn;
+        L = L * keep + p;
+        acc.x = acc.x * keep + p * bf16lo_to_f32(v.x);
+        acc.y = acc.y * keep + p * bf16hi_to_f32(v.x);
+        acc.z = acc.z * keep + p * bf16lo_to_f32(v.y);
+        acc.w = acc.w * keep + p * bf16hi_to_f32(v.y);
+      }
     }
+    __syncthreads();
   }
   const float inv = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll
-  for (int k = 0; k < CPL; ++k) acc[k] *= inv;
+  acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
   if (a.rot) {
-    // back from the rotated basis: sigma * (H o) / d, stages below CPL inside
-    // the lane, the others across lanes
+    // back from the rotated basis, sigma * (H o) / d: stages 1 and 2 in the
+    // thread, the others between threads through shared memory
+    float t0 = acc.x + acc.y, t1 = acc.x - acc.y, t2 = acc.z + acc.w, t3 = acc.z - acc.w;
+    float4 y = make_float4(t0 + t2, t1 + t3, t0 - t2, t1 - t3);
 #pragma unroll
-    for (int s = 1; s < CPL; s <<= 1)
-#pragma unroll
-      for (int k = 0; k < CPL; ++k)
-        if (!(k & s)) {
-          const float x = acc[k], y = acc[k + s];
-          acc[k] = x + y;
-          acc[k + s] = x - y;
-        }
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-#pragma unroll
-      for (int k = 0; k < CPL; ++k) {
-        const float p = __shfl_xor_sync(0xffffffffu, acc[k], s);
-        acc[k] = (lane & s) ? p - acc[k] : acc[k] + p;
-      }
+    for (int s = 1; s < CG; s <<= 1) {
+      *reinterpret_cast<float4 *>(&sh[rl][4 * cg]) = y;
+      __syncthreads();
+      const float4 p = *reinterpret_cast<const float4 *>(&sh[rl][4 * (cg ^ s)]);
+      const float f = (cg & s) ? -1.f : 1.f;
+      y = make_float4(fmaf(f, y.x, p.x), fmaf(f, y.y, p.y), fmaf(f, y.z, p.z), fmaf(f, y.w, p.w));
+      __syncthreads();
     }
-#pragma unroll
-    for (int k = 0; k < CPL; ++k) {
-      const int ch = lane * CPL + k;
-      const float x = acc[k] * (1.f / D);
-      acc[k] = (a.rot_signs[ch >> 5] >> (ch & 31)) & 1u ? -x : x;
-    }
+    const uint32_t neg = a.rot_signs[cg >> 3] >> (4 * (cg & 7));
+    constexpr float kInvD = 1.f / D;
+    acc.x = y.x * (neg & 1u ? -kInvD : kInvD);
+    acc.y = y.y * (neg & 2u ? -kInvD : kInvD);
+    acc.z = y.z * (neg & 4u ? -kInvD : kInvD);
+    acc.w = y.w * (neg & 8u ? -kInvD : kInvD);
   }
   // BF16 out, rounded once: what the output projection reads
-  uint32_t *out = reinterpret_cast<uint32_t *>(a.out + static_cast<int64_t>(id) * D + lane * CPL);
-#pragma unroll
-  for (int k = 0; k < CPL; k += 2) {
-    uint32_t w;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(acc[k + 1]), "f"(acc[k]));
-    out[k / 2] = w;
+  if (live) {
+    uint2 w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(acc.y), "f"(acc.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(acc.w), "f"(acc.z));
+    *reinterpret_cast<uint2 *>(a.out + (static_cast<int64_t>(b) * a.Hq + h * a.G + gq) * D + 4 * cg) = w;
   }
 }
 
@@ -340,9 +378,9 @@ cudaError_t launch_prefix_attend(int head_dim, int kf, int vf, const PrefixArgs 
 }
 
 cudaError_t launch_prefix_merge(int head_dim, const PrefixArgs &a, cudaStream_t stream) {
-  const int n = (a.B * a.Hq + 7) / 8;
-  if (head_dim == 128) prefix_merge_kernel<128><<<n, 256, 0, stream>>>(a);
-  else prefix_merge_kernel<64><<<n, 256, 0, stream>>>(a);
+  const int n = (a.B * a.G + kMergeRows - 1) / kMergeRows * a.H;
+  if (head_dim == 128) prefix_merge_kernel<128><<<n, kMergeRows * 32, 0, stream>>>(a);
+  else prefix_merge_kernel<64><<<n, kMergeRows * 16, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
