@@ -4,17 +4,17 @@
 // Mathematics.  For the rows of a unit (256 or 128 (sequence, query head)
 // pairs of one kv head) and a tile of 128 shared positions:
 //   S = Q' K'^T          f16 operands, FP32 accumulators in tensor memory
-//   t = S ks, z = t c    ks the position's factor, c the row's (z in log2 units)
-//   p = 2^(z - m), l += p, O += (p vs) V'
+//   z = S 2^-eb c        c the row's factor (z in log2 units)
+//   p = 2^(z - m + 8), l += p, O += p V'
 // Q' = q 2^er in f16 (the row's largest in [2^14, 2^15): a BF16 q is exact
-// down to 2^-32 of it).  K' is the codes (exact), ks their scale per token; or,
-// with scales per channel, code * s 2^eb rounded once (the tile's largest
-// s 2^eb in [2^7, 2^8)), ks = 2^-eb.  V' is the codes (exact) and vs = s_v 2^F;
-// or, with scales per 32 channels, code * s 2^F rounded once and vs = 1.  F
-// only falls: the largest s 2^F of a tile stays below 2^9, and p <= 2^6 (the
-// reference m is raised only when a score passes m + 6), so p vs fits f16; a
-// new m or F rescales O in tensor memory.  p vs is rounded to f16 once; l sums
-// the unrounded p.
+// down to 2^-32 of it).  K' = code * s 2^eb and V' = code * s 2^F, each rounded to
+// f16 once: scales per position multiplied into the scores and probabilities
+// instead would keep the codes exact, but every thread then reads all 128 of
+// them from shared memory, whose bandwidth bounds the kernel (the products read
+// their operands there).  Powers of two keep K' and V' below 2^15: eb by tile; F
+// falls when a tile's scales need it and O follows, as it does when m is
+// raised (only past m + 6, so p <= 2^14).  p is rounded to f16 once; l sums the
+// unrounded p.
 //
 // Roles, one CTA per SM: two softmax warpgroups (thread = row), two
 // warpgroups that turn codes into f16 tiles in shared memory (one K, one V),
@@ -41,12 +41,12 @@ constexpr int kTileBlocks = kTile / kBlockSize;
 // Warps by role: the single-warp roles, which everybody waits for, come first.
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kScaleWarp = 2, kKWarp = 4, kVWarp = 8, kSoftmaxWarp = 12;
 constexpr int kThreads = 20 * 32;
-constexpr uint32_t kUnit = 4096;               // unit of the rings of codes: a part of a tile
+constexpr uint32_t kPair = 4096;               // codes that a converter warpgroup takes in one turn
 constexpr int kMaxUnits = 8;                   // per ring
 constexpr uint32_t kMaxSmem = 227 * 1024;
 constexpr int kMeta = 4;                       // ring of per-tile factors
 constexpr float kRaise = 6.f;                  // m is raised past m + 6
-constexpr int kTopV = 9;                       // s 2^F < 2^9
+constexpr float kBias = 8.f;                   // p's factor 2^8: small p stay normal f16 numbers
 
 // Bits per code and the conversion.
 enum Code : int { C_INT8, C_FP8, C_INT4, C_INT2 };
@@ -61,6 +61,8 @@ struct VCode {
   static constexpr bool group = VF == V_INT4_G32 || VF == V_INT2_G32;
 };
 constexpr int code_bits(Code c) { return c == C_INT4 ? 4 : c == C_INT2 ? 2 : 8; }
+// Scales below 2^top keep code * scale below 2^15 (codes up to 448, 127, 7, 1).
+constexpr int top_exponent(Code c) { return c == C_FP8 ? 6 : 8; }
 
 // Shared memory: f16 tiles ([64-channel half][row][128 bytes], swizzled), then
 // the small arrays, then the ring of codes, as long as there is room.
@@ -68,27 +70,28 @@ template <int D>
 struct Smem {
   static constexpr uint32_t HALF = 128 * 128;           // 64 channels of 128 rows
   static constexpr uint32_t TILE = HALF * (D / 64);
-  static constexpr uint32_t CHAN = kTileBlocks * D * 2; // one part of the channel scales
-  static constexpr uint32_t GRP = kTile * (D / 32) * 4; // group scales, f16 pairs (high, low)
+  static constexpr uint32_t CHAN = kTileBlocks * D * 2; // one part (high or low) of the channel scales
+  static constexpr uint32_t POS = kTile * 4;            // scales per position, f16 pairs (high, low)
+  static constexpr uint32_t GRP = POS * (D / 32);       // and per position and group
   static constexpr uint32_t k = 0;                      // [2] stages
   static constexpr uint32_t v = k + 2 * TILE;           // [2] stages
   static constexpr uint32_t q = v + 2 * TILE;           // [1 or 2] row tiles
   // offsets from the end of q
-  static constexpr uint32_t ks = 0;                     // [kMeta][128] FP32
-  static constexpr uint32_t vs = ks + kMeta * kTile * 4;
-  static constexpr uint32_t info = vs + kMeta * kTile * 4;         // [kMeta] {F, block mask}
-  static constexpr uint32_t bars = info + kMeta * 8;    // mbarriers
+  static constexpr uint32_t info = 0;                   // [kMeta] {F, block mask, 2^-eb, -}
+  static constexpr uint32_t bars = info + kMeta * 16;   // mbarriers
   static constexpr uint32_t tmem = bars + 56 * 8;       // tensor memory address, then the abort flag
   static constexpr uint32_t factors = tmem + 16;        // [128] row factors
-  static constexpr uint32_t scales = factors + 512;     // [2] channel scales (high, low parts) and group scales
-  static_assert(scales % 16 == 0 && scales <= 5 * 1024 + 512, "small arrays");
+  static constexpr uint32_t segment = factors + 512;    // the CTA's first segment
+  static constexpr uint32_t scales = segment + 96;      // [2] scales of K, then [2] of V, as f16 pairs
+  static_assert(scales % 16 == 0, "small arrays");
 };
 
 // What depends on the formats and on whether any unit has two row tiles.
 struct Layout {
-  uint32_t small, grp;        // offsets: small arrays, group scales (from `scales`)
+  uint32_t small, vscales;    // offsets: small arrays, scales of V (from `scales`)
   uint32_t ring[2];           // the rings of K and V codes
-  int units[2];
+  int units[2];               // places in the rings,
+  uint32_t unit[2];           // and their bytes: a tile of codes or a part of one
   uint32_t bytes;
 };
 template <int D>
@@ -96,17 +99,21 @@ inline Layout layout_of(bool chan, bool group, bool two, int krow, int vrow) {
   using L = Smem<D>;
   Layout y;
   y.small = L::q + (two ? 2 : 1) * L::TILE;
-  y.grp = chan ? 4 * L::CHAN : 0;
-  y.ring[0] = (y.small + L::scales + y.grp + (group ? 2 * L::GRP : 0) + 1023) & ~1023u;
-  // as many units as there is room for, shared out by the bytes of a row
-  const int room = static_cast<int>((kMaxSmem - y.ring[0]) / kUnit);
-  int k = (room * krow + (krow + vrow) / 2) / (krow + vrow);
+  y.vscales = chan ? 4 * L::CHAN : 2 * L::POS;
+  y.ring[0] = (y.small + L::scales + y.vscales + 2 * (group ? L::GRP : L::POS) + 1023) & ~1023u;
+  // Units of up to 8 KB, fewer to wait for; of 4 KB where two row tiles leave
+  // little room.  As many as fit, shared out by the bytes of a row.
+  const uint32_t room = kMaxSmem - y.ring[0], most = two ? kPair : 2 * kPair;
+  const int row[2] = {krow, vrow};
+  for (int i = 0; i < 2; ++i) y.unit[i] = kTile * row[i] < static_cast<int>(most) ? kTile * row[i] : most;
+  int k = static_cast<int>((room * krow / (krow + vrow) + y.unit[0] / 2) / y.unit[0]);
   if (k < 1) k = 1;
-  if (k > room - 1) k = room - 1;
+  while (k > 1 && k * y.unit[0] + y.unit[1] > room) --k;
+  const int v = static_cast<int>((room - k * y.unit[0]) / y.unit[1]);
   y.units[0] = k < kMaxUnits ? k : kMaxUnits;
-  y.units[1] = room - k < kMaxUnits ? room - k : kMaxUnits;
-  y.ring[1] = y.ring[0] + y.units[0] * kUnit;
-  y.bytes = y.ring[1] + y.units[1] * kUnit;
+  y.units[1] = v < kMaxUnits ? v : kMaxUnits;
+  y.ring[1] = y.ring[0] + y.units[0] * y.unit[0];
+  y.bytes = y.ring[1] + y.units[1] * y.unit[1];
   return y;
 }
 
@@ -127,7 +134,7 @@ struct Segment {
   bool two;          // two row tiles
 };
 
-__device__ __noinline__ void segment_at(const PrefixArgs &a, int x, int x1, Segment *out) {
+__device__ __noinline__ void find_segment(const PrefixArgs &a, int x, int x1, Segment *out) {
   int lo = 0, hi = a.groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -145,6 +152,16 @@ __device__ __noinline__ void segment_at(const PrefixArgs &a, int x, int x1, Segm
   *out = s;
 }
 
+// The CTA's first segment is found once and kept in shared memory.
+struct Segments {
+  const Segment *first;
+  int x0;
+};
+__device__ __forceinline__ void segment_at(const PrefixArgs &a, const Segments &f, int x, int x1, Segment *out) {
+  if (x == f.x0) *out = *f.first;
+  else find_segment(a, x, x1, out);
+}
+
 // Waits for a phase of an mbarrier.  When a wait runs out, the error is set and
 // every later wait of the CTA returns at once: the roles run to their ends (all
 // barriers between threads are met, all accesses stay in bounds), and the
@@ -159,18 +176,6 @@ __device__ __forceinline__ bool mbar_suspend_wait(uint64_t *bar, uint32_t parity
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-      : "memory");
-  return ok != 0;
-}
-
-__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -240,7 +245,7 @@ struct Cover {
   static constexpr int CH = ROW / 16;              // chunks per row = loads per thread
   static constexpr int NP = 16 * 8 / code_bits(C) / 8;  // pieces per chunk
   static constexpr int STEP = kTile / CH;
-  static constexpr int UNITS = kTile * ROW / static_cast<int>(kUnit);  // ring units of a tile
+  static constexpr int PAIRS = CH / 2;             // turns of two loads, kPair bytes of codes
   int c, k0;
   bool swap;
   uint32_t place, row0;  // of piece 0 at row k0
@@ -263,28 +268,28 @@ __device__ __forceinline__ void convert_tile(const Cover<D, C> &f, const Waiter 
                                              const Layout &y, int &unit, uint32_t &phase, uint32_t tile, uint32_t mask,
                                              int lane, Scale scale) {
   using F = Cover<D, C>;
-  constexpr int LPU = F::CH / F::UNITS;  // loads per thread and unit
-  static_assert(LPU == 2, "two loads per thread and unit");
   // loads that are unrolled together: enough to overlap their latencies, few
   // enough for the instruction caches that the roles of an SM's warps share
   constexpr int U = C == C_INT2 ? 1 : 2;
+  const uint32_t end = y.unit[which];
+  uint32_t done = 0;  // bytes of the unit
 #pragma unroll 1
-  for (int u = 0; u < F::UNITS; ++u) {
-    wait(B_FULL + which * kMaxUnits + unit, phase);
-    const uint32_t raw = ring + unit * kUnit;
+  for (int u = 0; u < F::PAIRS; ++u) {
+    if (done == 0) wait(B_FULL + which * kMaxUnits + unit, phase);
+    const uint32_t raw = ring + unit * end + done;
 #pragma unroll 1
-    for (int e0 = 0; e0 < LPU; e0 += U) {
+    for (int e0 = 0; e0 < 2; e0 += U) {
       uint4 w[U];
 #pragma unroll
       for (int e = 0; e < U; ++e) w[e] = lds128(raw + swz<F::ROW>((f.k0 + F::STEP * (e0 + e)) * F::ROW + 16 * f.c));
       if (mask != 0xFFu) {
 #pragma unroll
         for (int e = 0; e < U; ++e)
-          if (!((mask >> ((f.k0 + F::STEP * (LPU * u + e0 + e)) / kBlockSize)) & 1u)) w[e] = make_uint4(0u, 0u, 0u, 0u);
+          if (!((mask >> ((f.k0 + F::STEP * (2 * u + e0 + e)) / kBlockSize)) & 1u)) w[e] = make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int e = 0; e < U; ++e) {
-        const int i = LPU * u + e0 + e;
+        const int i = 2 * u + e0 + e;
         const uint4 x = f.swap ? make_uint4(w[e].z, w[e].w, w[e].x, w[e].y) : w[e];
         const uint32_t at = tile + f.row0 + i * F::STEP * 128;
         auto piece = [&](auto jj) {
@@ -305,6 +310,9 @@ __device__ __forceinline__ void convert_tile(const Cover<D, C> &f, const Waiter 
         piece(std::integral_constant<int, 7>{});
       }
     }
+    done += kPair;
+    if (done < end) continue;
+    done = 0;
     __syncwarp();
     if (lane == 0) mbar_arrive(&wait.bars[B_EMPTY + which * kMaxUnits + unit]);
     if (++unit == y.units[which]) {
@@ -314,6 +322,16 @@ __device__ __forceinline__ void convert_tile(const Cover<D, C> &f, const Waiter 
   }
 }
 
+// The f16 pair (high, low) of one scale, each part in both halves.
+struct ScalePair {
+  uint4 hi, lo;
+  __device__ __forceinline__ explicit ScalePair(uint32_t z) {
+    const uint32_t h = prmt(z, 0u, 0x1010u), l = prmt(z, 0u, 0x3232u);
+    hi = make_uint4(h, h, h, h);
+    lo = make_uint4(l, l, l, l);
+  }
+};
+
 template <int D, int KF>
 __device__ __noinline__ void convert_k_role(uint32_t base, const Layout &y, const Waiter &wait, int tiles) {
   using L = Smem<D>;
@@ -321,7 +339,7 @@ __device__ __noinline__ void convert_k_role(uint32_t base, const Layout &y, cons
   using F = Cover<D, KC::code>;
   const int tid = threadIdx.x & 127, lane = tid & 31;
   const F f(tid);
-  const uint32_t chan = base + y.small + L::scales, ring = base + y.ring[0];
+  const uint32_t scales = base + y.small + L::scales, ring = base + y.ring[0];
   int unit = 0;
   uint32_t phase = 0;
 #pragma unroll 1
@@ -329,16 +347,19 @@ __device__ __noinline__ void convert_k_role(uint32_t base, const Layout &y, cons
     const int st = n & 1;
     const uint32_t ph = (n >> 1) & 1;
     wait(B_META + st, ph);
-    const uint32_t mask = lds64(base + y.small + L::info + (n % kMeta) * 8).y;
+    const uint32_t mask = lds32(base + y.small + L::info + (n % kMeta) * 16 + 4);
     wait(B_KEMPTY + st, ph ^ 1);
     convert_tile<D, KC::code>(f, wait, 0, ring, y, unit, phase, base + L::k + st * L::TILE, mask, lane,
                               [&](int i, int j, uint4 &r) {
       if constexpr (KC::chan) {
         const int blk = (f.k0 + F::STEP * i) / kBlockSize;
         const int piece = f.c * F::NP + (f.swap ? j ^ (F::NP / 2) : j);
-        const uint32_t p = chan + st * 2 * L::CHAN + (blk * D + 8 * piece) * 2;
+        const uint32_t p = scales + st * 2 * L::CHAN + (blk * D + 8 * piece) * 2;
         const uint4 hi = lds128(p);
         apply_scales<KC::code>(r, hi, KC::code == C_INT2 ? hi : lds128(p + L::CHAN));
+      } else {
+        const ScalePair z(lds32(scales + st * L::POS + (f.k0 + F::STEP * i) * 4));
+        apply_scales<KC::code>(r, z.hi, z.lo);
       }
     });
     fence_proxy_async_shared();
@@ -352,10 +373,10 @@ __device__ __noinline__ void convert_v_role(uint32_t base, const Layout &y, cons
   using L = Smem<D>;
   using VC = VCode<VF>;
   using F = Cover<D, VC::code>;
-  constexpr int NG = D / 32;
+  constexpr int NG = VC::group ? D / 32 : 1;
   const int tid = threadIdx.x & 127, lane = tid & 31;
   const F f(tid);
-  const uint32_t grp = base + y.small + L::scales + y.grp, ring = base + y.ring[1];
+  const uint32_t scales = base + y.small + L::scales + y.vscales, ring = base + y.ring[1];
   int unit = 0;
   uint32_t phase = 0;
 #pragma unroll 1
@@ -363,17 +384,14 @@ __device__ __noinline__ void convert_v_role(uint32_t base, const Layout &y, cons
     const int st = n & 1;
     const uint32_t ph = (n >> 1) & 1;
     wait(B_META + st, ph);
-    const uint32_t mask = lds64(base + y.small + L::info + (n % kMeta) * 8).y;
+    const uint32_t mask = lds32(base + y.small + L::info + (n % kMeta) * 16 + 4);
     wait(B_VEMPTY + st, ph ^ 1);
     convert_tile<D, VC::code>(f, wait, 1, ring, y, unit, phase, base + L::v + st * L::TILE, mask, lane,
                               [&](int i, int j, uint4 &r) {
-      if constexpr (VC::group) {
-        const int key = f.k0 + F::STEP * i;
-        const int piece = f.c * F::NP + (f.swap ? j ^ (F::NP / 2) : j);
-        const uint32_t z = lds32(grp + st * L::GRP + (key * NG + piece / 4) * 4);
-        const uint32_t hi = prmt(z, 0u, 0x1010u), lo = prmt(z, 0u, 0x3232u);
-        apply_scales<VC::code>(r, make_uint4(hi, hi, hi, hi), make_uint4(lo, lo, lo, lo));
-      }
+      const int key = f.k0 + F::STEP * i;
+      const int piece = f.c * F::NP + (f.swap ? j ^ (F::NP / 2) : j);
+      const ScalePair z(lds32(scales + st * L::POS * NG + (key * NG + (VC::group ? piece / 4 : 0)) * 4));
+      apply_scales<VC::code>(r, z.hi, z.lo);
     });
     fence_proxy_async_shared();
     __syncwarp();
@@ -396,14 +414,15 @@ __device__ __forceinline__ void tma_tile_load(uint32_t dst, const CUtensorMap *m
 // next two tiles under way: lane j of a warp has block j % 8.
 struct TileWalk {
   const PrefixArgs &a;
+  const Segments &seg;
   const int x1;
   int x;                  // this tile
   const int32_t *row;     // of the next tile: the leader's table, its shared blocks, its segment's end
   int count, t1, end;
   int h, h1, raw, raw1, b;
   bool first, first1;     // first tile of a segment
-  __device__ __forceinline__ TileWalk(const PrefixArgs &args, int from, int to)
-      : a(args), x1(to), x(from - 2), t1(0), end(0), h1(0), raw1(INT_MIN), b(threadIdx.x & 7), first1(false) {}
+  __device__ __forceinline__ TileWalk(const PrefixArgs &args, const Segments &segments, int from, int to)
+      : a(args), seg(segments), x1(to), x(from - 2), t1(0), end(0), h1(0), raw1(INT_MIN), b(threadIdx.x & 7), first1(false) {}
   // to the next tile, and the ids of the one after it (twice to reach the first)
   __device__ __forceinline__ void next() {
     ++x;
@@ -414,7 +433,7 @@ struct TileWalk {
     first1 = ++t1 >= end;
     if (first1) {
       Segment s;
-      segment_at(a, x + 1, x1, &s);
+      segment_at(a, seg, x + 1, x1, &s);
       row = a.tables + static_cast<int64_t>(s.g.lead) * a.max_blocks;
       count = s.g.shared / kBlockSize;
       t1 = s.t0;
@@ -432,166 +451,228 @@ struct TileWalk {
   }
 };
 
-// Codes into the rings, a TMA box (16 rows of one head) per block: lanes 0 .. 7
-// have the tile's K blocks, 8 .. 15 its V blocks.  The lanes of a ring poll
-// together for its next place, so K and V do not wait for each other.
+// Codes into the rings, a TMA box (16 rows of one head) per block, in the order
+// K(0), K(1), V(0), K(2), V(1), ...: K is wanted about a tile before V.
 __device__ __noinline__ void load_role(const PrefixArgs &a, const CUtensorMap *kmap, const CUtensorMap *vmap, int krow,
-                                       int vrow, uint32_t base, const Layout &y, const Waiter &wait, int x, int x1) {
-  const int lane = threadIdx.x & 31, r = (lane >> 3) & 1;
-  const int row = r ? vrow : krow, units = kTile * row / static_cast<int>(kUnit);  // units of a tile
-  const int u = (lane & 7) * units / kTileBlocks;  // the unit of this lane's block
-  const uint32_t box = kBlockSize * row, place = base + y.ring[r] + ((lane & 7) - u * (kTileBlocks / units)) * box;
-  const CUtensorMap *map = r ? vmap : kmap;
-  TileWalk w(a, x, x1);
+                                       int vrow, uint32_t base, const Layout &y, const Waiter &wait, const Segments &seg,
+                                       int x, int x1) {
+  const int lane = threadIdx.x & 31, tiles = x1 - x;
+  TileWalk w(a, seg, x, x1);
+  int slot[2] = {0, 0}, kid = -1, kh = 0, vid, vh;
+  uint32_t phase[2] = {1, 1};
+  w.next();
+  // step n: K of tile n, then V of tile n - 1
 #pragma unroll 1
-  for (int k = 0; k < 2; ++k) w.next();
-  int id = w.id(lane < 8), slot = 0, turn = 0, used = 0;
-  uint32_t phase = 1, used_phase = 0;
-  bool left = lane < 16, stopped = false;
-  long long last = clock64();
+  for (int n = 0; n <= tiles; ++n) {
+    vid = kid;
+    vh = kh;
+    if (n < tiles) {
+      w.next();
+      kid = w.id(lane < 8);
+      kh = w.h;
+    }
 #pragma unroll 1
-  while (__any_sync(0xffffffffu, left) && !stopped) {
-    const int bar = r * kMaxUnits + slot;
-    const bool go = left && mbar_test_wait(&wait.bars[B_EMPTY + bar], phase);
-    const bool in = go && u == turn && id >= 0;
-    const uint32_t went = __ballot_sync(0xffffffffu, go), boxes = __ballot_sync(0xffffffffu, in) >> (8 * r) & 0xFFu;
-    uint64_t *full = &wait.bars[B_FULL + bar];
-    if (go && (lane & 7) == 0) {
-      if (boxes) mbar_arrive_expect_tx(full, __popc(boxes) * box);
-      else mbar_arrive(full);
-    }
-    __syncwarp();
-    if (in) tma_tile_load(place + slot * kUnit, map, w.h, id, full);
-    if (go) {
-      used = slot;
-      used_phase = phase;
-      if (++slot == y.units[r]) {
-        slot = 0;
-        phase ^= 1;
+    for (int r = n < tiles ? 0 : 1; r < (n > 0 ? 2 : 1); ++r) {
+      const CUtensorMap *map = r ? vmap : kmap;
+      const int row = r ? vrow : krow, id = r ? vid : kid, h = r ? vh : kh;
+      const int places = y.units[r];
+      const uint32_t box = kBlockSize * row, bytes = y.unit[r], ring = base + y.ring[r];
+      const int per = static_cast<int>(bytes / box);  // blocks of a unit
+      int at = r ? slot[1] : slot[0];
+      uint32_t ph = r ? phase[1] : phase[0];
+#pragma unroll 1
+      for (int b = 0; b < kTileBlocks; b += per) {
+        const int bar = r * kMaxUnits + at;
+        wait(B_EMPTY + bar, ph);
+        const bool in = static_cast<unsigned>(lane - b) < static_cast<unsigned>(per) && id >= 0;
+        const int boxes = __popc(__ballot_sync(0xffffffffu, in));
+        uint64_t *full = &wait.bars[B_FULL + bar];
+        if (lane == 0) {
+          if (boxes) mbar_arrive_expect_tx(full, boxes * box);
+          else mbar_arrive(full);
+        }
+        __syncwarp();
+        // (after a wait that ran out nobody reads: no further copies)
+        if (in && !*wait.abort) tma_tile_load(ring + at * bytes + (lane - b) * box, map, h, id, full);
+        if (++at == places) {
+          at = 0;
+          ph ^= 1;
+        }
       }
-      if (++turn == units) {
-        turn = 0;
-        w.next();
-        left = w.x < x1;
-        id = w.id(lane < 8 && left);
+      if (r) {
+        slot[1] = at;
+        phase[1] = ph;
+      } else {
+        slot[0] = at;
+        phase[0] = ph;
       }
-    }
-    __syncwarp();
-    if (went) {
-      last = clock64();
-    } else {
-      // (decided by the whole warp: its lanes leave the loop together)
-      const bool late = clock64() - last > kWaitTicks;
-      if (late && lane == 0) {
-        *wait.abort = 1;
-        set_error(a.err, KVQ_DEVERR_TIMEOUT);
-      }
-      stopped = __any_sync(0xffffffffu, late || *wait.abort != 0);
     }
   }
-  // no copy in flight when the CTA exits: the rings' last units, and so all
-  // before them, are read, or (a wait ran out, and nobody reads) a millisecond
-  // goes by
-  if (stopped) {
+  // no copy in flight when the CTA exits: all units are read, or (a wait ran
+  // out) a millisecond goes by
+  if (*wait.abort) {
     const long long t0 = clock64();
     while (clock64() - t0 < 2000000) {
     }
-  } else if (lane == 0 || lane == 8) {
-    wait(B_EMPTY + r * kMaxUnits + used, used_phase ^ 1);
   }
-  __syncwarp();
+#pragma unroll 1
+  for (int r = 0; r < 2; ++r) {
+    int at = r ? slot[1] : slot[0];
+    uint32_t ph = r ? phase[1] : phase[0];
+#pragma unroll 1
+    for (int k = 0; k < y.units[r]; ++k) {
+      wait(B_EMPTY + r * kMaxUnits + at, ph);
+      if (++at == y.units[r]) {
+        at = 0;
+        ph ^= 1;
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
 // scales
 // ---------------------------------------------------------------------------
-// Per tile: the position factors ks and vs, F and the block mask, and for the
-// converters the scaled channel or group scales as f16 pairs.  Lane l has the
-// positions 4 l .. 4 l + 3.
-template <int D, bool CHAN, bool GROUP>
-__device__ __noinline__ void scale_role(const PrefixArgs &a, uint32_t base, const Layout &y, const Waiter &wait, int x,
-                                        int x1) {
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// Two warps: the scales of K 2^eb and of V 2^F as pairs of f16 (high and low
+// part), for the converters; F, the block mask and 2^-eb, for the softmax.  Lane
+// l has the positions 4 l .. 4 l + 3.  Tile n is written while the loads of n + 1
+// are under way, and the ids of n + 2; one copy of each part.
+
+// Tile n - 2 is converted, and so tile n - 4 is out of the products: tile n's
+// places are free.
+__device__ __forceinline__ void wait_places(const Waiter &wait, int n) {
+  wait(B_KFULL + (n & 1), ((n >> 1) & 1) ^ 1);
+  wait(B_VFULL + (n & 1), ((n >> 1) & 1) ^ 1);
+}
+
+// x f and y f as two f16 pairs, high and (LOW) low parts.
+template <bool LOW>
+__device__ __forceinline__ void scaled_pair(float x, float y, float f, uint32_t &hi, uint32_t &lo) {
+  mul_f32x2(x, y, f, f, x, y);
+  if constexpr (LOW) {
+    split_f16x2(x, y, hi, lo);
+  } else {
+    hi = f32x2_to_f16x2(x, y);
+    lo = 0u;
+  }
+}
+
+// Pairs of N scales (N even) times f, as (high, low) words.
+template <bool LOW, int N>
+__device__ __forceinline__ void pair_scales(const float (&s)[N], float f, uint32_t (&z)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 2) {
+    uint32_t hi, lo;
+    scaled_pair<LOW>(s[e], s[e + 1], f, hi, lo);
+    z[e] = prmt(hi, lo, 0x5410u);
+    z[e + 1] = prmt(hi, lo, 0x7632u);
+  }
+}
+
+// LOW false: 2-bit codes, whose scales are BF16 numbers (q_max 1).
+template <int D, bool CHAN, bool LOW>
+__device__ __noinline__ void scale_k_role(const PrefixArgs &a, uint32_t base, const Layout &y,
+                                          const Waiter &wait, const Segments &seg, int top, int x, int x1) {
   using L = Smem<D>;
-  constexpr int NG = GROUP ? D / 32 : 1;
-  constexpr int NC = CHAN ? kTileBlocks * D / 128 : 1;  // float4 of channel scales
-  const int lane = threadIdx.x & 31;
-  const uint32_t small = base + y.small, chan = small + L::scales, grp = chan + y.grp;
-  TileWalk w(a, x, x1);
-  float sk[CHAN ? 1 : 4], sv[4][NG];
-  float4 sc[NC];
-  uint32_t mask = 0;
-  bool first = false;
-  int F = kNoScale;
-  const int tiles = x1 - x;
-  // this lane's places in block 0 of head 0, and the bytes of a block's scales
+  constexpr int NC = CHAN ? kTileBlocks * D / 128 : 1;  // float4 of scales
+  const int lane = threadIdx.x & 31, tiles = x1 - x;
+  const uint32_t small = base + y.small, to = small + L::scales;
+  TileWalk w(a, seg, x, x1);
+  float sk[NC][4];
+  // this lane's place in block 0 of head 0, and the bytes of a block's scales
   const uint8_t *const kp = reinterpret_cast<const uint8_t *>(a.ks) + (CHAN ? 4 * lane % D : 4 * (lane & 3) * a.H) * 4;
-  const uint8_t *const vp = reinterpret_cast<const uint8_t *>(a.vs) + 4 * (lane & 3) * a.H * NG * 4;
-  const uint32_t kblock = (CHAN ? D : kBlockSize) * a.H * 4, vblock = kBlockSize * a.H * NG * 4;
-  // tile n is written while the loads of n + 1 are under way, and the ids of
-  // n + 2; one copy of each part
+  const uint32_t kblock = (CHAN ? D : kBlockSize) * a.H * 4;
 #pragma unroll 1
   for (int n = -2; n < tiles; ++n) {
     if (n >= 0) {
-    const int st = n & 1, slot = n % kMeta;
-    if (first) F = kNoScale;
-    float vmax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < NG; ++e) vmax = fmaxf(vmax, sv[i][e]);
-    vmax = __uint_as_float(warp_max_u32(__float_as_uint(vmax)));
-    // F: the tile's largest V scale times 2^F below 2^9, set to [2^7, 2^8)
-    if (vmax > 0.f && (F == kNoScale || ilog2f(vmax) + F >= kTopV)) F = min(kTopV - 2 - ilog2f(vmax), kMaxVExp);
-    const float pf = F == kNoScale ? 1.f : pow2i(F);
-    // tile n - 2 is converted, and so tile n - 4 is out of the products: this
-    // tile's places are free
-    wait(B_KFULL + st, ((n >> 1) & 1) ^ 1);
-    wait(B_VFULL + st, ((n >> 1) & 1) ^ 1);
-    const uint32_t at = small + (slot * kTile + 4 * lane) * 4;
-    auto store4 = [](uint32_t to, float p, float q, float r, float s) {
-      sts128(to, __float_as_uint(p), __float_as_uint(q), __float_as_uint(r), __float_as_uint(s));
-    };
-    if constexpr (CHAN) {
+      const int st = n & 1;
       float kmax = 0.f;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) kmax = fmaxf(fmaxf(kmax, fmaxf(sc[i].x, sc[i].y)), fmaxf(sc[i].z, sc[i].w));
+      for (int i = 0; i < NC; ++i) kmax = max3(max3(kmax, sk[i][0], sk[i][1]), sk[i][2], sk[i][3]);
       kmax = __uint_as_float(warp_max_u32(__float_as_uint(kmax)));
-      const int eb = kmax > 0.f ? min(7 - ilog2f(kmax), kMaxVExp) : 0;
-      const float f = pow2i(eb), back = pow2i(-eb);
-      store4(at + L::ks, back, back, back, back);
+      const int eb = kmax > 0.f ? min(top - 1 - ilog2f(kmax), kMaxVExp) : 0;
+      const float f = pow2i(eb);
+      wait_places(wait, n);
+      if constexpr (CHAN) {
+        const uint32_t p = to + st * 2 * L::CHAN + 8 * lane;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        uint32_t h0, l0, h1, l1;
-        split_f16x2(sc[i].x * f, sc[i].y * f, h0, l0);
-        split_f16x2(sc[i].z * f, sc[i].w * f, h1, l1);
-        const uint32_t p = chan + st * 2 * L::CHAN + 8 * (lane + 32 * i);
-        sts64(p, h0, h1);
-        sts64(p + L::CHAN, l0, l1);
-      }
-    } else {
-      store4(at + L::ks, sk[0], sk[1], sk[2], sk[3]);
-    }
-    if constexpr (!GROUP) {
-      store4(at + L::vs, sv[0][0] * pf, sv[1][0] * pf, sv[2][0] * pf, sv[3][0] * pf);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t z[NG];
-#pragma unroll
-        for (int e = 0; e < NG; e += 2) {
-          uint32_t hi, lo;
-          split_f16x2(sv[i][e] * pf, sv[i][e + 1] * pf, hi, lo);
-          z[e] = prmt(hi, lo, 0x5410u);
-          z[e + 1] = prmt(hi, lo, 0x7632u);
+        for (int i = 0; i < NC; ++i) {
+          uint32_t h0, l0, h1, l1;
+          scaled_pair<LOW>(sk[i][0], sk[i][1], f, h0, l0);
+          scaled_pair<LOW>(sk[i][2], sk[i][3], f, h1, l1);
+          sts64(p + 256 * i, h0, h1);
+          if constexpr (LOW) sts64(p + 256 * i + L::CHAN, l0, l1);
         }
-        const uint32_t p = grp + st * L::GRP + (4 * lane + i) * NG * 4;
-        if constexpr (NG == 4) sts128(p, z[0], z[1], z[2], z[3]);
-        else sts64(p, z[0], z[1]);
+      } else {
+        uint32_t z[4];
+        pair_scales<LOW>(sk[0], f, z);
+        sts128(to + st * L::POS + 16 * lane, z[0], z[1], z[2], z[3]);
+      }
+      if (lane == 0) sts32(small + L::info + (n % kMeta) * 16 + 8, __float_as_uint(pow2i(-eb)));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&wait.bars[B_META + st]);
+    }
+    w.next();
+    if (n + 1 < 0 || n + 1 >= tiles) continue;
+    const int ids = w.id(false);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      // channels 4 (lane + 32 i) .. of the tile's [block][channel] scales, or positions
+      const int b = __shfl_sync(0xffffffffu, ids, CHAN ? 4 * (lane + 32 * i) / D : lane / 4);
+      const uint8_t *const kq = kp + static_cast<uint64_t>(static_cast<uint32_t>(max(b, 0))) * kblock + w.h * (CHAN ? D * 4 : 4);
+      if constexpr (CHAN) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(kq));
+        sk[i][0] = v.x; sk[i][1] = v.y; sk[i][2] = v.z; sk[i][3] = v.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sk[i][e] = __ldg(reinterpret_cast<const float *>(kq + e * a.H * 4));
       }
     }
-    if (lane == 0) sts64(small + L::info + slot * 8, static_cast<uint32_t>(F), mask);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&wait.bars[B_META + st]);
+    if (__any_sync(0xffffffffu, ids < 0)) {  // missing blocks count as scale 0
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (__shfl_sync(0xffffffffu, ids, CHAN ? 4 * (lane + 32 * i) / D : lane / 4) < 0)
+          sk[i][0] = sk[i][1] = sk[i][2] = sk[i][3] = 0.f;
+    }
+  }
+}
+
+template <int D, bool GROUP, bool LOW>
+__device__ __noinline__ void scale_v_role(const PrefixArgs &a, uint32_t base, const Layout &y,
+                                          const Waiter &wait, const Segments &seg, int top, int x, int x1) {
+  using L = Smem<D>;
+  constexpr int NG = GROUP ? D / 32 : 1;
+  const int lane = threadIdx.x & 31, tiles = x1 - x;
+  const uint32_t small = base + y.small, to = small + L::scales + y.vscales;
+  TileWalk w(a, seg, x, x1);
+  float sv[4 * NG];
+  uint32_t mask = 0;
+  bool first = false;
+  int F = kNoScale;
+  const uint8_t *const vp = reinterpret_cast<const uint8_t *>(a.vs) + 4 * (lane & 3) * a.H * NG * 4;
+  const uint32_t vblock = kBlockSize * a.H * NG * 4;
+#pragma unroll 1
+  for (int n = -2; n < tiles; ++n) {
+    if (n >= 0) {
+      const int st = n & 1;
+      if (first) F = kNoScale;
+      float vmax = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4 * NG; ++e) vmax = fmaxf(vmax, sv[e]);
+      vmax = __uint_as_float(warp_max_u32(__float_as_uint(vmax)));
+      // F: the tile's largest V scale times 2^F below 2^top, set two below
+      if (vmax > 0.f && (F == kNoScale || ilog2f(vmax) + F >= top)) F = min(top - 2 - ilog2f(vmax), kMaxVExp);
+      wait_places(wait, n);
+      uint32_t z[4 * NG];
+      pair_scales<LOW>(sv, F == kNoScale ? 1.f : pow2i(F), z);
+#pragma unroll
+      for (int e = 0; e < 4 * NG; e += 4)
+        sts128(to + (st * L::POS + 16 * lane) * NG + 4 * e, z[e], z[e + 1], z[e + 2], z[e + 3]);
+      if (lane == 0) sts64(small + L::info + (n % kMeta) * 16, static_cast<uint32_t>(F), mask);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&wait.bars[B_META + st]);
     }
     w.next();
     if (n + 1 < 0 || n + 1 >= tiles) continue;
@@ -599,43 +680,22 @@ __device__ __noinline__ void scale_role(const PrefixArgs &a, uint32_t base, cons
     first = w.first;
     mask = __ballot_sync(0xffffffffu, ids >= 0) & 0xFFu;
     const int id = __shfl_sync(0xffffffffu, ids, lane / 4);
-    const uint64_t blk = static_cast<uint32_t>(max(id, 0));
-    const uint8_t *const vq = vp + blk * vblock + w.h * NG * 4;
+    const uint8_t *const vq = vp + static_cast<uint64_t>(static_cast<uint32_t>(max(id, 0))) * vblock + w.h * NG * 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (!CHAN) sk[i] = __ldg(reinterpret_cast<const float *>(kp + blk * kblock + (w.h + i * a.H) * 4));
       if constexpr (NG == 4) {
         const float4 f = __ldg(reinterpret_cast<const float4 *>(vq + i * a.H * NG * 4));
-        sv[i][0] = f.x; sv[i][1] = f.y; sv[i][2] = f.z; sv[i][3] = f.w;
+        sv[4 * i] = f.x; sv[4 * i + 1] = f.y; sv[4 * i + 2] = f.z; sv[4 * i + 3] = f.w;
       } else if constexpr (NG == 2) {
         const float2 f = __ldg(reinterpret_cast<const float2 *>(vq + i * a.H * NG * 4));
-        sv[i][0] = f.x; sv[i][1] = f.y;
+        sv[2 * i] = f.x; sv[2 * i + 1] = f.y;
       } else {
-        sv[i][0] = __ldg(reinterpret_cast<const float *>(vq + i * a.H * NG * 4));
+        sv[i] = __ldg(reinterpret_cast<const float *>(vq + i * a.H * NG * 4));
       }
     }
-    if constexpr (CHAN) {
-      // channels 4 (lane + 32 i) .. of the tile's [block][channel] scales
-      const uint8_t *const kq = kp + w.h * D * 4;
+    if (id < 0)  // missing blocks count as scale 0
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const uint32_t b = max(__shfl_sync(0xffffffffu, ids, 4 * (lane + 32 * i) / D), 0);
-        sc[i] = __ldg(reinterpret_cast<const float4 *>(kq + static_cast<uint64_t>(b) * kblock));
-      }
-    }
-    if (mask != 0xFFu) {  // missing blocks count as scale 0
-      if (id < 0)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (!CHAN) sk[i] = 0.f;
-#pragma unroll
-          for (int e = 0; e < NG; ++e) sv[i][e] = 0.f;
-        }
-      if constexpr (CHAN)
-#pragma unroll
-        for (int i = 0; i < NC; ++i)
-          if (!((mask >> (4 * (lane + 32 * i) / D)) & 1u)) sc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+      for (int e = 0; e < 4 * NG; ++e) sv[e] = 0.f;
   }
 }
 
@@ -647,7 +707,7 @@ __device__ __noinline__ void scale_role(const PrefixArgs &a, uint32_t base, cons
 // branch of one lane, 16 products took 3000 cycles, three times their work.
 template <int D>
 __device__ __forceinline__ void product_role(const PrefixArgs &a, uint32_t base, const Waiter &wait, uint32_t tmem_addr,
-                                             int x, int x1) {
+                                             const Segments &sg, int x, int x1) {
   using L = Smem<D>;
   constexpr uint32_t id_s = mma_idesc_f16(128, kTile, false), id_o = mma_idesc_f16(128, D, true);
   const bool leader = elect_one();
@@ -659,7 +719,7 @@ __device__ __forceinline__ void product_role(const PrefixArgs &a, uint32_t base,
   uint32_t np = 0;             // bit i: parity of warpgroup i's steps so far
   for (int seg = 0; x < x1; ++seg) {
     Segment s;
-    segment_at(a, x, x1, &s);
+    segment_at(a, sg, x, x1, &s);
     const int tiles = __shfl_sync(0xffffffffu, s.t1 - s.t0, 0), two = __shfl_sync(0xffffffffu, s.two ? 1 : 0, 0);
     const int steps = tiles << two;
     wait(B_Q, seg & 1);
@@ -716,12 +776,10 @@ __device__ __forceinline__ void product_role(const PrefixArgs &a, uint32_t base,
 // ---------------------------------------------------------------------------
 // softmax
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-
 // H (sigma q) of a row spread over a warp, CPL channels per lane: stages below
 // CPL inside the lane, the others across lanes.
 template <int D>
-__device__ __noinline__ void rotate_row(const PrefixArgs &a, float (&y)[D / 32], int lane) {
+__device__ __forceinline__ void rotate_row(const PrefixArgs &a, float (&y)[D / 32], int lane) {
   constexpr int CPL = D / 32;
 #pragma unroll
   for (int e = 0; e < CPL; ++e) {
@@ -749,26 +807,27 @@ __device__ __noinline__ void rotate_row(const PrefixArgs &a, float (&y)[D / 32],
 // The warp's 32 rows of Q' into their tile; `from` is the lane's row of q, -1
 // for none.  Returns this lane's row factor c.  The BF16 rows are copied to the
 // places of the f16 rows (all copies in flight at once) and converted there.
-template <int D>
+template <int D, bool ROT>
 __device__ __noinline__ float stage_queries(const PrefixArgs &a, int from, uint32_t tile, int row0, int lane) {
   constexpr int CPL = D / 32;  // channels per lane
   const uint16_t *const q = a.q + lane * CPL;
   const int ch = lane * CPL;
   const uint32_t at = tile + (ch >> 6) * Smem<D>::HALF + (ch & 7) * 2 + row0 * 128;
-  const uint32_t chunk = (ch & 63) >> 3;
+  const uint32_t chunk = ((ch & 63) >> 3) << 4;
   float c = 0.f;
-#pragma unroll 1
+#pragma unroll 4
   for (int r = 0; r < 32; ++r) {
     const int row = __shfl_sync(0xffffffffu, from, r);
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at + r * 128 + ((chunk ^ (r & 7)) << 4)),
-                 "l"(q + static_cast<int64_t>(max(row, 0)) * D), "n"(CPL * 2), "r"(row < 0 ? 0 : CPL * 2)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at + r * 128 + (chunk ^ ((r & 7) << 4))),
+                 "l"(q + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * D), "n"(CPL * 2),
+                 "r"(row < 0 ? 0 : CPL * 2)
                  : "memory");
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
-#pragma unroll 4
+#pragma unroll(ROT ? 1 : 4)
   for (int r = 0; r < 32; ++r) {
-    const uint32_t to = at + r * 128 + ((chunk ^ (r & 7)) << 4);
+    const uint32_t to = at + r * 128 + (chunk ^ ((r & 7) << 4));
     float y[CPL];
     if constexpr (CPL == 4) {
       const uint2 w = lds64(to);
@@ -777,14 +836,14 @@ __device__ __noinline__ float stage_queries(const PrefixArgs &a, int from, uint3
       const uint32_t w = lds32(to);
       y[0] = bf16lo_to_f32(w); y[1] = bf16hi_to_f32(w);
     }
-    if (a.rot) rotate_row<D>(a, y, lane);
+    if constexpr (ROT) rotate_row<D>(a, y, lane);
     float m = 0.f;
 #pragma unroll
     for (int e = 0; e < CPL; ++e) m = fmaxf(m, fabsf(y[e]));
-    m = __uint_as_float(warp_max_u32(__float_as_uint(m)));
-    // 2^er brings m into [2^14, 2^15).  Below 2^-86 the scores vanish anyway:
-    // er <= 100 keeps 2^er and c normal floats.
-    const int er = m > 0.f ? min(14 - ilog2f(m), 100) : 0;
+    const uint32_t mb = warp_max_u32(__float_as_uint(m));
+    // 2^er brings m into [2^14, 2^15) (a subnormal m counts as 2^-127).  Below
+    // 2^-86 the scores vanish anyway: er <= 100 keeps 2^er and c normal floats.
+    const int er = min(14 + 127 - static_cast<int>(mb >> 23), 100);
     const float f = pow2i(er);
     if (lane == r) c = pow2i(-er);
     uint32_t h[CPL / 2];
@@ -793,14 +852,12 @@ __device__ __noinline__ float stage_queries(const PrefixArgs &a, int from, uint3
     if constexpr (CPL == 4) sts64(to, h[0], h[1]);
     else sts32(to, h[0]);
   }
-  return c * rsqrtf(static_cast<float>(D)) * kLog2e * (a.rot ? 1.f / D : 1.f);
+  return c * rsqrtf(static_cast<float>(D)) * kLog2e * (ROT ? 1.f / D : 1.f);
 }
 
-// KS, VS: factors per position of K and V (else the K factor is one number per
-// tile, and the V factors are 1).
-template <int D, bool KS, bool VS>
+template <int D>
 __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, const Layout &y0, const Waiter &wait,
-                                             uint32_t tmem, int x, int x1) {
+                                             uint32_t tmem, const Segments &sg, int x, int x1) {
   using L = Smem<D>;
   const uint32_t base = smem_u32(smem);
   const int wg = (threadIdx.x >> 7) - kSoftmaxWarp / 4, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
@@ -810,7 +867,7 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
   uint32_t ns = 0, no = 0;     // steps and segments of this warpgroup so far
   for (int seg = 0; x < x1; ++seg) {
     Segment s;
-    segment_at(a, x, x1, &s);
+    segment_at(a, sg, x, x1, &s);
     const int tiles = s.t1 - s.t0, R = s.g.nseq * a.G;
     const int r0 = s.two ? 128 * wg : 0, r = r0 + 32 * warp + lane, row = s.rb * s.g.rows + r;
     const bool live = r < s.g.rows && row < R;
@@ -818,8 +875,9 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
     const int b = s.g.start + row / a.G;
     float c = 0.f;
     if (s.two || wg == 0) {
-      c = stage_queries<D>(a, live ? b * a.Hq + s.h * a.G + row % a.G : -1, base + L::q + (s.two ? wg : 0) * L::TILE,
-                           32 * warp, lane);
+      const int from = live ? b * a.Hq + s.h * a.G + row - (b - s.g.start) * a.G : -1;
+      const uint32_t tile = base + L::q + (s.two ? wg : 0) * L::TILE;
+      c = a.rot ? stage_queries<D, true>(a, from, tile, 32 * warp, lane) : stage_queries<D, false>(a, from, tile, 32 * warp, lane);
       fence_proxy_async_shared();
     }
     __syncwarp();
@@ -844,21 +902,17 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
       __syncwarp();
       ++ns;
       tmem_fence_after();
-      const uint2 info = lds64(base + y0.small + L::info + slot * 8);
+      const uint4 info = lds128(base + y0.small + L::info + slot * 16);
       const int Ft = static_cast<int>(info.x);
-      // plain loads, which the compiler may place ahead of their uses
-      const float4 *ks = reinterpret_cast<const float4 *>(smem + y0.small + L::ks) + slot * (kTile / 4);
-      const float4 *vs = reinterpret_cast<const float4 *>(smem + y0.small + L::vs) + slot * (kTile / 4);
+      const float k0 = __uint_as_float(info.z);
       const int seen = limit - (s.t0 + k) * kTile;  // positions of the tile that the row attends to
       const bool masked = nearest < (s.t0 + k + 1) * kTile || info.y != 0xFFu;
       // The loops over the tile's four pieces of 32 positions stay rolled: fully
       // unrolled, the roles' code does not fit the instruction caches, and
       // fetching it bounds the kernel.
       //
-      // ---- the row's largest t = S ks; with factors per position, t replaces S
-      // (-inf where the row does not attend)
+      // ---- the row's largest t = S 2^-eb (masked scores become -inf in place)
       float top = -INFINITY;
-      const float k0 = KS ? 1.f : ks[0].x;
       auto largest = [&](auto tag) {
         constexpr bool MASK = decltype(tag)::value;
         float t0 = -INFINITY, t1 = -INFINITY;
@@ -866,38 +920,21 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
         for (int cc = 0; cc < kTile / 32; ++cc) {
           uint32_t w[32];
           tmem_ld32(S + 32 * cc, w);
-          const float4 *const f = ks + 8 * cc;
           tmem_wait_ld(w);
-          float y[32];
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            if constexpr (KS) {
-              const float4 g = f[e / 4];
-              mul_f32x2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]), g.x, g.y, y[e], y[e + 1]);
-              mul_f32x2(__uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]), g.z, g.w, y[e + 2], y[e + 3]);
-            } else {
-#pragma unroll
-              for (int d = 0; d < 4; ++d) y[e + d] = __uint_as_float(w[e + d]);
-            }
-          }
           if constexpr (MASK) {
             const uint32_t in = info.y >> (2 * cc);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (32 * cc + e >= seen || !((in >> (e / kBlockSize)) & 1u)) y[e] = -INFINITY;
+              if (32 * cc + e >= seen || !((in >> (e / kBlockSize)) & 1u)) w[e] = 0xFF800000u;
+            tmem_st32(S + 32 * cc, w);
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            t0 = max3(t0, y[e], y[e + 1]);
-            t1 = max3(t1, y[e + 2], y[e + 3]);
-          }
-          if constexpr (KS || MASK) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(y[e]);
-            tmem_st32(S + 32 * cc, w);
+            t0 = max3(t0, __uint_as_float(w[e]), __uint_as_float(w[e + 1]));
+            t1 = max3(t1, __uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]));
           }
         }
-        if constexpr (KS || MASK) tmem_wait_st();
+        if constexpr (MASK) tmem_wait_st();
         top = fmaxf(t0, t1) * k0;
       };
       if (masked) largest(std::true_type{}); else largest(std::false_type{});
@@ -925,18 +962,17 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
         huge = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m * c) > 0x1p10f);
       }
       begun = true;
-      // ---- p = 2^(z - m): plainly t c - RN(m c) in one FMA; beyond |m c| = 2^10
-      // the rounding of m c would show in the exponent, so the careful form
-      // takes (t - m) c
+      // ---- p = 2^(z - m + 8): plainly t c - RN(m c - 8) in one FMA; beyond
+      // |m c| = 2^10 the rounding of m c would show in the exponent, so the
+      // careful form takes (t - m) c + 8
       auto exponentials = [&](auto tag) {
         constexpr bool careful = decltype(tag)::value;
-        const float ref = m == -INFINITY ? 0.f : m, mu = -ref * c, ck = c * k0;
+        const float ref = m == -INFINITY ? 0.f : m, mu = kBias - ref * c, ck = c * k0;
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll 1
         for (int cc = 0; cc < kTile / 32; ++cc) {
           uint32_t w[32];
           tmem_ld32(S + 32 * cc, w);
-          const float4 *const f = vs + 8 * cc;
           tmem_wait_ld(w);
           uint32_t P[16];
 #pragma unroll
@@ -944,10 +980,10 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
             float a0 = __uint_as_float(w[e]), a1 = __uint_as_float(w[e + 1]), a2 = __uint_as_float(w[e + 2]),
                   a3 = __uint_as_float(w[e + 3]);
             if constexpr (careful) {
-              a0 = (a0 * k0 - ref) * c;
-              a1 = (a1 * k0 - ref) * c;
-              a2 = (a2 * k0 - ref) * c;
-              a3 = (a3 * k0 - ref) * c;
+              a0 = (a0 * k0 - ref) * c + kBias;
+              a1 = (a1 * k0 - ref) * c + kBias;
+              a2 = (a2 * k0 - ref) * c + kBias;
+              a3 = (a3 * k0 - ref) * c + kBias;
             } else {
               fma_f32x2(a0, a1, ck, ck, mu, mu, a0, a1);
               fma_f32x2(a2, a3, ck, ck, mu, mu, a2, a3);
@@ -958,11 +994,6 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
             a3 = fast_exp2(a3);
             add_f32x2(s0, s1, a0, a1, s0, s1);
             add_f32x2(s2, s3, a2, a3, s2, s3);
-            if constexpr (VS) {
-              const float4 g = f[e / 4];
-              mul_f32x2(a0, a1, g.x, g.y, a0, a1);
-              mul_f32x2(a2, a3, g.z, g.w, a2, a3);
-            }
             P[e / 2] = f32x2_to_f16x2(a0, a1);
             P[e / 2 + 1] = f32x2_to_f16x2(a2, a3);
           }
@@ -1008,7 +1039,7 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
       wait(B_O, seg & 1);
       __syncwarp();
     }
-    if (live) *reinterpret_cast<float2 *>(a.ws_ml + (slot0 + r) * 2) = make_float2(m == -INFINITY ? m : m * c, l);
+    if (live) *reinterpret_cast<float2 *>(a.ws_ml + (slot0 + r) * 2) = make_float2(m == -INFINITY ? m : m * c - kBias, l);
     x += tiles;
     n0 += tiles;
   }
@@ -1029,29 +1060,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (cta >= P) return;
   const int x = static_cast<int>(cta * T / P), x1 = static_cast<int>((cta + 1) * T / P);
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[B_KFULL + i], 4);
-      mbar_init(&bars[B_KEMPTY + i], 1);
-      mbar_init(&bars[B_VFULL + i], 4);
-      mbar_init(&bars[B_VEMPTY + i], 1);
-      mbar_init(&bars[B_S + i], 1);
-      mbar_init(&bars[B_P + i], 4);
-      mbar_init(&bars[B_O + i], 1);
-      mbar_init(&bars[B_META + i], 1);
-    }
-    mbar_init(&bars[B_Q], 8);
-    mbar_init(&bars[B_END], 1);
-    for (int i = 0; i < 2 * kMaxUnits; ++i) {
-      mbar_init(&bars[B_FULL + i], 1);
-      mbar_init(&bars[B_EMPTY + i], 4);
+  uint32_t *const tm = reinterpret_cast<uint32_t *>(smem + y.small + L::tmem);
+  Segment *const first = reinterpret_cast<Segment *>(smem + y.small + L::segment);
+  if (warp == kLoadWarp) {
+    // arrivals per phase: 4 for a warpgroup's warps, 8 for B_Q, 2 for B_META, else 1
+    for (int i = threadIdx.x & 31; i < B_COUNT; i += 32) {
+      const bool four = (i >= B_KFULL && i < B_KFULL + 2) || (i >= B_VFULL && i < B_VFULL + 2) || (i >= B_P && i < B_P + 2) ||
+                        i >= B_EMPTY;
+      const bool two = i >= B_META && i < B_META + 2;
+      mbar_init(&bars[i], i == B_Q ? 8 : four ? 4 : two ? 2 : 1);
     }
     mbar_init_fence();
-    prefetch_tensormap(&kmap);
-    prefetch_tensormap(&vmap);
+    if (threadIdx.x % 32 == 0) {
+      prefetch_tensormap(&kmap);
+      prefetch_tensormap(&vmap);
+      *reinterpret_cast<volatile uint32_t *>(tm + 1) = 0;
+    }
   }
-  uint32_t *const tm = reinterpret_cast<uint32_t *>(smem + y.small + L::tmem);
-  if (threadIdx.x == 32) *reinterpret_cast<volatile uint32_t *>(tm + 1) = 0;
+  if (threadIdx.x == 32 * kScaleWarp) {
+    Segment s;
+    find_segment(a, x, x1, &s);
+    *first = s;
+  }
   __syncwarp();
   if (warp == kMmaWarp) tmem_alloc(smem_u32(tm), 512);
   tmem_fence_before();
@@ -1060,13 +1090,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tm);
 
   const Waiter wait = {bars, tm + 1, a.err};
+  const Segments sg = {first, x};
   const int tiles = x1 - x;
   const bool chan = kf == K_INT8_CHAN || kf == K_INT2_CHAN, group = vf == V_INT4_G32 || vf == V_INT2_G32;
   if (warp >= kSoftmaxWarp) {
-    if (!chan && !group) softmax_role<D, true, true>(a, smem, y, wait, tmem, x, x1);
-    else if (!chan) softmax_role<D, true, false>(a, smem, y, wait, tmem, x, x1);
-    else if (!group) softmax_role<D, false, true>(a, smem, y, wait, tmem, x, x1);
-    else softmax_role<D, false, false>(a, smem, y, wait, tmem, x, x1);
+    softmax_role<D>(a, smem, y, wait, tmem, sg, x, x1);
   } else if (warp >= kVWarp) {
     if (vf == V_INT8_TOK) convert_v_role<D, V_INT8_TOK>(base, y, wait, tiles);
     else if (vf == V_FP8_TOK) convert_v_role<D, V_FP8_TOK>(base, y, wait, tiles);
@@ -1079,14 +1107,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (kf == K_INT4_TOK) convert_k_role<D, K_INT4_TOK>(base, y, wait, tiles);
     else if constexpr (D == 128) convert_k_role<D, K_INT2_CHAN>(base, y, wait, tiles);
   } else if (warp == kMmaWarp) {
-    product_role<D>(a, base, wait, tmem, x, x1);
+    product_role<D>(a, base, wait, tmem, sg, x, x1);
   } else if (warp == kLoadWarp) {
-    load_role(a, &kmap, &vmap, krow, vrow, base, y, wait, x, x1);
+    load_role(a, &kmap, &vmap, krow, vrow, base, y, wait, sg, x, x1);
   } else if (warp == kScaleWarp) {
-    if (chan && group) scale_role<D, true, true>(a, base, y, wait, x, x1);
-    else if (chan) scale_role<D, true, false>(a, base, y, wait, x, x1);
-    else if (group) scale_role<D, false, true>(a, base, y, wait, x, x1);
-    else scale_role<D, false, false>(a, base, y, wait, x, x1);
+    const int top = top_exponent(kf == K_FP8_TOK ? C_FP8 : C_INT8);
+    if (kf == K_INT2_CHAN) scale_k_role<D, true, false>(a, base, y, wait, sg, top, x, x1);
+    else if (chan) scale_k_role<D, true, true>(a, base, y, wait, sg, top, x, x1);
+    else scale_k_role<D, false, true>(a, base, y, wait, sg, top, x, x1);
+  } else {
+    const int top = top_exponent(vf == V_FP8_TOK ? C_FP8 : C_INT8);
+    if (vf == V_INT2_G32) scale_v_role<D, true, false>(a, base, y, wait, sg, top, x, x1);
+    else if (group) scale_v_role<D, true, true>(a, base, y, wait, sg, top, x, x1);
+    else scale_v_role<D, false, true>(a, base, y, wait, sg, top, x, x1);
   }
   __syncwarp();
   tmem_fence_before();
