@@ -1,6 +1,7 @@
 // The C ABI of libkvq (declared in include/kvq.h): argument checks, format
 // decoding, tensor-map encoding and kernel launches.  Nothing here computes
 // on the host; every step of the path runs in the kernels.
+#include <algorithm>
 #include <mutex>
 #include <unordered_map>
 
@@ -719,6 +720,10 @@ int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
   if (static_cast<int64_t>(batch) * max_blocks_per_seq >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   if (fmt->num_blocks < 1 || fmt->num_blocks >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   const int H = fmt->num_kv_heads, D = fmt->head_dim, G = num_q_heads / H;
+  // Tiles count in 32 bits: a group has nseq * G / 256 row blocks, rounded up,
+  // for each kv head, so with two sequences or more in it fewer than nseq.
+  const int64_t prefix_blocks = std::min<int64_t>(max_blocks_per_seq, max_prefix_len / kBlockSize);
+  if (static_cast<int64_t>(batch) * H * ((prefix_blocks + 7) / 8) >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   const PrefixWs wl = prefix_ws(batch, num_q_heads, H, D, num_groups, plan.max_ctas, sms);
   if (workspace_bytes < wl.total) return KVQ_ERR_WORKSPACE;
   unsigned int *err = nullptr;
@@ -759,7 +764,8 @@ int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
   p.G = G;
   p.groups = num_groups;
   p.max_blocks = max_blocks_per_seq;
-  p.max_ctx = max_context_len;
+  const int64_t held = static_cast<int64_t>(max_blocks_per_seq) * kBlockSize + (tail ? kBlockSize - 1 : 0);
+  p.ctx_cap = held < max_context_len ? static_cast<int>(held) : max_context_len;
   p.max_prefix = max_prefix_len;
   p.nctas = sms;
   p.sfx_nctas = plan.max_ctas;

@@ -152,8 +152,8 @@ struct PrefixGroup {
   int lead;              // the sequence whose table holds all shared blocks
   int row_blocks, rows;  // row blocks, and rows in each (the last may have fewer)
   int tiles, slots;      // tiles of a unit, and its row slots
-  int64_t tile0;         // tiles of the groups before
-  int64_t row0;          // row slots of the groups before
+  int tile0;             // tiles of the groups before (< 2^31 in all, the host has checked)
+  int row0;              // row slots of the groups before (<= 2 batch * num_q_heads in all)
 };
 struct PrefixArgs {
   const uint16_t *q;             // BF16 [B, Hq, D]
@@ -172,7 +172,8 @@ struct PrefixArgs {
   uint16_t *out;                 // BF16 [B, Hq, D]
   unsigned int *err;
   int64_t num_blocks;
-  int B, Hq, H, G, groups, max_blocks, max_ctx, max_prefix;
+  int B, Hq, H, G, groups, max_blocks, max_prefix;
+  int ctx_cap;                   // largest valid context
   int nctas;                     // CTAs of the prefix kernel
   int sfx_nctas, sfx_blocks_per_cta;
   int rot;

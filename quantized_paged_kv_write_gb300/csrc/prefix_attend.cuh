@@ -123,11 +123,9 @@ enum Bar : int {
 };
 static_assert(B_COUNT <= 56, "mbarriers");
 
-// The part of a unit that this CTA works on.  Tiles count in 32 bits: with
-// batch * max_blocks_per_seq < 2^31 and two sequences or more in a group there
-// are fewer than 2^31 of them.  Out of line, like all that runs once a segment:
-// the roles of an SM's warps share its instruction caches, and the code of the
-// steps has to stay there.
+// The part of a unit that this CTA works on.  Out of line, like all that runs
+// once a segment: the roles of an SM's warps share its instruction caches, and
+// the code of the steps has to stay there.
 struct Segment {
   PrefixGroup g;
   int u, h, rb, t0, t1;
@@ -142,7 +140,7 @@ __device__ __noinline__ void find_segment(const PrefixArgs &a, int x, int x1, Se
   }
   Segment s;
   s.g = a.ws_groups[lo];
-  const int y = x - static_cast<int>(s.g.tile0);
+  const int y = x - s.g.tile0;
   s.u = y / s.g.tiles;
   s.t0 = y - s.u * s.g.tiles;
   s.t1 = min(s.g.tiles, s.t0 + (x1 - x));
@@ -1010,8 +1008,7 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
     }
     // ---- the unit's partial state: ml by row, O as [D / 4][rows][4], so that the
     // lanes' 16-byte stores are consecutive
-    const int64_t slot0 = s.g.row0 + static_cast<int64_t>(s.u) * s.g.slots + static_cast<int64_t>(blockIdx.x) * kPrefixRows +
-                          (s.two ? 0 : wg * s.g.rows);
+    const int64_t slot0 = s.g.row0 + s.u * s.g.slots + static_cast<int>(blockIdx.x) * kPrefixRows + (s.two ? 0 : wg * s.g.rows);
     if (begun) {
       wait(B_O + wg, no & 1);
       __syncwarp();
@@ -1055,10 +1052,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + y.small + L::bars);
   const uint32_t base = smem_u32(smem);
   const int warp = threadIdx.x >> 5;
-  const int64_t T = a.ws_groups[a.groups].tile0;
-  const int P = a.ws_groups[a.groups].tiles, cta = blockIdx.x;
+  const int T = a.ws_groups[a.groups].tile0, P = a.ws_groups[a.groups].tiles, cta = blockIdx.x;
   if (cta >= P) return;
-  const int x = static_cast<int>(cta * T / P), x1 = static_cast<int>((cta + 1) * T / P);
+  // c T / P in 32 bits
+  const int whole = T / P, rest = T - whole * P;
+  const int x = cta * whole + cta * rest / P, x1 = (cta + 1) * whole + (cta + 1) * rest / P;
 
   uint32_t *const tm = reinterpret_cast<uint32_t *>(smem + y.small + L::tmem);
   Segment *const first = reinterpret_cast<Segment *>(smem + y.small + L::segment);

@@ -12,6 +12,8 @@
 //
 // Three steps around the suffix's split decode: the plan (what is shared, and
 // the list of work), the prefix attention, and the merge.
+#include <limits.h>
+
 #include <atomic>
 
 #include "prefix_attend.cuh"
@@ -19,147 +21,135 @@
 namespace kvq {
 namespace {
 
+// The plan and the merge run once a call, in microseconds.  What they cost is
+// first of all fetching their code (it left the instruction caches while the
+// prefix kernel ran): loops stay rolled, sums are in 32 bits, divisions few.
+
+// The CTA of P that holds item x of T shared out as [c T / P, (c + 1) T / P):
+// floor(((x + 1) P - 1) / T) by a reciprocal that is off by less than one.
+__device__ __noinline__ int cta_of(int x, int T, int P) {
+  const unsigned long long n = (static_cast<unsigned long long>(x) + 1) * static_cast<unsigned>(P) - 1;
+  unsigned q = static_cast<unsigned>(static_cast<float>(n) * __frcp_rn(static_cast<float>(T)));
+  if (static_cast<unsigned long long>(q) * static_cast<unsigned>(T) > n) --q;
+  if (static_cast<unsigned long long>(q + 1) * static_cast<unsigned>(T) <= n) ++q;
+  return min(static_cast<int>(q), P - 1);
+}
+
 // ---------------------------------------------------------------------------
 // plan
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 
-// A sequence's context if it is valid, else 0 (the split decode's rule).
-__device__ __forceinline__ int valid_ctx(const PrefixArgs &a, int b, bool &bad) {
-  const int c = __ldg(a.ctx + b);
-  const int64_t cap = static_cast<int64_t>(a.max_blocks) * kBlockSize + (a.res_k != nullptr ? kBlockSize - 1 : 0);
-  bad = c < 0 || c > cap || c > a.max_ctx;
-  return bad ? 0 : c;
-}
-
+// One CTA: a chain of dependent loads and a few barriers.  The records of up to
+// kPlanGroups groups stay in shared memory between the steps.
+constexpr int kPlanGroups = 256;
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixArgs a) {
-  __shared__ long long wt[kPlanThreads / 32], wr[kPlanThreads / 32];
-  __shared__ int wn[kPlanThreads / 32];
+  __shared__ PrefixGroup sh[kPlanGroups];
+  __shared__ int2 sums[kPlanThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  PrefixGroup *const rec = a.groups <= kPlanGroups ? sh : a.ws_groups;
+  // a sequence's context if it is valid, else 0 (the split decode's rule)
+  auto context = [&](int b) {
+    const int c = __ldg(a.ctx + b);
+    return c < 0 || c > a.ctx_cap ? 0 : c;
+  };
   // ---- per group: how far its sequences share, and who holds the blocks
+  bool order = true;
+#pragma unroll 1
   for (int g = warp; g < a.groups; g += kPlanThreads / 32) {
-    const int st = __ldg(a.group_starts + g), en = __ldg(a.group_starts + g + 1);
-    const int pl = __ldg(a.prefix_lens + g);
-    const bool range = st >= 0 && en >= st && en <= a.B;
-    const bool len = pl >= 0 && pl <= a.max_prefix;
-    int best = -1, lead = 0;
-    if (range) {
+    const int st = __ldg(a.group_starts + g), en = __ldg(a.group_starts + g + 1), pl = __ldg(a.prefix_lens + g);
+    const bool range = st >= 0 && en >= st && en <= a.B, len = pl >= 0 && pl <= a.max_prefix;
+    order = order && range;
+    if (!len && lane == 0) set_error(a.err, KVQ_DEVERR_CONTEXT_RANGE);
+    // the longest context, and the first sequence that has it
+    int best = 0, lead = st;
+    if (range)
+#pragma unroll 1
       for (int b = st + lane; b < en; b += 32) {
-        bool bad;
-        const int c = valid_ctx(a, b, bad);
+        const int c = context(b);
         if (c > best) {
           best = c;
           lead = b;
         }
       }
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      const int c = __shfl_xor_sync(0xffffffffu, best, o), l = __shfl_xor_sync(0xffffffffu, lead, o);
-      if (c > best || (c == best && l < lead)) {
-        best = c;
-        lead = l;
-      }
-    }
+    const int most = __reduce_max_sync(0xffffffffu, best);
+    lead = __reduce_min_sync(0xffffffffu, best == most ? lead : INT_MAX);
     if (lane == 0) {
-      if (!range) set_error(a.err, KVQ_DEVERR_GROUP_RANGE);
-      if (!len) set_error(a.err, KVQ_DEVERR_CONTEXT_RANGE);
+      // no further than the longest sequence: past it nothing was written; a
+      // prefix of one sequence is that sequence's own
+      const int S = range && len && en - st >= 2 ? min(pl, most) / kBlockSize * kBlockSize : 0;
+      const int R = S > 0 ? (en - st) * a.G : 0;
       PrefixGroup r;
       r.start = st;
-      r.nseq = range ? en - st : 0;
-      // no further than the longest sequence: past it nothing was written
-      r.shared = range && len ? max(0, min(pl, best)) / kBlockSize * kBlockSize : 0;
+      r.nseq = S > 0 ? en - st : 0;
+      r.shared = S;
       r.lead = lead;
-      a.ws_groups[g] = r;
+      r.row_blocks = (R + kPrefixRows - 1) / kPrefixRows;
+      r.rows = R > kPrefixRows ? (R + r.row_blocks - 1) / r.row_blocks : R;
+      r.tiles = (S + kPrefixTile - 1) / kPrefixTile;
+      r.slots = r.rows > kPrefixRows / 2 ? r.rows : 2 * r.rows;
+      r.tile0 = r.row0 = 0;
+      rec[g] = r;
     }
   }
-  __syncthreads();
+  // groups out of order or range may overlap: then nothing is shared
+  const bool none = __syncthreads_or(!order);
+  if (none && threadIdx.x == 0) set_error(a.err, KVQ_DEVERR_GROUP_RANGE);
   // ---- the list of work
-  long long t0 = 0, r0 = 0;
-  int n0 = 0;
+  int t0 = 0, r0 = 0;
+#pragma unroll 1
   for (int base = 0; base < a.groups; base += kPlanThreads) {
     const int g = base + threadIdx.x;
     PrefixGroup r = {};
-    if (g < a.groups) r = a.ws_groups[g];
-    // groups that overlap earlier ones (starts out of order) share nothing:
-    // the sequences counted so far never exceed the batch
-    int in = r.nseq;
-#pragma unroll
+    if (g < a.groups) r = rec[g];
+    if (none) r.nseq = r.shared = r.row_blocks = r.tiles = 0;
+    const int t = r.row_blocks * a.H * r.tiles, s = r.row_blocks * a.H * r.slots;
+    int it = t, is = s;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, in, o);
-      if (lane >= o) in += x;
-    }
-    if (lane == 31) wn[warp] = in;
-    __syncthreads();
-    int nb = n0;
-    for (int w = 0; w < warp; ++w) nb = min(a.B + 1, nb + wn[w]);
-    if (static_cast<long long>(nb) + in > a.B) {
-      if (r.nseq > 0) set_error(a.err, KVQ_DEVERR_GROUP_RANGE);
-      r.nseq = 0;
-    }
-    // a prefix of one sequence is that sequence's own
-    if (r.nseq < 2 || r.shared == 0) r.nseq = r.shared = 0;
-    const int R = r.nseq * a.G;
-    r.row_blocks = (R + kPrefixRows - 1) / kPrefixRows;
-    r.rows = R > 0 ? (R + r.row_blocks - 1) / r.row_blocks : 0;
-    r.tiles = (r.shared + kPrefixTile - 1) / kPrefixTile;
-    r.slots = r.rows > kPrefixRows / 2 ? r.rows : 2 * r.rows;
-    const long long units = static_cast<long long>(r.row_blocks) * a.H;
-    long long it = units * r.tiles, ir = units * r.slots;
-    const long long t = it, rr = ir;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, it, o), y = __shfl_up_sync(0xffffffffu, ir, o);
+      const int x = __shfl_up_sync(0xffffffffu, it, o), y = __shfl_up_sync(0xffffffffu, is, o);
       if (lane >= o) {
         it += x;
-        ir += y;
+        is += y;
       }
     }
-    if (lane == 31) {
-      wt[warp] = it;
-      wr[warp] = ir;
-    }
+    if (lane == 31) sums[warp] = make_int2(it, is);
     __syncthreads();
-    long long bt = t0, br = r0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-      if (w == warp) {
-        bt = t0;
-        br = r0;
-      }
-      t0 += wt[w];
-      r0 += wr[w];
-      n0 = min(a.B + 1, n0 + wn[w]);
+    const int2 w = sums[lane];  // every warp sums the warps' totals for itself
+    const bool before = lane < warp;
+    r.tile0 = t0 + it - t + __reduce_add_sync(0xffffffffu, before ? w.x : 0);
+    r.row0 = r0 + is - s + __reduce_add_sync(0xffffffffu, before ? w.y : 0);
+    t0 += __reduce_add_sync(0xffffffffu, w.x);
+    r0 += __reduce_add_sync(0xffffffffu, w.y);
+    if (g < a.groups) {
+      rec[g] = r;
+      if (rec == sh) a.ws_groups[g] = r;
     }
-    r.tile0 = bt + it - t;
-    r.row0 = br + ir - rr;
-    if (g < a.groups) a.ws_groups[g] = r;
     __syncthreads();
   }
   if (threadIdx.x == 0) {
     PrefixGroup r = {};
     r.tile0 = t0;
-    r.tiles = static_cast<int>(min(static_cast<long long>(a.nctas), t0));
+    r.tiles = min(a.nctas, t0);
     a.ws_groups[a.groups] = r;
   }
-  __syncthreads();
   // ---- per sequence: where the prefix ends and the suffix begins
+#pragma unroll 1
   for (int b = threadIdx.x; b < a.B; b += kPlanThreads) {
+    // the last group that starts at or before b
     int lo = 0, hi = a.groups;
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(a.group_starts + mid) <= b) lo = mid; else hi = mid;
+      if (rec[mid].start <= b) lo = mid; else hi = mid;
     }
     int g = -1, S = 0;
-    if (a.groups > 0) {
-      const PrefixGroup &r = a.ws_groups[lo];
-      if (r.nseq > 0 && b >= r.start && b < r.start + r.nseq) {
-        g = lo;
-        S = r.shared;
-      }
+    if (a.groups > 0 && b >= rec[lo].start && b < rec[lo].start + rec[lo].nseq) {
+      g = lo;
+      S = rec[lo].shared;
     }
-    bool bad;
-    const int c = valid_ctx(a, b, bad);
-    if (bad) set_error(a.err, KVQ_DEVERR_CONTEXT_RANGE);
+    const int raw = __ldg(a.ctx + b), c = context(b);
+    if (raw != c) set_error(a.err, KVQ_DEVERR_CONTEXT_RANGE);
     const int cached = a.res_k != nullptr ? c / kBlockSize * kBlockSize : c;
     a.ws_group[b] = g;
     a.ws_limit[b] = min(cached, S);
@@ -174,170 +164,190 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
 // ---------------------------------------------------------------------------
 // A CTA merges kMergeRows rows of one kv head (row = sequence * G + query head
 // of the group, as the units count them); a thread has 4 channels of a row, so
-// the rows' 16-byte pieces of a partial are consecutive in memory.  Bound by the
-// latency of the partials in L2 (up to ~40 of them for a row): eight are in
-// flight at a time.
+// the rows' 16-byte pieces of a partial are consecutive in memory, and every
+// SPLIT-th partial.  Bound by the latency of the partials in L2 (up to ~46 of
+// them for a row), so U are in flight in each thread, nothing branches around a
+// load (that would end in a wait for it), and few rows are split further.
 constexpr int kMergeRows = 8;
 
-template <int D>
-__global__ void __launch_bounds__(kMergeRows *D / 4) prefix_merge_kernel(const PrefixArgs a) {
-  constexpr int CG = D / 4;  // channel groups
-  constexpr int U = 8;
-  __shared__ float sh[kMergeRows][D + 4];
-  const int rl = threadIdx.x % kMergeRows, cg = threadIdx.x / kMergeRows;
-  const int h = blockIdx.x % a.H, row = blockIdx.x / a.H * kMergeRows + rl;
-  const bool live = row < a.B * a.G;
-  const int b = live ? row / a.G : 0, gq = live ? row % a.G : 0;
+// A row's running state, four channels of it.
+struct RowState {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void raise(float mn) {  // mn >= m, finite
+    const float keep = fast_exp2(m - mn);
+    m = mn;
+    l *= keep;
+    o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
+  }
+  // a state with reference mp <= m; one without weight (-inf: a warpgroup that
+  // had no tile, a row masked there) holds no output
+  __device__ __forceinline__ void add(float mp, float lp, float4 v) {
+    const float w = fast_exp2(mp - m);
+    if (mp == -INFINITY) v = make_float4(lp = 0.f, 0.f, 0.f, 0.f);
+    l = fmaf(w, lp, l);
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+};
 
-  // ---- where the row's partials are: prefix (CTA c of its unit, one or two
-  // streams), then suffix (the split decode's)
-  int n0 = 0, streams = 1, prows = 0, n1 = 0;
-  int64_t pslot = 0, srec = 0;
-  const int gi = live ? a.ws_group[b] : -1;
-  if (gi >= 0) {
-    const PrefixGroup g = a.ws_groups[gi];
-    const int r = (b - g.start) * a.G + gq, rb = r / g.rows, u = rb * a.H + h;
-    const int T = static_cast<int>(a.ws_groups[a.groups].tile0), P = a.ws_groups[a.groups].tiles;
-    const int x0 = static_cast<int>(g.tile0) + u * g.tiles;
-    // the CTA that holds tile x of the list
-    auto cta_of = [&](int x) { return min(P - 1, static_cast<int>(((static_cast<int64_t>(x) + 1) * P - 1) / T)); };
-    const int c0 = cta_of(x0), c1 = cta_of(x0 + g.tiles - 1);
-    streams = g.slots > g.rows ? 2 : 1;
-    prows = g.rows;
-    n0 = (c1 - c0 + 1) * streams;
-    pslot = g.row0 + static_cast<int64_t>(u) * g.slots + static_cast<int64_t>(c0) * kPrefixRows;
-    srec = r % g.rows;  // (the row in its block, for now)
+// The full-precision tail of a per-channel K cache: every SPLIT-th of its nt
+// tokens, dot products summed over the row's threads.
+template <int D, int SPLIT>
+__device__ __noinline__ RowState add_tail(const PrefixArgs &a, RowState s, int b, int h, int gq, int rl, int cg, int sp, int nt) {
+  constexpr int WARPS = kMergeRows * D / 128, NT = kBlockSize / SPLIT;
+  __shared__ float sd[kBlockSize][kMergeRows][WARPS];
+  const uint2 q = *reinterpret_cast<const uint2 *>(a.q + (static_cast<int64_t>(b) * a.Hq + h * a.G + gq) * D + 4 * cg);
+  const int64_t at = (static_cast<int64_t>(b) * kBlockSize + sp) * a.H * D + h * D + 4 * cg;
+  const int step = SPLIT * a.H * D;
+#pragma unroll 4
+  for (int k = 0; k < NT; ++k) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(a.res_k + at + k * step);
+    float z = bf16lo_to_f32(q.x) * bf16lo_to_f32(w.x) + bf16hi_to_f32(q.x) * bf16hi_to_f32(w.x) +
+              bf16lo_to_f32(q.y) * bf16lo_to_f32(w.y) + bf16hi_to_f32(q.y) * bf16hi_to_f32(w.y);
+    // lanes rl, rl + 8, .. of a warp share a row; then the split's warps
+    z += __shfl_xor_sync(0xffffffffu, z, 8);
+    z += __shfl_xor_sync(0xffffffffu, z, 16);
+    if ((threadIdx.x & 31) < kMergeRows) sd[k * SPLIT + sp][rl][threadIdx.x / 32 % WARPS] = z;
   }
-  const int prow = static_cast<int>(srec);
-  const bool packed = 2 * a.G <= 8;  // suffix columns g (high) and g + G (low)
-  if (live) {
-    const int s0 = a.sfx_cum[b], s1 = a.sfx_cum[b + 1];
-    if (s1 > s0) {
-      const int total = a.sfx_cum[a.B];
-      const int P = min(a.sfx_nctas, max(1, (total + a.sfx_blocks_per_cta - 1) / a.sfx_blocks_per_cta));
-      auto cta_of = [&](int x) { return min(P - 1, static_cast<int>(((static_cast<int64_t>(x) + 1) * P - 1) / total)); };
-      const int c0 = cta_of(s0);
-      n1 = cta_of(s1 - 1) - c0 + 1;
-      srec = ((static_cast<int64_t>(b) + c0) * a.H + h) * 8 + gq;
-    }
-  }
-  auto ml_of = [&](int i) -> float2 {
-    if (i < n0) {
-      const int64_t at = pslot + static_cast<int64_t>(i / streams) * kPrefixRows + (i % streams) * prows + prow;
-      return *reinterpret_cast<const float2 *>(a.ws_ml + at * 2);
-    }
-    return *reinterpret_cast<const float2 *>(a.sfx_ml + (srec + static_cast<int64_t>(i - n0) * a.H * 8) * 2);
-  };
-  auto o_of = [&](int i) -> float4 {
-    if (i < n0) {
-      const int64_t at = pslot + static_cast<int64_t>(i / streams) * kPrefixRows + (i % streams) * prows;
-      return reinterpret_cast<const float4 *>(a.ws_o + at * D)[cg * prows + prow];
-    }
-    const float *p = a.sfx_o + (srec + static_cast<int64_t>(i - n0) * a.H * 8) * D + 4 * cg;
-    float4 v = *reinterpret_cast<const float4 *>(p);
-    if (packed) {
-      const float4 y = *reinterpret_cast<const float4 *>(p + a.G * D);
-      v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
-    }
-    return v;
-  };
-  const int n = n0 + n1;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float L = 0.f, mx = -INFINITY;
-  for (int i = 0; i < n; i += U) {
-    // a batch's largest m, then its weighted sum; partials without weight (a
-    // warpgroup that had no tile, a row masked there) hold no O
-    float2 ml[U];
+  __syncthreads();
+  const float zs = rsqrtf(static_cast<float>(D)) * kLog2e;
+#pragma unroll 1
+  for (int k = 0; k < NT; ++k) {
+    float z = 0.f;
 #pragma unroll
-    for (int k = 0; k < U; ++k) ml[k] = i + k < n ? ml_of(i + k) : make_float2(-INFINITY, 0.f);
-    float4 v[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) v[k] = i + k < n ? o_of(i + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-    float mn = mx;
-#pragma unroll
-    for (int k = 0; k < U; ++k) mn = fmaxf(mn, ml[k].x);
-    if (mn == -INFINITY) continue;
-    const float keep = exp2f(mx - mn);
-    mx = mn;
-    L *= keep;
-    acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (ml[k].x == -INFINITY) continue;
-      const float w = exp2f(ml[k].x - mn);
-      L = fmaf(w, ml[k].y, L);
-      acc.x = fmaf(w, v[k].x, acc.x);
-      acc.y = fmaf(w, v[k].y, acc.y);
-      acc.z = fmaf(w, v[k].z, acc.z);
-      acc.w = fmaf(w, v[k].w, acc.w);
+    for (int w = 0; w < WARPS; ++w) z += sd[k * SPLIT + sp][rl][w];
+    const uint2 v = *reinterpret_cast<const uint2 *>(a.res_v + at + k * step);
+    if (k * SPLIT + sp < nt) {  // (rows past the tail hold anything)
+      z *= zs;
+      s.raise(fmaxf(s.m, z));
+      s.add(z, 1.f, make_float4(bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y), bf16hi_to_f32(v.y)));
     }
   }
-  // ---- the full-precision tail of a per-channel K cache (products summed over
-  // the row's threads in shared memory)
-  if (a.res_k != nullptr) {
-    const int nt = live ? a.ws_ctx[b] % kBlockSize : 0;
-    const uint2 qw = live ? *reinterpret_cast<const uint2 *>(a.q + (static_cast<int64_t>(b) * a.Hq + h * a.G + gq) * D + 4 * cg)
-                          : make_uint2(0u, 0u);
-    const float zs = rsqrtf(static_cast<float>(D)) * kLog2e;
-    for (int t = 0; t < kBlockSize; ++t) {
-      const bool in = t < nt;
-      const int64_t at = ((static_cast<int64_t>(b) * kBlockSize + t) * a.H + h) * D + 4 * cg;
-      float dot = 0.f;
-      if (in) {
-        const uint2 k = *reinterpret_cast<const uint2 *>(a.res_k + at);
-        dot = bf16lo_to_f32(qw.x) * bf16lo_to_f32(k.x) + bf16hi_to_f32(qw.x) * bf16hi_to_f32(k.x) +
-              bf16lo_to_f32(qw.y) * bf16lo_to_f32(k.y) + bf16hi_to_f32(qw.y) * bf16hi_to_f32(k.y);
-      }
-      // lanes rl, rl + 8, .. of a warp share a row; then the warps
-#pragma unroll
-      for (int o = kMergeRows; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      __syncthreads();
-      if ((threadIdx.x & 31) < kMergeRows) sh[rl][threadIdx.x >> 5] = dot;
-      __syncthreads();
-      if (in) {
-        float z = 0.f;
-        for (int w = 0; w < kMergeRows * CG / 32; ++w) z += sh[rl][w];
-        z *= zs;
-        const uint2 v = *reinterpret_cast<const uint2 *>(a.res_v + at);
-        const float mn = fmaxf(mx, z), keep = exp2f(mx - mn), p = exp2f(z - mn);
-        mx = mn;
-        L = L * keep + p;
-        acc.x = acc.x * keep + p * bf16lo_to_f32(v.x);
-        acc.y = acc.y * keep + p * bf16hi_to_f32(v.x);
-        acc.z = acc.z * keep + p * bf16lo_to_f32(v.y);
-        acc.w = acc.w * keep + p * bf16hi_to_f32(v.y);
-      }
-    }
+  return s;
+}
+
+// Back from the rotated basis, sigma * (H o) / d: stages 1 and 2 in the thread,
+// the others between threads through shared memory (every thread of the CTA
+// comes here; split 0 has the rows).
+template <int D>
+__device__ __noinline__ float4 rotate_back(const PrefixArgs &a, float4 o, int rl, int cg, bool writes) {
+  __shared__ float4 sh[D / 4][kMergeRows];
+  float4 y = make_float4((o.x + o.y) + (o.z + o.w), (o.x - o.y) + (o.z - o.w), (o.x + o.y) - (o.z + o.w), (o.x - o.y) - (o.z - o.w));
+#pragma unroll 1
+  for (int s = 1; s < D / 4; s <<= 1) {
+    if (writes) sh[cg][rl] = y;
+    __syncthreads();
+    const float4 p = sh[cg ^ s][rl];
+    const float f = (cg & s) ? -1.f : 1.f;
+    y = make_float4(fmaf(f, y.x, p.x), fmaf(f, y.y, p.y), fmaf(f, y.z, p.z), fmaf(f, y.w, p.w));
     __syncthreads();
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
-  if (a.rot) {
-    // back from the rotated basis, sigma * (H o) / d: stages 1 and 2 in the
-    // thread, the others between threads through shared memory
-    float t0 = acc.x + acc.y, t1 = acc.x - acc.y, t2 = acc.z + acc.w, t3 = acc.z - acc.w;
-    float4 y = make_float4(t0 + t2, t1 + t3, t0 - t2, t1 - t3);
-#pragma unroll
-    for (int s = 1; s < CG; s <<= 1) {
-      *reinterpret_cast<float4 *>(&sh[rl][4 * cg]) = y;
-      __syncthreads();
-      const float4 p = *reinterpret_cast<const float4 *>(&sh[rl][4 * (cg ^ s)]);
-      const float f = (cg & s) ? -1.f : 1.f;
-      y = make_float4(fmaf(f, y.x, p.x), fmaf(f, y.y, p.y), fmaf(f, y.z, p.z), fmaf(f, y.w, p.w));
-      __syncthreads();
-    }
-    const uint32_t neg = a.rot_signs[cg >> 3] >> (4 * (cg & 7));
-    constexpr float kInvD = 1.f / D;
-    acc.x = y.x * (neg & 1u ? -kInvD : kInvD);
-    acc.y = y.y * (neg & 2u ? -kInvD : kInvD);
-    acc.z = y.z * (neg & 4u ? -kInvD : kInvD);
-    acc.w = y.w * (neg & 8u ? -kInvD : kInvD);
+  const uint32_t neg = a.rot_signs[cg >> 3] >> (4 * (cg & 7));
+  constexpr float kInvD = 1.f / D;
+  return make_float4(y.x * (neg & 1u ? -kInvD : kInvD), y.y * (neg & 2u ? -kInvD : kInvD), y.z * (neg & 4u ? -kInvD : kInvD),
+                     y.w * (neg & 8u ? -kInvD : kInvD));
+}
+
+template <int D, int SPLIT>
+__global__ void __launch_bounds__(kMergeRows *SPLIT *D / 4, 1024 / (kMergeRows * SPLIT * D / 4))
+    prefix_merge_kernel(const __grid_constant__ PrefixArgs a) {
+  constexpr int CG = D / 4;  // channel groups
+  constexpr int U = 4;
+  __shared__ float4 so[SPLIT][CG][kMergeRows];
+  __shared__ float2 sm[SPLIT][kMergeRows];
+  const int rl = threadIdx.x % kMergeRows, cg = threadIdx.x / kMergeRows % CG, sp = threadIdx.x / (kMergeRows * CG);
+  const int h = blockIdx.x % a.H, row = blockIdx.x / a.H * kMergeRows + rl;
+  const bool live = row < a.B * a.G;
+  const int b = live ? row / a.G : 0, gq = live ? row - b * a.G : 0;
+
+  // What does not depend on one another is loaded side by side.
+  const int gi = live ? a.ws_group[b] : -1, total = a.sfx_cum[a.B], s0 = a.sfx_cum[b], s1 = live ? a.sfx_cum[b + 1] : 0;
+  const int T = a.ws_groups[a.groups].tile0, P = a.ws_groups[a.groups].tiles;
+  const PrefixGroup &g = a.ws_groups[max(gi, 0)];
+
+  // ---- the row's partials, as lists of (m, l) and outputs: the prefix's first
+  // and second stream, the suffix's high and (packed: columns g and g + G) low parts
+  int n0 = 0, n1 = 0, streams = 1;
+  const float2 *pml = reinterpret_cast<const float2 *>(a.ws_ml), *sml = reinterpret_cast<const float2 *>(a.sfx_ml);
+  const float4 *po = reinterpret_cast<const float4 *>(a.ws_o), *qo = reinterpret_cast<const float4 *>(a.sfx_o);
+  int rows = 0;
+  if (gi >= 0) {
+    const int r = (b - g.start) * a.G + gq, rb = r / g.rows, u = rb * a.H + h, x0 = g.tile0 + u * g.tiles;
+    const int c0 = cta_of(x0, T, P);
+    rows = g.rows;
+    streams = g.slots > rows ? 2 : 1;
+    n0 = cta_of(x0 + g.tiles - 1, T, P) - c0 + 1;
+    const int slot = g.row0 + u * g.slots + c0 * kPrefixRows, prow = r - rb * rows;
+    pml += slot + prow;
+    po += static_cast<int64_t>(slot) * CG + cg * rows + prow;
   }
+  if (s1 > s0) {
+    const int Ps = min(a.sfx_nctas, max(1, (total + a.sfx_blocks_per_cta - 1) / a.sfx_blocks_per_cta));
+    const int c0 = cta_of(s0, total, Ps);
+    n1 = cta_of(s1 - 1, total, Ps) - c0 + 1;
+    const int64_t rec = (static_cast<int64_t>(b + c0) * a.H + h) * 8 + gq;
+    sml += rec;
+    qo += rec * CG + cg;
+  }
+  const bool packed = 2 * a.G <= 8;
+  RowState s;
+#pragma unroll 1
+  for (int list = 0; list < 4; ++list) {
+    const bool pre = list < 2, second = list & 1;
+    const int n = pre ? (second && streams < 2 ? 0 : n0) : (second && !packed ? 0 : n1);
+    const int step = pre ? kPrefixRows : a.H * 8;
+    const float2 *const ml = (pre ? pml : sml) + (pre && second ? rows : 0);
+    const float4 *const o = (pre ? po : qo) + (second ? (pre ? rows * CG : a.G * CG) : 0);
+    const float count = pre || !second ? 1.f : 0.f;  // (the low parts' l is the high parts')
+#pragma unroll 1
+    for (int i = sp; i < n; i += U * SPLIT) {
+      float2 w[U];
+      float4 v[U];
+      float mn = s.m;
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int e = i + k * SPLIT;
+        const int64_t at = static_cast<int64_t>(min(e, n - 1)) * step;
+        w[k] = ml[at];
+        v[k] = o[at * CG];
+        if (e >= n) w[k].x = -INFINITY;
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) mn = fmaxf(mn, w[k].x);
+      if (mn == -INFINITY) continue;
+      s.raise(mn);
+#pragma unroll
+      for (int k = 0; k < U; ++k) s.add(w[k].x, w[k].y * count, v[k]);
+    }
+  }
+  if (a.res_k != nullptr) s = add_tail<D, SPLIT>(a, s, b, h, gq, rl, cg, sp, live ? a.ws_ctx[b] % kBlockSize : 0);
+  // ---- the splits' sums
+  if constexpr (SPLIT > 1) {
+    if (cg == 0) sm[sp][rl] = make_float2(s.m, s.l);
+    so[sp][cg][rl] = s.o;
+    __syncthreads();
+    if (sp == 0) {
+      float mn = s.m;
+#pragma unroll 1
+      for (int k = 1; k < SPLIT; ++k) mn = fmaxf(mn, sm[k][rl].x);
+      if (mn != -INFINITY) {
+        s.raise(mn);
+#pragma unroll 1
+        for (int k = 1; k < SPLIT; ++k) s.add(sm[k][rl].x, sm[k][rl].y, so[k][cg][rl]);
+      }
+    }
+  }
+  const float inv = s.l > 0.f ? __frcp_rn(s.l) : 0.f;
+  float4 o = make_float4(s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv);
+  if (a.rot) o = rotate_back<D>(a, o, rl, cg, sp == 0);
   // BF16 out, rounded once: what the output projection reads
-  if (live) {
+  if (live && sp == 0) {
     uint2 w;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(acc.y), "f"(acc.x));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(acc.w), "f"(acc.z));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(o.y), "f"(o.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(o.w), "f"(o.z));
     *reinterpret_cast<uint2 *>(a.out + (static_cast<int64_t>(b) * a.Hq + h * a.G + gq) * D + 4 * cg) = w;
   }
 }
@@ -377,10 +387,20 @@ cudaError_t launch_prefix_attend(int head_dim, int kf, int vf, const PrefixArgs 
   return head_dim == 128 ? attend<128>(kf, vf, a, m, stream) : attend<64>(kf, vf, a, m, stream);
 }
 
-cudaError_t launch_prefix_merge(int head_dim, const PrefixArgs &a, cudaStream_t stream) {
+template <int D>
+static void merge(const PrefixArgs &a, cudaStream_t stream) {
   const int n = (a.B * a.G + kMergeRows - 1) / kMergeRows * a.H;
-  if (head_dim == 128) prefix_merge_kernel<128><<<n, kMergeRows * 32, 0, stream>>>(a);
-  else prefix_merge_kernel<64><<<n, kMergeRows * 16, 0, stream>>>(a);
+  // threads for one wave of half-full SMs (64 registers): as many splits as that
+  // allows
+  const int64_t threads = static_cast<int64_t>(n) * kMergeRows * (D / 4), wave = static_cast<int64_t>(a.nctas) * 1024;
+  if (4 * threads <= wave) prefix_merge_kernel<D, 4><<<n, kMergeRows * D, 0, stream>>>(a);
+  else if (2 * threads <= wave) prefix_merge_kernel<D, 2><<<n, kMergeRows * D / 2, 0, stream>>>(a);
+  else prefix_merge_kernel<D, 1><<<n, kMergeRows * D / 4, 0, stream>>>(a);
+}
+
+cudaError_t launch_prefix_merge(int head_dim, const PrefixArgs &a, cudaStream_t stream) {
+  if (head_dim == 128) merge<128>(a, stream);
+  else merge<64>(a, stream);
   return cudaGetLastError();
 }
 
