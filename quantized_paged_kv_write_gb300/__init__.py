@@ -227,6 +227,10 @@ def _host_ptr(t: torch.Tensor, dtype, what: str) -> int:
 
 
 def _ptr(t: torch.Tensor, dtype=None, what: str = "tensor") -> int:
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == torch._C._cuda_getDevice()
+            and (dtype is None or t.dtype is dtype) and t.is_contiguous()):
+        return t.data_ptr()
+    # what is wrong with it
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch.Tensor")
     if not t.is_cuda:
@@ -245,7 +249,8 @@ def _ptr(t: torch.Tensor, dtype=None, what: str = "tensor") -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle: a Stream object costs as much as the rest of a call's marshalling
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

@@ -360,4 +360,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
 // 2^k as a float for -126 <= k <= 127.
 __device__ __forceinline__ float pow2i(int k) { return __int_as_float((k + 127) << 23); }
 
+// Kernels of one call that are launched while the one before still runs
+// (launch_overlapped): the next one may start once every CTA has released it,
+// and waits here until the one before has ended and its writes are visible.
+// Both do nothing in a kernel launched in plain stream order.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 }  // namespace kvq

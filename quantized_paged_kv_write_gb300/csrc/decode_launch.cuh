@@ -61,9 +61,14 @@ cudaError_t plan_one(int H, int B, DecodePlan *plan) {
 template <int D, int KF, int VF, bool WIDE, int HT, bool ROT>
 cudaError_t launch_one(const DecodeArgs &a, const DecodePlan &plan, const DecodeMaps &m, cudaStream_t stream) {
   if (a.nctas > 0) {
-    decode_split_kernel<D, KF, VF, WIDE, HT, ROT>
-        <<<a.nctas, plan.threads, plan.smem, stream>>>(m.k, m.v, m.vs, a, plan.nstages);
-    cudaError_t e = cudaGetLastError();
+    auto kern = decode_split_kernel<D, KF, VF, WIDE, HT, ROT>;
+    cudaError_t e;
+    if (a.overlap != 0) {
+      e = launch_overlapped(kern, a.nctas, plan.threads, plan.smem, stream, m.k, m.v, m.vs, a, plan.nstages);
+    } else {
+      kern<<<a.nctas, plan.threads, plan.smem, stream>>>(m.k, m.v, m.vs, a, plan.nstages);
+      e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return e;
   }
   if (a.split_only) return cudaSuccess;

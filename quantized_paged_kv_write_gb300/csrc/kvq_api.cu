@@ -800,9 +800,10 @@ int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
   a.blocks_per_cta = p.sfx_blocks_per_cta;
   a.split_only = true;
 
+  const bool prefix = num_groups > 0 && max_prefix_len >= kBlockSize;
+  a.overlap = prefix ? 2 : 1;
   if (launch_prefix_plan(p, s) != cudaSuccess) return KVQ_ERR_CUDA;
-  if (num_groups > 0 && max_prefix_len >= kBlockSize && launch_prefix_attend(D, kf, vf, p, maps, s) != cudaSuccess)
-    return KVQ_ERR_CUDA;
+  if (prefix && launch_prefix_attend(D, kf, vf, p, maps, s) != cudaSuccess) return KVQ_ERR_CUDA;
   if (launch_decode(D, kf, vf, a, plan, maps, s) != cudaSuccess) return KVQ_ERR_CUDA;
   return launch_prefix_merge(D, p, s) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }

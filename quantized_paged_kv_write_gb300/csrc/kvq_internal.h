@@ -59,7 +59,29 @@ struct DecodeArgs {
   const int32_t *tab_off = nullptr;
   int blocks_per_cta = 0;
   bool split_only = false;
+  // In what order it is launched: 0 plainly; 1 while the kernel before it, which
+  // writes ctx and tab_off, may still run; 2 while the kernel before it may still
+  // run, and ctx and tab_off are from an earlier one that has ended.
+  int overlap = 0;
 };
+
+// Launches kern so that it may start while the stream's kernel before it still
+// runs (that one says when, and kern waits for its results itself).
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kern)(Params...), int ctas, int threads, size_t smem, cudaStream_t stream,
+                              const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 // Launch plan of the split kernel for one shape on the current device.
 struct DecodePlan {
@@ -151,9 +173,9 @@ struct PrefixGroup {
   int shared;            // shared positions, a multiple of the block size
   int lead;              // the sequence whose table holds all shared blocks
   int row_blocks, rows;  // row blocks, and rows in each (the last may have fewer)
-  int tiles, slots;      // tiles of a unit, and its row slots
+  int tiles;             // tiles of a unit
   int tile0;             // tiles of the groups before (< 2^31 in all, the host has checked)
-  int row0;              // row slots of the groups before (<= 2 batch * num_q_heads in all)
+  int row0;              // row slots of the groups before (a unit has `rows`; <= 2 batch * num_q_heads in all)
 };
 struct PrefixArgs {
   const uint16_t *q;             // BF16 [B, Hq, D]

@@ -327,6 +327,11 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
+  // Launched before the kernel before it has ended (a.overlap): the next one may
+  // start when these CTAs have, and this grid ends after the one before, which
+  // at least one thread of every CTA waits for.
+  if (a.overlap == 1) grid_wait();
+  grid_release();
   if (threadIdx.x == 0) {
     for (int s = 0; s < nstages; ++s) {
       mbar_init(&full[s], 1);
@@ -342,7 +347,7 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
       const int b = base + lane;
       int nb = 0;
       if (b < B) {
-        const int ctx = __ldg(a.ctx + b);
+        const int ctx = __ldcg(a.ctx + b);  // (a kernel before may have just written it)
         // with a full-precision tail only the complete blocks are cached and
         // need block table entries
         const bool tail = a.res_k != nullptr;
@@ -367,14 +372,20 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
   const int c = blockIdx.x;
   int P = a.nctas;
   if (a.blocks_per_cta > 0) P = min(P, max(1, (total + a.blocks_per_cta - 1) / a.blocks_per_cta));
-  if (c >= P) return;
+  if (c >= P) {
+    grid_wait();
+    return;
+  }
   const int g0 = static_cast<int>((static_cast<int64_t>(c) * total) / P);
   const int g1 = static_cast<int>((static_cast<int64_t>(c + 1) * total) / P);
   if (c == 0) {
     // the reduce kernel reads the prefix sums from the workspace
     for (int k = threadIdx.x; k <= B; k += blockDim.x) a.ws_cum[k] = cum[k];
   }
-  if (g0 >= g1) return;
+  if (g0 >= g1) {
+    grid_wait();
+    return;
+  }
   if constexpr (!T::KCHAN) {
     if (a.knew != nullptr) {
       fused_write_new_tokens<D, KF, VF, HT, ROT>(a, cum, g0, g1, H, warp, H + 1);
@@ -399,7 +410,7 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
       int phys = -1;
       if (gl < g1) {
         const int bl = seq_of(cum, B, gl);
-        const int skip = a.tab_off != nullptr ? __ldg(a.tab_off + bl) : 0;
+        const int skip = a.tab_off != nullptr ? __ldcg(a.tab_off + bl) : 0;
         phys = __ldg(a.tables + static_cast<int64_t>(bl) * a.max_blocks + skip + (gl - cum[bl]));
       }
       const int n = min(32, g1 - base);
@@ -447,6 +458,7 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
         break;
       }
     }
+    grid_wait();
     return;
   }
   if (warp > H) return;

@@ -853,6 +853,60 @@ __device__ __noinline__ float stage_queries(const PrefixArgs &a, int from, uint3
   return c * rsqrtf(static_cast<float>(D)) * kLog2e * (ROT ? 1.f / D : 1.f);
 }
 
+// The unit's partial state: ml by row, O as [D / 4][rows][4], so that the lanes'
+// 16-byte stores are consecutive.  Two warpgroups with the same rows (one row
+// tile) join their streams here: both see both outputs in tensor memory and
+// take half of the channels each, which halves what the merge has to read.
+template <int D>
+__device__ __noinline__ void store_partial(const PrefixArgs &a, const Segment &s, uint8_t *exchange, uint32_t O, int wg, bool live,
+                                           int r, float m, float l, float back) {
+  const int rows = s.g.rows;
+  const int64_t slot = s.g.row0 + s.u * rows + static_cast<int>(blockIdx.x) * kPrefixRows;
+  float w0 = back, w1 = 0.f;  // of O and of the other stream's
+  uint32_t other = O;
+  if (s.two) {
+    O += 128 * wg;
+    other = O;
+  } else {
+    float4 *const x = reinterpret_cast<float4 *>(exchange);
+    x[128 * wg + r] = make_float4(m, l, back, 0.f);
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const float4 y0 = x[r], y1 = x[128 + r];
+    m = fmaxf(y0.x, y1.x);
+    // (a stream without weight, -inf, may have left anything in its O)
+    w0 = y0.x == -INFINITY ? 0.f : fast_exp2(y0.x - m);
+    w1 = y1.x == -INFINITY ? 0.f : fast_exp2(y1.x - m);
+    l = w0 * y0.y + w1 * y1.y;
+    w0 *= y0.z;
+    w1 *= y1.z;
+    other = O + 128;
+  }
+  const int n = s.two ? D / 16 : D / 32, c0 = s.two ? 0 : wg * (D / 32);
+#pragma unroll 1
+  for (int cc = c0; cc < c0 + n; ++cc) {
+    uint32_t u[16], v[16];
+    __syncwarp();
+    tmem_ld16(O + 16 * cc, u);
+    tmem_ld16(other + 16 * cc, v);
+    tmem_wait_ld(u);
+    tmem_wait_ld(v);
+    if (live) {
+      float4 *o = reinterpret_cast<float4 *>(a.ws_o + slot * D) + 4 * cc * rows + r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float z[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float p = __uint_as_float(u[4 * e + k]), q = __uint_as_float(v[4 * e + k]);
+          z[k] = (w0 != 0.f ? w0 * p : 0.f) + (w1 != 0.f ? w1 * q : 0.f);
+        }
+        o[e * rows] = make_float4(z[0], z[1], z[2], z[3]);
+      }
+    }
+  }
+  if (live && (s.two || wg == 0)) *reinterpret_cast<float2 *>(a.ws_ml + (slot + r) * 2) = make_float2(m, l);
+}
+
 template <int D>
 __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, const Layout &y0, const Waiter &wait,
                                              uint32_t tmem, const Segments &sg, int x, int x1) {
@@ -888,7 +942,7 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
       c = f[32 * warp + lane];
       asm volatile("bar.sync 1, 256;" ::: "memory");
     }
-    const int limit = live ? __ldg(a.ws_limit + b) : s.g.shared;
+    const int limit = live ? __ldcg(a.ws_limit + b) : s.g.shared;
     const int nearest = __reduce_min_sync(0xffffffffu, limit);
 
     float m = -INFINITY, l = 0.f;  // m as a value of t
@@ -1006,37 +1060,21 @@ __device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, co
       __syncwarp();
       if (lane == 0) mbar_arrive(&wait.bars[B_P + wg]);
     }
-    // ---- the unit's partial state: ml by row, O as [D / 4][rows][4], so that the
-    // lanes' 16-byte stores are consecutive
-    const int64_t slot0 = s.g.row0 + s.u * s.g.slots + static_cast<int>(blockIdx.x) * kPrefixRows + (s.two ? 0 : wg * s.g.rows);
     if (begun) {
       wait(B_O + wg, no & 1);
-      __syncwarp();
       ++no;
-      tmem_fence_after();
-      const float back = F == kNoScale ? 1.f : pow2i(-F);
-#pragma unroll 1
-      for (int cc = 0; cc < D / 16; ++cc) {
-        uint32_t w[16];
-        __syncwarp();
-        tmem_ld16(O + 16 * cc, w);
-        tmem_wait_ld(w);
-        if (live) {
-          float4 *o = reinterpret_cast<float4 *>(a.ws_o + slot0 * D) + 4 * cc * s.g.rows + r;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o[e * s.g.rows] = make_float4(__uint_as_float(w[4 * e]) * back, __uint_as_float(w[4 * e + 1]) * back,
-                               __uint_as_float(w[4 * e + 2]) * back, __uint_as_float(w[4 * e + 3]) * back);
-        }
-      }
-      tmem_fence_before();
     } else {
-      // one tile for two warpgroups: the other one has it.  Its end is awaited,
-      // so that no warpgroup runs a segment ahead.
+      // one tile for two warpgroups: the other one has it
       wait(B_O, seg & 1);
-      __syncwarp();
     }
-    if (live) *reinterpret_cast<float2 *>(a.ws_ml + (slot0 + r) * 2) = make_float2(m == -INFINITY ? m : m * c - kBias, l);
+    __syncwarp();
+    tmem_fence_after();
+    // The scores' products are behind either B_O too, so Q is free to be written.
+    store_partial<D>(a, s, smem + L::q, tmem + lanes + 256, wg, live, r, m == -INFINITY ? m : m * c - kBias, l,
+                     F == kNoScale ? 0.f : pow2i(-F));
+    tmem_fence_before();
+    // no warpgroup goes on while the other one reads O, or Q's place
+    if (!s.two) asm volatile("bar.sync 1, 256;" ::: "memory");
     x += tiles;
     n0 += tiles;
   }
@@ -1052,6 +1090,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + y.small + L::bars);
   const uint32_t base = smem_u32(smem);
   const int warp = threadIdx.x >> 5;
+  grid_wait();  // the plan
+  grid_release();
   const int T = a.ws_groups[a.groups].tile0, P = a.ws_groups[a.groups].tiles, cta = blockIdx.x;
   if (cta >= P) return;
   // c T / P in 32 bits

@@ -46,6 +46,7 @@ constexpr int kPlanGroups = 256;
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixArgs a) {
   __shared__ PrefixGroup sh[kPlanGroups];
   __shared__ int2 sums[kPlanThreads / 32];
+  grid_release();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   PrefixGroup *const rec = a.groups <= kPlanGroups ? sh : a.ws_groups;
   // a sequence's context if it is valid, else 0 (the split decode's rule)
@@ -87,7 +88,6 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
       r.row_blocks = (R + kPrefixRows - 1) / kPrefixRows;
       r.rows = R > kPrefixRows ? (R + r.row_blocks - 1) / r.row_blocks : R;
       r.tiles = (S + kPrefixTile - 1) / kPrefixTile;
-      r.slots = r.rows > kPrefixRows / 2 ? r.rows : 2 * r.rows;
       r.tile0 = r.row0 = 0;
       rec[g] = r;
     }
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
     PrefixGroup r = {};
     if (g < a.groups) r = rec[g];
     if (none) r.nseq = r.shared = r.row_blocks = r.tiles = 0;
-    const int t = r.row_blocks * a.H * r.tiles, s = r.row_blocks * a.H * r.slots;
+    const int t = r.row_blocks * a.H * r.tiles, s = r.row_blocks * a.H * r.rows;
     int it = t, is = s;
 #pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
@@ -263,26 +263,24 @@ __global__ void __launch_bounds__(kMergeRows *SPLIT *D / 4, 1024 / (kMergeRows *
   const bool live = row < a.B * a.G;
   const int b = live ? row / a.G : 0, gq = live ? row - b * a.G : 0;
 
+  grid_wait();
   // What does not depend on one another is loaded side by side.
   const int gi = live ? a.ws_group[b] : -1, total = a.sfx_cum[a.B], s0 = a.sfx_cum[b], s1 = live ? a.sfx_cum[b + 1] : 0;
   const int T = a.ws_groups[a.groups].tile0, P = a.ws_groups[a.groups].tiles;
   const PrefixGroup &g = a.ws_groups[max(gi, 0)];
 
-  // ---- the row's partials, as lists of (m, l) and outputs: the prefix's first
-  // and second stream, the suffix's high and (packed: columns g and g + G) low parts
-  int n0 = 0, n1 = 0, streams = 1;
+  // ---- the row's partials, as lists of (m, l) and outputs: the prefix's, the
+  // suffix's high and (packed: columns g and g + G) low parts
+  int n0 = 0, n1 = 0;
   const float2 *pml = reinterpret_cast<const float2 *>(a.ws_ml), *sml = reinterpret_cast<const float2 *>(a.sfx_ml);
   const float4 *po = reinterpret_cast<const float4 *>(a.ws_o), *qo = reinterpret_cast<const float4 *>(a.sfx_o);
-  int rows = 0;
   if (gi >= 0) {
     const int r = (b - g.start) * a.G + gq, rb = r / g.rows, u = rb * a.H + h, x0 = g.tile0 + u * g.tiles;
     const int c0 = cta_of(x0, T, P);
-    rows = g.rows;
-    streams = g.slots > rows ? 2 : 1;
     n0 = cta_of(x0 + g.tiles - 1, T, P) - c0 + 1;
-    const int slot = g.row0 + u * g.slots + c0 * kPrefixRows, prow = r - rb * rows;
+    const int slot = g.row0 + u * g.rows + c0 * kPrefixRows, prow = r - rb * g.rows;
     pml += slot + prow;
-    po += static_cast<int64_t>(slot) * CG + cg * rows + prow;
+    po += static_cast<int64_t>(slot) * CG + cg * g.rows + prow;
   }
   if (s1 > s0) {
     const int Ps = min(a.sfx_nctas, max(1, (total + a.sfx_blocks_per_cta - 1) / a.sfx_blocks_per_cta));
@@ -292,16 +290,14 @@ __global__ void __launch_bounds__(kMergeRows *SPLIT *D / 4, 1024 / (kMergeRows *
     sml += rec;
     qo += rec * CG + cg;
   }
-  const bool packed = 2 * a.G <= 8;
+  const int lists = 2 * a.G <= 8 ? 3 : 2;
   RowState s;
 #pragma unroll 1
-  for (int list = 0; list < 4; ++list) {
-    const bool pre = list < 2, second = list & 1;
-    const int n = pre ? (second && streams < 2 ? 0 : n0) : (second && !packed ? 0 : n1);
-    const int step = pre ? kPrefixRows : a.H * 8;
-    const float2 *const ml = (pre ? pml : sml) + (pre && second ? rows : 0);
-    const float4 *const o = (pre ? po : qo) + (second ? (pre ? rows * CG : a.G * CG) : 0);
-    const float count = pre || !second ? 1.f : 0.f;  // (the low parts' l is the high parts')
+  for (int list = 0; list < lists; ++list) {
+    const int n = list == 0 ? n0 : n1, step = list == 0 ? kPrefixRows : a.H * 8;
+    const float2 *const ml = list == 0 ? pml : sml;
+    const float4 *const o = list == 0 ? po : qo + (list == 2 ? a.G * CG : 0);
+    const float count = list == 2 ? 0.f : 1.f;  // (the low parts' l is the high parts')
 #pragma unroll 1
     for (int i = sp; i < n; i += U * SPLIT) {
       float2 w[U];
@@ -378,8 +374,7 @@ static cudaError_t attend(int kf, int vf, const PrefixArgs &a, const DecodeMaps 
   const int vrow = vf == V_INT4_G32 ? D / 2 : vf == V_INT2_G32 ? D / 4 : D;
   const prefix::Layout y = prefix::layout_of<D>(kf == K_INT8_CHAN || kf == K_INT2_CHAN, vf == V_INT4_G32 || vf == V_INT2_G32,
                                                 a.B * a.G > kPrefixRows / 2, krow, vrow);
-  kern<<<a.nctas, prefix::kThreads, y.bytes, stream>>>(m.k, m.v, a, y, kf, vf, krow, vrow);
-  return cudaGetLastError();
+  return launch_overlapped(kern, a.nctas, prefix::kThreads, y.bytes, stream, m.k, m.v, a, y, kf, vf, krow, vrow);
 }
 
 cudaError_t launch_prefix_attend(int head_dim, int kf, int vf, const PrefixArgs &a, const DecodeMaps &m,
@@ -388,20 +383,19 @@ cudaError_t launch_prefix_attend(int head_dim, int kf, int vf, const PrefixArgs 
 }
 
 template <int D>
-static void merge(const PrefixArgs &a, cudaStream_t stream) {
+static cudaError_t merge(const PrefixArgs &a, cudaStream_t stream) {
   const int n = (a.B * a.G + kMergeRows - 1) / kMergeRows * a.H;
   // threads for one wave of half-full SMs (64 registers): as many splits as that
   // allows
   const int64_t threads = static_cast<int64_t>(n) * kMergeRows * (D / 4), wave = static_cast<int64_t>(a.nctas) * 1024;
-  if (4 * threads <= wave) prefix_merge_kernel<D, 4><<<n, kMergeRows * D, 0, stream>>>(a);
-  else if (2 * threads <= wave) prefix_merge_kernel<D, 2><<<n, kMergeRows * D / 2, 0, stream>>>(a);
-  else prefix_merge_kernel<D, 1><<<n, kMergeRows * D / 4, 0, stream>>>(a);
+  constexpr int kOne = kMergeRows * D / 4;
+  if (4 * threads <= wave) return launch_overlapped(prefix_merge_kernel<D, 4>, n, 4 * kOne, 0, stream, a);
+  if (2 * threads <= wave) return launch_overlapped(prefix_merge_kernel<D, 2>, n, 2 * kOne, 0, stream, a);
+  return launch_overlapped(prefix_merge_kernel<D, 1>, n, kOne, 0, stream, a);
 }
 
 cudaError_t launch_prefix_merge(int head_dim, const PrefixArgs &a, cudaStream_t stream) {
-  if (head_dim == 128) merge<128>(a, stream);
-  else merge<64>(a, stream);
-  return cudaGetLastError();
+  return head_dim == 128 ? merge<128>(a, stream) : merge<64>(a, stream);
 }
 
 }  // namespace kvq
