@@ -769,7 +769,7 @@ int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
   p.max_prefix = max_prefix_len;
   p.nctas = sms;
   p.sfx_nctas = plan.max_ctas;
-  p.sfx_blocks_per_cta = 4;
+  p.sfx_blocks_per_cta = 1;
   p.rot = fmt->rotation;
   for (int w = 0; w < 4; ++w) p.rot_signs[w] = fmt->rotation_signs[w];
 

@@ -339,31 +339,42 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
     }
     mbar_init_fence();
   }
-  // block counts per sequence (invalid contexts count as empty)
+  // block counts per sequence (invalid contexts count as empty); eight loads of
+  // a lane in flight, as their latency is most of a short call's start
   if (warp == 0) {
+    constexpr int U = 8;
     int carry = 0;
     if (lane == 0) cum[0] = 0;
-    for (int base = 0; base < B; base += 32) {
-      const int b = base + lane;
-      int nb = 0;
-      if (b < B) {
-        const int ctx = __ldcg(a.ctx + b);  // (a kernel before may have just written it)
-        // with a full-precision tail only the complete blocks are cached and
-        // need block table entries
-        const bool tail = a.res_k != nullptr;
-        const bool bad = ctx < 0 || (tail ? ctx / kBlockSize > a.max_blocks : ctx > a.max_blocks * kBlockSize) ||
-                         ctx > a.max_ctx;
-        if (bad && blockIdx.x == 0) set_error(a.err, KVQ_DEVERR_CONTEXT_RANGE);
-        nb = bad ? 0 : (tail ? ctx / kBlockSize : (ctx + kBlockSize - 1) / kBlockSize);
-      }
-      int v = nb;
+    for (int base = 0; base < B; base += 32 * U) {
+      int cl[U];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += n;
+      for (int u = 0; u < U; ++u)
+        cl[u] = __ldcg(a.ctx + min(base + 32 * u + lane, B - 1));  // (a kernel before may have just written it)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int b = base + 32 * u + lane;
+        int nb = 0;
+        if (b < B) {
+          const int ctx = cl[u];
+          // with a full-precision tail only the complete blocks are cached and
+          // need block table entries
+          const bool tail = a.res_k != nullptr;
+          const bool bad = ctx < 0 || (tail ? ctx / kBlockSize > a.max_blocks : ctx > a.max_blocks * kBlockSize) ||
+                           ctx > a.max_ctx;
+          if (bad && blockIdx.x == 0) set_error(a.err, KVQ_DEVERR_CONTEXT_RANGE);
+          nb = bad ? 0 : (tail ? ctx / kBlockSize : (ctx + kBlockSize - 1) / kBlockSize);
+        }
+        if (base + 32 * u < B) {
+          int v = nb;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += n;
+          }
+          if (b < B) cum[b + 1] = carry + v;
+          carry += __shfl_sync(0xffffffffu, v, 31);
+        }
       }
-      if (b < B) cum[b + 1] = carry + v;
-      carry += __shfl_sync(0xffffffffu, v, 31);
     }
   }
   __syncthreads();
