@@ -39,8 +39,8 @@ namespace prefix {
 constexpr int kTile = kPrefixTile;             // positions per tile
 constexpr int kTileBlocks = kTile / kBlockSize;
 // Warps by role: the single-warp roles, which everybody waits for, come first.
-constexpr int kMmaWarp = 0, kLoadWarp = 1, kScaleWarp = 2, kKWarp = 4, kVWarp = 8, kSoftmaxWarp = 12;
-constexpr int kThreads = 20 * 32;
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kScaleWarp = 2, kKWarp = 4, kVWarp = 8, kSoftmaxWarp = 12, kLoadVWarp = 20;
+constexpr int kThreads = 21 * 32;
 constexpr uint32_t kPair = 4096;               // codes that a converter warpgroup takes in one turn
 constexpr int kMaxUnits = 8;                   // per ring
 constexpr uint32_t kMaxSmem = 227 * 1024;
@@ -331,7 +331,7 @@ struct ScalePair {
 };
 
 template <int D, int KF>
-__device__ __noinline__ void convert_k_role(uint32_t base, const Layout &y, const Waiter &wait, int tiles) {
+__device__ __forceinline__ void convert_k_role(uint32_t base, const Layout &y, const Waiter &wait, int tiles) {
   using L = Smem<D>;
   using KC = KCode<KF>;
   using F = Cover<D, KC::code>;
@@ -367,7 +367,7 @@ __device__ __noinline__ void convert_k_role(uint32_t base, const Layout &y, cons
 }
 
 template <int D, int VF>
-__device__ __noinline__ void convert_v_role(uint32_t base, const Layout &y, const Waiter &wait, int tiles) {
+__device__ __forceinline__ void convert_v_role(uint32_t base, const Layout &y, const Waiter &wait, int tiles) {
   using L = Smem<D>;
   using VC = VCode<VF>;
   using F = Cover<D, VC::code>;
@@ -449,60 +449,40 @@ struct TileWalk {
   }
 };
 
-// Codes into the rings, a TMA box (16 rows of one head) per block, in the order
-// K(0), K(1), V(0), K(2), V(1), ...: K is wanted about a tile before V.
-__device__ __noinline__ void load_role(const PrefixArgs &a, const CUtensorMap *kmap, const CUtensorMap *vmap, int krow,
-                                       int vrow, uint32_t base, const Layout &y, const Waiter &wait, const Segments &seg,
-                                       int x, int x1) {
-  const int lane = threadIdx.x & 31, tiles = x1 - x;
+// Codes into a ring (r = 0: of K, 1: of V), a TMA box (16 rows of one head) per
+// block.  A warp's box takes it ~175 cycles (its lanes issue one by one; one
+// lane for all boxes took twice as long), which bounds the kernel with one warp
+// for both rings.
+__device__ __forceinline__ void load_role(const PrefixArgs &a, const CUtensorMap *map, int row, int r, uint32_t base,
+                                          const Layout &y, const Waiter &wait, const Segments &seg, int x, int x1) {
+  const int lane = threadIdx.x & 31, tiles = x1 - x, places = y.units[r];
+  const uint32_t box = kBlockSize * row, bytes = y.unit[r], ring = base + y.ring[r];
+  const int per = static_cast<int>(bytes / box);  // blocks of a unit
   TileWalk w(a, seg, x, x1);
-  int slot[2] = {0, 0}, kid = -1, kh = 0, vid, vh;
-  uint32_t phase[2] = {1, 1};
+  int at = 0;
+  uint32_t ph = 1;
   w.next();
-  // step n: K of tile n, then V of tile n - 1
 #pragma unroll 1
-  for (int n = 0; n <= tiles; ++n) {
-    vid = kid;
-    vh = kh;
-    if (n < tiles) {
-      w.next();
-      kid = w.id(lane < 8);
-      kh = w.h;
-    }
+  for (int n = 0; n < tiles; ++n) {
+    w.next();
+    const int id = w.id(lane < 8 && r == 0);
 #pragma unroll 1
-    for (int r = n < tiles ? 0 : 1; r < (n > 0 ? 2 : 1); ++r) {
-      const CUtensorMap *map = r ? vmap : kmap;
-      const int row = r ? vrow : krow, id = r ? vid : kid, h = r ? vh : kh;
-      const int places = y.units[r];
-      const uint32_t box = kBlockSize * row, bytes = y.unit[r], ring = base + y.ring[r];
-      const int per = static_cast<int>(bytes / box);  // blocks of a unit
-      int at = r ? slot[1] : slot[0];
-      uint32_t ph = r ? phase[1] : phase[0];
-#pragma unroll 1
-      for (int b = 0; b < kTileBlocks; b += per) {
-        const int bar = r * kMaxUnits + at;
-        wait(B_EMPTY + bar, ph);
-        const bool in = static_cast<unsigned>(lane - b) < static_cast<unsigned>(per) && id >= 0;
-        const int boxes = __popc(__ballot_sync(0xffffffffu, in));
-        uint64_t *full = &wait.bars[B_FULL + bar];
-        if (lane == 0) {
-          if (boxes) mbar_arrive_expect_tx(full, boxes * box);
-          else mbar_arrive(full);
-        }
-        __syncwarp();
-        // (after a wait that ran out nobody reads: no further copies)
-        if (in && !*wait.abort) tma_tile_load(ring + at * bytes + (lane - b) * box, map, h, id, full);
-        if (++at == places) {
-          at = 0;
-          ph ^= 1;
-        }
+    for (int b = 0; b < kTileBlocks; b += per) {
+      const int bar = r * kMaxUnits + at;
+      wait(B_EMPTY + bar, ph);
+      const bool in = static_cast<unsigned>(lane - b) < static_cast<unsigned>(per) && id >= 0;
+      const int boxes = __popc(__ballot_sync(0xffffffffu, in));
+      uint64_t *full = &wait.bars[B_FULL + bar];
+      if (lane == 0) {
+        if (boxes) mbar_arrive_expect_tx(full, boxes * box);
+        else mbar_arrive(full);
       }
-      if (r) {
-        slot[1] = at;
-        phase[1] = ph;
-      } else {
-        slot[0] = at;
-        phase[0] = ph;
+      __syncwarp();
+      // (after a wait that ran out nobody reads: no further copies)
+      if (in && !*wait.abort) tma_tile_load(ring + at * bytes + (lane - b) * box, map, w.h, id, full);
+      if (++at == places) {
+        at = 0;
+        ph ^= 1;
       }
     }
   }
@@ -514,16 +494,11 @@ __device__ __noinline__ void load_role(const PrefixArgs &a, const CUtensorMap *k
     }
   }
 #pragma unroll 1
-  for (int r = 0; r < 2; ++r) {
-    int at = r ? slot[1] : slot[0];
-    uint32_t ph = r ? phase[1] : phase[0];
-#pragma unroll 1
-    for (int k = 0; k < y.units[r]; ++k) {
-      wait(B_EMPTY + r * kMaxUnits + at, ph);
-      if (++at == y.units[r]) {
-        at = 0;
-        ph ^= 1;
-      }
+  for (int k = 0; k < places; ++k) {
+    wait(B_EMPTY + r * kMaxUnits + at, ph);
+    if (++at == places) {
+      at = 0;
+      ph ^= 1;
     }
   }
 }
@@ -571,7 +546,7 @@ __device__ __forceinline__ void pair_scales(const float (&s)[N], float f, uint32
 
 // LOW false: 2-bit codes, whose scales are BF16 numbers (q_max 1).
 template <int D, bool CHAN, bool LOW>
-__device__ __noinline__ void scale_k_role(const PrefixArgs &a, uint32_t base, const Layout &y,
+__device__ __forceinline__ void scale_k_role(const PrefixArgs &a, uint32_t base, const Layout &y,
                                           const Waiter &wait, const Segments &seg, int top, int x, int x1) {
   using L = Smem<D>;
   constexpr int NC = CHAN ? kTileBlocks * D / 128 : 1;  // float4 of scales
@@ -638,7 +613,7 @@ __device__ __noinline__ void scale_k_role(const PrefixArgs &a, uint32_t base, co
 }
 
 template <int D, bool GROUP, bool LOW>
-__device__ __noinline__ void scale_v_role(const PrefixArgs &a, uint32_t base, const Layout &y,
+__device__ __forceinline__ void scale_v_role(const PrefixArgs &a, uint32_t base, const Layout &y,
                                           const Waiter &wait, const Segments &seg, int top, int x, int x1) {
   using L = Smem<D>;
   constexpr int NG = GROUP ? D / 32 : 1;
@@ -908,7 +883,7 @@ __device__ __noinline__ void store_partial(const PrefixArgs &a, const Segment &s
 }
 
 template <int D>
-__device__ __noinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, const Layout &y0, const Waiter &wait,
+__device__ __forceinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, const Layout &y0, const Waiter &wait,
                                              uint32_t tmem, const Segments &sg, int x, int x1) {
   using L = Smem<D>;
   const uint32_t base = smem_u32(smem);
@@ -1131,7 +1106,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Segments sg = {first, x};
   const int tiles = x1 - x;
   const bool chan = kf == K_INT8_CHAN || kf == K_INT2_CHAN, group = vf == V_INT4_G32 || vf == V_INT2_G32;
-  if (warp >= kSoftmaxWarp) {
+  if (warp == kLoadWarp || warp == kLoadVWarp) {
+    const int r = warp == kLoadWarp ? 0 : 1;
+    load_role(a, r ? &vmap : &kmap, r ? vrow : krow, r, base, y, wait, sg, x, x1);
+  } else if (warp >= kSoftmaxWarp) {
     softmax_role<D>(a, smem, y, wait, tmem, sg, x, x1);
   } else if (warp >= kVWarp) {
     if (vf == V_INT8_TOK) convert_v_role<D, V_INT8_TOK>(base, y, wait, tiles);
@@ -1146,8 +1124,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if constexpr (D == 128) convert_k_role<D, K_INT2_CHAN>(base, y, wait, tiles);
   } else if (warp == kMmaWarp) {
     product_role<D>(a, base, wait, tmem, sg, x, x1);
-  } else if (warp == kLoadWarp) {
-    load_role(a, &kmap, &vmap, krow, vrow, base, y, wait, sg, x, x1);
   } else if (warp == kScaleWarp) {
     const int top = top_exponent(kf == K_FP8_TOK ? C_FP8 : C_INT8);
     if (kf == K_INT2_CHAN) scale_k_role<D, true, false>(a, base, y, wait, sg, top, x, x1);
