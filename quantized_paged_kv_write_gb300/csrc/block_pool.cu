@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWarps = kPoolThreads / 32;
+constexpr int kFlight = 4;  // loads of a thread that are under way together
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -172,33 +173,50 @@ __global__ void __launch_bounds__(kPoolThreads) assign_blocks_kernel(const Assig
   const int tid = rank * kPoolThreads + threadIdx.x, nth = nct * kPoolThreads;
   // ---- offsets, slots and positions
   for (int b = tid; b <= B; b += nth) a.token_offsets[b] = ok ? tok[b] : 0;
-  for (int64_t t = tid; t < a.max_tokens; t += nth) {
-    int64_t slot = -1;
-    int pos = -1;
-    if (t < ntok) {
-      const int b = row_of(tok, B, static_cast<int>(t));
+#pragma unroll 1
+  for (unsigned int t0 = tid; t0 < static_cast<unsigned int>(a.max_tokens); t0 += kFlight * nth) {
+    int pos[kFlight], id[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const unsigned int at = t0 + u * nth;
+      pos[u] = id[u] = -1;
+      if (at >= static_cast<unsigned int>(ntok)) continue;
+      const int t = static_cast<int>(at), b = row_of(tok, B, t);
       const int c = ctx[b], have = blocks_of(c);
-      pos = c + static_cast<int>(t) - tok[b];
-      const int j = pos / kBlockSize;
-      const int id = j < have ? __ldcg(a.tables + static_cast<int64_t>(b) * M + j)
-                              : __ldg(a.free_list + (f - 1 - (blk[b] + j - have)));
-      if (id >= 0 && id < a.num_blocks) slot = static_cast<int64_t>(id) * kBlockSize + pos % kBlockSize;
+      pos[u] = c + t - tok[b];
+      const int j = pos[u] / kBlockSize;
+      id[u] = __ldcg(j < have ? a.tables + static_cast<int64_t>(b) * M + j : a.free_list + (f - 1 - (blk[b] + j - have)));
     }
-    a.slots[t] = slot;
-    if (a.positions != nullptr) a.positions[t] = pos;
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const unsigned int t = t0 + u * nth;
+      if (t >= static_cast<unsigned int>(a.max_tokens)) break;
+      a.slots[t] = id[u] >= 0 && id[u] < a.num_blocks ? static_cast<int64_t>(id[u]) * kBlockSize + pos[u] % kBlockSize : -1;
+      if (a.positions != nullptr) a.positions[t] = pos[u];
+    }
   }
   if (ok) {
     // ---- shared blocks, then new ones
     if (a.prefix_rows != nullptr) {
+#pragma unroll 1
       for (int b = rank; b < B; b += nct) {
         const int s = __ldg(a.prefix_rows + b);
         if (s < 0) continue;
         const int k = ctx[b] / kBlockSize;
-        for (int i = threadIdx.x; i < k; i += kPoolThreads) {
-          const int id = __ldcg(a.tables + static_cast<int64_t>(s) * M + i);
-          a.tables[static_cast<int64_t>(b) * M + i] = id;
-          if (id >= 0 && id < a.num_blocks) atomicAdd(a.ref_counts + id, 1);
-          else set_error(a.err, KVQ_DEVERR_BLOCK_RANGE);
+        const int32_t *const from = a.tables + static_cast<int64_t>(s) * M;
+        int32_t *const to = a.tables + static_cast<int64_t>(b) * M;
+#pragma unroll 1
+        for (int i = threadIdx.x; i < k; i += kFlight * kPoolThreads) {
+          int id[kFlight];
+#pragma unroll
+          for (int u = 0; u < kFlight; ++u) id[u] = __ldcg(from + min(i + u * kPoolThreads, k - 1));
+#pragma unroll
+          for (int u = 0; u < kFlight; ++u) {
+            if (i + u * kPoolThreads >= k) break;
+            to[i + u * kPoolThreads] = id[u];
+            if (id[u] >= 0 && id[u] < a.num_blocks) atomicAdd(a.ref_counts + id[u], 1);
+            else set_error(a.err, KVQ_DEVERR_BLOCK_RANGE);
+          }
         }
       }
     }
@@ -269,8 +287,8 @@ __global__ void __launch_bounds__(kPoolThreads) release_blocks_kernel(const Rele
   __syncthreads();
 
   // each warp owns a contiguous run of items
-  const int64_t w = static_cast<int64_t>(rank) * kPoolWarps + warp, nw = static_cast<int64_t>(nct) * kPoolWarps;
-  const int lo = static_cast<int>(w * n / nw), hi = static_cast<int>((w + 1) * n / nw);
+  const unsigned int items = n, each = (items + nct * kPoolWarps - 1) / (nct * kPoolWarps);
+  const int lo = min(items, (rank * kPoolWarps + warp) * each), hi = min(items, lo + each);
   auto entry = [&](int i) -> int32_t * {
     const int b = row_of(off, B, i);
     return a.tables + static_cast<int64_t>(b) * M + first[b] + (i - off[b]);
@@ -298,9 +316,13 @@ __global__ void __launch_bounds__(kPoolThreads) release_blocks_kernel(const Rele
   cluster_arrive();
   cluster_wait();
   int mine = 0;  // pushes of this warp
-  for (int i = lo + lane; i < hi; i += 32) {
+  // which of the first 64 turns pushes: the scattered counts are read once
+  unsigned long long which = 0;
+  for (int i = lo + lane, k = 0; i < hi; i += 32, ++k) {
     const int id = __ldcg(entry(i));
-    mine += id >= 0 && __ldcg(a.ref_counts + id) == INT_MIN + i;
+    const bool push = id >= 0 && __ldcg(a.ref_counts + id) == INT_MIN + i;
+    mine += push;
+    if (push && k < 64) which |= 1ull << k;
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -319,14 +341,14 @@ __global__ void __launch_bounds__(kPoolThreads) release_blocks_kernel(const Rele
   }
   // the descending loop pushes the last item first
   int done = before;
-  for (int base = lo; base < hi; base += 32) {
+  for (int base = lo, k = 0; base < hi; base += 32, ++k) {
     const int i = base + lane;
     bool push = false;
     int id = -1;
     if (i < hi) {
       int32_t *e = entry(i);
       id = __ldcg(e);
-      push = id >= 0 && __ldcg(a.ref_counts + id) == INT_MIN + i;
+      push = k < 64 ? which >> k & 1 : id >= 0 && __ldcg(a.ref_counts + id) == INT_MIN + i;
       *e = -1;
     }
     const unsigned int votes = __ballot_sync(0xffffffffu, push);
@@ -354,11 +376,15 @@ __global__ void __launch_bounds__(kPoolThreads) release_blocks_kernel(const Rele
 
 template <typename Args>
 cudaError_t launch_cluster(void (*kern)(const Args), const Args &a, int ctas, size_t smem, cudaStream_t stream) {
-  // above the default 48 KB only with many rows; the attribute is per device
-  // and idempotent
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
-    if (e != cudaSuccess) return e;
+  // Above the default 48 KB only with many rows, and sixteen CTAs only with much
+  // work; the attributes are per device and idempotent.
+  cudaError_t e;
+  if (smem > 48 * 1024 &&
+      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024)) != cudaSuccess)
+    return e;
+  if (ctas > 8 && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) {
+    cudaGetLastError();
+    ctas = 8;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
@@ -375,10 +401,12 @@ cudaError_t launch_cluster(void (*kern)(const Args), const Args &a, int ctas, si
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-// Portable cluster sizes, one CTA per 4096 items of work.
+// One CTA per 4096 items of work, up to the largest cluster: scattered accesses
+// to the counts bound large calls, and so the SMs that make them (release of 64
+// rows behind 2048 shared blocks: 8 CTAs 73 us, 16 CTAs 41 us).
 int cluster_for(int64_t items) {
   int c = 1;
-  while (c < 8 && static_cast<int64_t>(c) * 4096 < items) c *= 2;
+  while (c < 16 && static_cast<int64_t>(c) * 4096 < items) c *= 2;
   return c;
 }
 
