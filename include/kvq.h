@@ -410,16 +410,18 @@ int kvq_release_blocks(const int32_t *keep_lens, int32_t num_rows, int32_t *cont
  *
  * The result is kvq_paged_decode's (kvq_kivi_decode's with a tail) but for
  * the prefix's operands: queries, probabilities and scaled codes enter the
- * matrix products as f16, rounded once (a relative 2^-12 each, with the row's
- * or tile's power of two taken out; codes alone are exact); products,
- * softmax statistics and partial outputs are FP32, and the output is rounded
- * once to BF16, which is coarser.
+ * matrix products as f16, rounded once (at most a relative 2^-11 each, with
+ * the row's or tile's power of two taken out; BF16 queries down to 2^-32 of
+ * their row's largest are exact); products, softmax statistics and partial
+ * outputs are FP32, and the output is rounded once to BF16 (2^-8).
  * A group of fewer than two sequences shares nothing and costs what
  * kvq_paged_decode costs.  A prefix_lens entry outside [0, max_prefix_len]
  * (KVQ_DEVERR_CONTEXT_RANGE) and groups out of order
  * (KVQ_DEVERR_GROUP_RANGE) are decoded without sharing; other errors as
  * kvq_paged_decode.  num_groups <= 8192 (0: group_starts, prefix_lens may be
- * NULL); batch == 0 is a no-op.
+ * NULL); batch == 0 is a no-op.  batch * max_blocks_per_seq and batch *
+ * num_kv_heads * (blocks of max_prefix_len / 8, rounded up) stay below 2^31,
+ * else KVQ_ERR_UNSUPPORTED.
  */
 int kvq_prefix_decode_workspace_size(const kvq_format *fmt, int32_t batch, int32_t num_q_heads,
                                      int32_t max_context_len, int32_t num_groups, size_t *bytes);

@@ -23,6 +23,7 @@ namespace {
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWarps = kPoolThreads / 32;
 constexpr int kFlight = 4;  // loads of a thread that are under way together
+constexpr int kStrip = 8;   // rows that a thread takes together where they may share blocks
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -198,24 +199,34 @@ __global__ void __launch_bounds__(kPoolThreads) assign_blocks_kernel(const Assig
   if (ok) {
     // ---- shared blocks, then new ones
     if (a.prefix_rows != nullptr) {
+      // A thread has one column of kStrip rows: rows behind the same prefix read
+      // its entry once, and its count goes up once for all of them.  A unit is
+      // every other 1024 columns of a strip.
 #pragma unroll 1
-      for (int b = rank; b < B; b += nct) {
-        const int s = __ldg(a.prefix_rows + b);
-        if (s < 0) continue;
-        const int k = ctx[b] / kBlockSize;
-        const int32_t *const from = a.tables + static_cast<int64_t>(s) * M;
-        int32_t *const to = a.tables + static_cast<int64_t>(b) * M;
+      for (int unit = rank; unit / 2 * kStrip < B; unit += nct) {
+        const int b0 = unit / 2 * kStrip;
+        int from[kStrip], k[kStrip], most = 0;
+#pragma unroll
+        for (int u = 0; u < kStrip; ++u) {
+          const int b = min(b0 + u, B - 1);
+          from[u] = __ldg(a.prefix_rows + b);
+          k[u] = b0 + u < B && from[u] >= 0 ? ctx[b] / kBlockSize : 0;
+          most = max(most, k[u]);
+        }
 #pragma unroll 1
-        for (int i = threadIdx.x; i < k; i += kFlight * kPoolThreads) {
-          int id[kFlight];
+        for (int i = (unit & 1) * kPoolThreads + threadIdx.x; i < most; i += 2 * kPoolThreads) {
+          int id[kStrip];
 #pragma unroll
-          for (int u = 0; u < kFlight; ++u) id[u] = __ldcg(from + min(i + u * kPoolThreads, k - 1));
+          for (int u = 0; u < kStrip; ++u) id[u] = i < k[u] ? max(__ldcg(a.tables + static_cast<int64_t>(from[u]) * M + i), INT_MIN + 1) : INT_MIN;
+          int run = 0;
 #pragma unroll
-          for (int u = 0; u < kFlight; ++u) {
-            if (i + u * kPoolThreads >= k) break;
-            to[i + u * kPoolThreads] = id[u];
-            if (id[u] >= 0 && id[u] < a.num_blocks) atomicAdd(a.ref_counts + id[u], 1);
-            else set_error(a.err, KVQ_DEVERR_BLOCK_RANGE);
+          for (int u = 0; u < kStrip; ++u) {
+            if (i < k[u]) a.tables[static_cast<int64_t>(b0 + u) * M + i] = id[u];
+            ++run;
+            if (u + 1 < kStrip && id[u + 1] == id[u]) continue;
+            if (id[u] >= 0 && id[u] < a.num_blocks) atomicAdd(a.ref_counts + id[u], run);
+            else if (id[u] != INT_MIN) set_error(a.err, KVQ_DEVERR_BLOCK_RANGE);
+            run = 0;
           }
         }
       }
@@ -293,25 +304,88 @@ __global__ void __launch_bounds__(kPoolThreads) release_blocks_kernel(const Rele
     const int b = row_of(off, B, i);
     return a.tables + static_cast<int64_t>(b) * M + first[b] + (i - off[b]);
   };
-  for (int i = lo + lane; i < hi; i += 32) {
-    int32_t *e = entry(i);
-    const int id = __ldcg(e);
-    if (id < 0 || id >= a.num_blocks) {
-      set_error(a.err, KVQ_DEVERR_BLOCK_RANGE);
-      *e = -1;
-      continue;
+  // Long rows may share most of their blocks: a lane then has one column of
+  // kStrip rows, whose runs of one id give it back, and offer for it, once.
+  const bool strips = n / 32 >= B;
+  const int gw = rank * kPoolWarps + warp, warps = nct * kPoolWarps;
+  // visit(row of the strip's first entry, column) for this warp's columns
+  auto each_column = [&](auto visit) {
+    int skip = gw;  // the warp's first group of 32 columns in the strip
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += kStrip) {
+      const int b = min(b0 + lane % kStrip, B - 1), cnt = off[b + 1] - off[b];
+      const int j0 = __reduce_min_sync(0xffffffffu, cnt > 0 ? first[b] : INT_MAX);
+      const int j1 = __reduce_max_sync(0xffffffffu, cnt > 0 ? first[b] + cnt : 0);
+      const int groups = j1 > j0 ? (j1 - j0 + 31) / 32 : 0;
+#pragma unroll 1
+      for (; skip < groups; skip += warps) visit(b0, j0 + 32 * skip + lane);
+      skip -= groups;  // the next strip's groups go on with the next warp
     }
-    if (atomicSub(a.ref_counts + id, 1) <= 0) {  // given back more often than held
-      atomicAdd(a.ref_counts + id, 1);
-      set_error(a.err, KVQ_DEVERR_POOL_STATE);
+  };
+  // the column's ids: INT_MIN where the row gives nothing back there
+  auto column = [&](int b0, int j, int (&id)[kStrip]) {
+#pragma unroll
+    for (int u = 0; u < kStrip; ++u) {
+      const int b = min(b0 + u, B - 1);
+      const bool in = b0 + u < B && off[b + 1] > off[b] && j >= first[b] && j - first[b] < off[b + 1] - off[b];
+      id[u] = in ? max(__ldcg(a.tables + static_cast<int64_t>(b) * M + j), INT_MIN + 1) : INT_MIN;
+    }
+  };
+  if (strips) {
+    each_column([&](int b0, int j) {
+      int id[kStrip], run = 0;
+      column(b0, j, id);
+#pragma unroll
+      for (int u = 0; u < kStrip; ++u) {
+        ++run;
+        if (u + 1 < kStrip && id[u + 1] == id[u]) continue;
+        if (id[u] != INT_MIN) {
+          const bool in = id[u] >= 0 && id[u] < a.num_blocks;
+          const int held = in ? atomicSub(a.ref_counts + id[u], run) : 0;
+          if (held < run) {  // no block, or given back more often than held
+            set_error(a.err, in ? KVQ_DEVERR_POOL_STATE : KVQ_DEVERR_BLOCK_RANGE);
+            if (in) atomicAdd(a.ref_counts + id[u], run - max(held, 0));
+            if (held <= 0)
+              for (int v = u - run + 1; v <= u; ++v) a.tables[static_cast<int64_t>(b0 + v) * M + j] = -1;
+          }
+        }
+        run = 0;
+      }
+    });
+  } else {
+#pragma unroll 1
+    for (int i = lo + lane; i < hi; i += 32) {
+      int32_t *e = entry(i);
+      const int id = __ldcg(e);
+      const bool in = id >= 0 && id < a.num_blocks;
+      if (in && atomicSub(a.ref_counts + id, 1) > 0) continue;
+      if (in) atomicAdd(a.ref_counts + id, 1);  // given back more often than held
+      set_error(a.err, in ? KVQ_DEVERR_POOL_STATE : KVQ_DEVERR_BLOCK_RANGE);
       *e = -1;
     }
   }
   cluster_arrive();
   cluster_wait();
-  for (int i = lo + lane; i < hi; i += 32) {
-    const int id = __ldcg(entry(i));
-    if (id >= 0 && __ldcg(a.ref_counts + id) <= 0) atomicMin(a.ref_counts + id, INT_MIN + i);
+  if (strips) {
+    each_column([&](int b0, int j) {
+      int id[kStrip];
+      column(b0, j, id);
+#pragma unroll
+      for (int u = kStrip - 1; u >= 0; --u) {  // (the first row of a run has its first item)
+        const bool lead = u == 0 || id[u - 1] != id[u];
+        if (id[u] < 0) continue;
+        if (lead && __ldcg(a.ref_counts + id[u]) <= 0)
+          atomicMin(a.ref_counts + id[u], INT_MIN + off[b0 + u] + (j - first[b0 + u]));
+        else
+          a.tables[static_cast<int64_t>(b0 + u) * M + j] = -1;  // does not push
+      }
+    });
+  } else {
+#pragma unroll 1
+    for (int i = lo + lane; i < hi; i += 32) {
+      const int id = __ldcg(entry(i));
+      if (id >= 0 && __ldcg(a.ref_counts + id) <= 0) atomicMin(a.ref_counts + id, INT_MIN + i);
+    }
   }
   cluster_arrive();
   cluster_wait();

@@ -18,14 +18,28 @@
 //
 // Roles, one CTA per SM: two softmax warpgroups (thread = row), two
 // warpgroups that turn codes into f16 tiles in shared memory (one K, one V),
-// and a warp each for the products, the TMA loads of codes and the scales.
-// Steps alternate between the two softmax warpgroups, so
-// the tensor core works for one while the other is in its exponentials:
+// and a warp each for the products, for the TMA loads of K and of V codes, and
+// for the scales of K and of V.  Steps alternate between the two softmax
+// warpgroups, so the tensor core works for one while the other is in its
+// exponentials:
 //   more than 128 rows: warpgroup i owns rows 128 i .. + 127, each tile of
 //     codes serves both (steps 2t, 2t + 1 of tile t);
 //   at most 128 rows: both own the same rows, warpgroup i the tiles of parity
-//     i; each keeps its own (m, l, O), merged later like any other partial.
+//     i; each keeps its own (m, l, O), joined in tensor memory at the end.
 // P overwrites S in tensor memory and is the A operand of the second product.
+//
+// What bounds it.  27 sequences, 32 query heads on 8, FP8 K and V, 32003 shared
+// positions: 34 us, 66 MB of codes and scales at 1.9 TB/s.  A tile takes ~3450
+// cycles of an SM, of which the converters' chains (load, decode, scale, store)
+// are busy for ~3100; twice the converter warps at fewer registers gained
+// nothing (36 us).  100 sequences, 64 query heads on 8, INT2 K and V, 65536
+// positions: 264 us, 0.81 PFLOP/s, a two-row-tile step in ~4450 cycles, 2080 of
+// them products; the rest is the chain S - softmax - P V of a warpgroup, whose
+// single S buffer (tensor memory is full: two S, two O) keeps its next S waiting
+// for its P V.  Halves of S to overlap them made products of 64 columns, which
+// shared memory's bandwidth slows (288 us).  Measured on the way: out-of-line
+// roles, which reload their parameters after every barrier, 46 instead of 41 us
+// (first shape); one load warp for both rings 41 instead of 34 us.
 #pragma once
 
 #include <limits.h>

@@ -106,6 +106,46 @@ def test_shared_prefixes_come_and_go():
     assert len(s.pool.free) == 700
 
 
+@pytest.mark.parametrize("rows,shared,keepers", [(2, 40, 1), (9, 33, 1), (16, 300, 2), (67, 129, 3), (24, 2100, 1),
+                                                 (530, 2048, 1)])
+def test_long_rows_behind_shared_prefixes(rows, shared, keepers):
+    """Rows of one id per column next to rows of others, ends and beginnings in
+    the middle of the shared blocks; the largest has more items than a warp's
+    first 64 turns hold."""
+    width, live = shared + 6, rows - keepers
+    s = Both(rows, width, keepers * shared + live * 7 + 3, seed=rows + shared)
+    n = np.zeros(rows, int)
+    n[live:] = shared * 16                               # the prompts
+    assert s.assign(n)
+    src, blocks = np.full(rows, -1), np.zeros(rows, int)
+    src[:live] = live + np.sort(s.rng.integers(0, keepers, live))
+    blocks[:live] = np.where(s.rng.random(live) < 0.7, shared, s.rng.integers(0, shared + 1, live))
+    n = np.where(np.arange(rows) < live, s.rng.integers(0, 90, rows), 0)
+    assert s.assign(n, rows=src, blocks=blocks)
+    some = s.rng.random(rows) < 0.5
+    s.release(np.where(some, s.rng.integers(0, shared * 16, rows) // 16 * 16, 10 ** 6))  # back into the shared blocks
+    s.release(np.where(s.rng.random(rows) < 0.3, 0, 10 ** 6))
+    s.release(np.zeros(rows, int))                       # all at once
+    assert len(s.pool.free) == len(s.pool.refs)
+
+
+def test_more_given_back_than_held():
+    """Tables that list a block more often than its count says: the block goes
+    back once, the counts end at 0, the bit is set."""
+    for rows, width in ((3, 4), (20, 64)):               # by items and by columns
+        pool = kvq.allocate_pool(width)
+        pool["free_count"].zero_()
+        pool["ref_counts"].fill_(2)
+        tables = _i32(np.tile(np.arange(width), (rows, 1)))
+        tables[0, 0] = -7
+        ctx = _i32([16 * width] * rows)
+        kvq.kvq_release_blocks(_i32([0] * rows), ctx, tables, pool)
+        assert kvq.kvq_device_errors() == kvq.DEVERR_POOL_STATE | kvq.DEVERR_BLOCK_RANGE
+        assert (tables == -1).all() and (pool["ref_counts"] == 0).all() and (ctx == 0).all()
+        assert int(pool["free_count"]) == width
+        assert sorted(pool["free_list"].tolist()) == list(range(width))
+
+
 def test_release_undoes_assign_exactly():
     s = Both(50, 30, 900, seed=6)
     assert s.assign(s.rng.integers(0, 200, 50))
