@@ -389,14 +389,39 @@ __global__ void __launch_bounds__(kPoolThreads) release_blocks_kernel(const Rele
   }
   cluster_arrive();
   cluster_wait();
+  // Which items push; the others are done.  kFlight of them are searched for and
+  // loaded together; `which` has the first 64 turns, so that the last pass takes
+  // only those that push.
   int mine = 0;  // pushes of this warp
-  // which of the first 64 turns pushes: the scattered counts are read once
   unsigned long long which = 0;
-  for (int i = lo + lane, k = 0; i < hi; i += 32, ++k) {
-    const int id = __ldcg(entry(i));
-    const bool push = id >= 0 && __ldcg(a.ref_counts + id) == INT_MIN + i;
-    mine += push;
-    if (push && k < 64) which |= 1ull << k;
+  int top = 1;
+  while (2 * top < B) top *= 2;
+#pragma unroll 1
+  for (int i = lo + lane, k = 0; i < hi; i += 32 * kFlight, k += kFlight) {
+    int b[kFlight], id[kFlight], code[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) b[u] = 0;
+#pragma unroll 1
+    for (int step = top; step > 0; step >>= 1)
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u)
+        if (b[u] + step < B && off[b[u] + step] <= min(i + 32 * u, hi - 1)) b[u] += step;
+    int32_t *e[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      e[u] = a.tables + static_cast<int64_t>(b[u]) * M + first[b[u]] + (min(i + 32 * u, hi - 1) - off[b[u]]);
+      id[u] = __ldcg(e[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) code[u] = id[u] >= 0 ? __ldcg(a.ref_counts + id[u]) : 0;
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      if (i + 32 * u >= hi) break;
+      const bool push = id[u] >= 0 && code[u] == INT_MIN + i + 32 * u;
+      mine += push;
+      if (push && k + u < 64) which |= 1ull << (k + u);
+      if (!push && id[u] != -1) *e[u] = -1;
+    }
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -417,12 +442,13 @@ __global__ void __launch_bounds__(kPoolThreads) release_blocks_kernel(const Rele
   int done = before;
   for (int base = lo, k = 0; base < hi; base += 32, ++k) {
     const int i = base + lane;
-    bool push = false;
+    bool push = k < 64 && (which >> k & 1);
+    if (k < 64 && !__any_sync(0xffffffffu, push)) continue;
     int id = -1;
-    if (i < hi) {
+    if (i < hi && (push || k >= 64)) {
       int32_t *e = entry(i);
       id = __ldcg(e);
-      push = k < 64 ? which >> k & 1 : id >= 0 && __ldcg(a.ref_counts + id) == INT_MIN + i;
+      if (k >= 64) push = id >= 0 && __ldcg(a.ref_counts + id) == INT_MIN + i;
       *e = -1;
     }
     const unsigned int votes = __ballot_sync(0xffffffffu, push);
