@@ -129,6 +129,31 @@ def test_long_rows_behind_shared_prefixes(rows, shared, keepers):
     assert len(s.pool.free) == len(s.pool.refs)
 
 
+def test_a_captured_admission_with_many_shared_blocks():
+    """The largest clusters in a graph: admit and evict, replayed."""
+    rows, shared = 65, 2048
+    s = Both(rows, shared + 10, shared + 64 * 9 + 5, seed=21)
+    assert s.assign([0] * 64 + [shared * 16])
+    n, keep = _i32([100] * 64 + [0]), _i32([0] * 64 + [10 ** 6])
+    src, blocks = _i32([64] * 64 + [-1]), _i32([shared] * 64 + [0])
+    before = {k: v.clone() for k, v in s.dpool.items()}
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = kvq.kvq_assign_blocks(n, s.dctx, s.dtables, s.dpool, 6400, prefix_rows=src, prefix_blocks=blocks)
+        held = s.dpool["ref_counts"].clone()
+        kvq.kvq_release_blocks(keep, s.dctx, s.dtables, s.dpool)
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        s.check()                                         # the pool and tables are as they were
+        assert torch.equal(s.dpool["free_list"], before["free_list"])
+        ids = s.dtables[64, :shared].long()
+        assert (held[ids] == 65).all() and int(held.sum()) == 65 * shared + 64 * 7
+        assert int(out[0][-1]) == 6400 and int(out[1].min()) >= 0
+        for x in out:
+            x.zero_()
+
+
 def test_more_given_back_than_held():
     """Tables that list a block more often than its count says: the block goes
     back once, the counts end at 0, the bit is set."""

@@ -16,6 +16,8 @@ Z = max_t sum_c |q_c k_tc| / sqrt(d):
 With the rotation, errors are taken in the rotated basis and the worst of
 them is summed over the d channels by the way back, (1/d) sum_c.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -364,6 +366,55 @@ def test_streams_and_captured_graphs():
     graphs[0].replay()
     torch.cuda.synchronize()
     s.check(outs[0][0], ctx=s.ctx - 3)
+
+
+def test_calls_in_a_row_share_a_workspace():
+    """The kernels of a call overlap; calls of a stream do not, nor the kernels
+    around them that change lengths and read outputs."""
+    a = Batch("fp8", "int8", hq=16, hkv=4, groups=[(2000, [2000 + 7 * i for i in range(40)])], seed=16)
+    b = Batch("fp8", "int8", hq=16, hkv=4, loose=[40 + 13 * i for i in range(40)], seed=17)  # no group at all
+    c = Batch("fp8", "int8", hq=16, hkv=4, groups=[(90, [100, 95, 3]), (640, [650] * 37)], seed=18)
+    args = [a.args(), b.args(), c.args()]
+    size = max(kvq.kvq_prefix_decode_workspace_size(x[1], 40, 16, x[5], int(x[7].shape[0])) for x in args)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    start = [x[4].clone() for x in args]
+    want = {}
+    for less in range(4):
+        for i, x in enumerate(args):
+            torch.sub(start[i], less, out=x[4])
+            torch.cuda.synchronize()
+            want[i, less] = kvq.kvq_prefix_decode(*x)
+            torch.cuda.synchronize()
+    ws.fill_(0xFF)
+    got = []
+    for n in range(48):
+        i, less = n % 3, n % 4
+        torch.sub(start[i], less, out=args[i][4])
+        out = kvq.kvq_prefix_decode(*args[i], workspace=ws)
+        got.append((i, less, out.clone()))
+        out.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for i, less, out in got:
+        assert torch.equal(out, want[i, less]), (i, less)
+    a.check(want[0, 3], ctx=a.ctx - 3)
+
+
+def test_more_tiles_than_counted_are_refused():
+    s = Batch(groups=[(100, [110, 120])], seed=19)
+    q, fmt, cache, tables, ctx, _, starts, prefix, _ = s.args()
+    lib, cf = kvq.load_library(), s.fmt.as_c()
+    caches, scales = kvq._caches(cache)
+
+    def call(batch, width, longest):
+        return lib.kvq_prefix_decode(q.data_ptr(), batch, 8, ctypes.byref(cf), caches, scales, tables.data_ptr(), width,
+                                     ctx.data_ptr(), 120, starts.data_ptr(), prefix.data_ptr(), 1, longest, None, None,
+                                     q.data_ptr(), ctx.data_ptr() // 256 * 256, 0, None)
+    assert call(8192, 1 << 18, 16) == kvq.KVQ_ERR_UNSUPPORTED        # 2^31 table entries
+    # sequences * kv heads * tiles (2^15 for 2^18 blocks): 2^31 with 8 heads; fewer go on to the next check
+    assert call(8192, (1 << 18) - 1, 0x7FFFFFFF) == kvq.KVQ_ERR_WORKSPACE
+    cf.num_kv_heads = 8
+    assert call(8191, (1 << 18) - 8, 0x7FFFFFFF) == kvq.KVQ_ERR_WORKSPACE
+    assert call(8192, (1 << 18) - 1, 0x7FFFFFFF) == kvq.KVQ_ERR_UNSUPPORTED
 
 
 def test_refusals():
