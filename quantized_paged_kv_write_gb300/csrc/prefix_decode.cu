@@ -259,7 +259,7 @@ template <int D, int SPLIT>
 __global__ void __launch_bounds__(kMergeRows *SPLIT *D / 4, 1024 / (kMergeRows * SPLIT * D / 4))
     prefix_merge_kernel(const __grid_constant__ PrefixArgs a) {
   constexpr int CG = D / 4;  // channel groups
-  constexpr int U = 4;
+  constexpr int U = 4, V = 3;
   __shared__ float4 so[SPLIT][CG][kMergeRows];
   __shared__ float2 sm[SPLIT][kMergeRows];
   const int rl = threadIdx.x % kMergeRows, cg = threadIdx.x / kMergeRows % CG, sp = threadIdx.x / (kMergeRows * CG);
@@ -267,24 +267,47 @@ __global__ void __launch_bounds__(kMergeRows *SPLIT *D / 4, 1024 / (kMergeRows *
   const bool live = row < a.B * a.G;
   const int b = live ? row / a.G : 0, gq = live ? row - b * a.G : 0;
 
-  grid_wait();
-  // What does not depend on one another is loaded side by side.
-  const int gi = live ? a.ws_group[b] : -1, total = a.sfx_cum[a.B], s0 = a.sfx_cum[b], s1 = live ? a.sfx_cum[b + 1] : 0;
-  const int T = a.ws_groups[a.groups].tile0, P = a.ws_groups[a.groups].tiles;
-  const PrefixGroup &g = a.ws_groups[max(gi, 0)];
-
-  // ---- the row's partials, as lists of (m, l) and outputs: the prefix's, the
-  // suffix's high and (packed: columns g and g + G) low parts
+  // ---- the row's partials: first what the plan says, which is complete before
+  // the kernel before this one starts (ended before the prefix kernel or the
+  // split went on): CTAs are on their SMs some microseconds before the partials
+  // are there, and this is ~4700 cycles of dependent loads and cold code
+  const int gi = live ? a.ws_group[b] : -1;
   int n0 = 0, n1 = 0;
   const float2 *pml = reinterpret_cast<const float2 *>(a.ws_ml), *sml = reinterpret_cast<const float2 *>(a.sfx_ml);
   const float4 *po = reinterpret_cast<const float4 *>(a.ws_o), *qo = reinterpret_cast<const float4 *>(a.sfx_o);
   if (gi >= 0) {
+    // (through L1: all CTAs read few records, which would wait in line at L2)
+    const PrefixGroup g = a.ws_groups[gi];
+    const int T = a.ws_groups[a.groups].tile0, P = a.ws_groups[a.groups].tiles;
     const int r = (b - g.start) * a.G + gq, rb = r / g.rows, u = rb * a.H + h, x0 = g.tile0 + u * g.tiles;
     const int c0 = cta_of(x0, T, P);
     n0 = cta_of(x0 + g.tiles - 1, T, P) - c0 + 1;
     const int slot = g.row0 + u * g.rows + c0 * kPrefixRows, prow = r - rb * g.rows;
     pml += slot + prow;
     po += static_cast<int64_t>(slot) * CG + cg * g.rows + prow;
+  }
+  grid_wait();
+  const int total = a.sfx_cum[a.B], s0 = a.sfx_cum[b], s1 = live ? a.sfx_cum[b + 1] : 0;
+  RowState s;
+#pragma unroll 1
+  for (int i = sp; i < n0; i += U * SPLIT) {
+    float2 w[U];
+    float4 v[U];
+    float mn = s.m;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int e = i + k * SPLIT;
+      const int64_t at = static_cast<int64_t>(min(e, n0 - 1)) * kPrefixRows;
+      w[k] = pml[at];
+      v[k] = po[at * CG];
+      if (e >= n0) w[k].x = -INFINITY;
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) mn = fmaxf(mn, w[k].x);
+    if (mn == -INFINITY) continue;
+    s.raise(mn);
+#pragma unroll
+    for (int k = 0; k < U; ++k) s.add(w[k].x, w[k].y, v[k]);
   }
   if (s1 > s0) {
     const int Ps = min(a.sfx_nctas, max(1, (total + a.sfx_blocks_per_cta - 1) / a.sfx_blocks_per_cta));
@@ -294,33 +317,39 @@ __global__ void __launch_bounds__(kMergeRows *SPLIT *D / 4, 1024 / (kMergeRows *
     sml += rec;
     qo += rec * CG + cg;
   }
-  const int lists = 2 * a.G <= 8 ? 3 : 2;
-  RowState s;
+  // the suffix's high and (packed: columns g and g + G) low parts; both have the
+  // high parts' m and l
+  const bool packed = 2 * a.G <= 8;
 #pragma unroll 1
-  for (int list = 0; list < lists; ++list) {
-    const int n = list == 0 ? n0 : n1, step = list == 0 ? kPrefixRows : a.H * 8;
-    const float2 *const ml = list == 0 ? pml : sml;
-    const float4 *const o = list == 0 ? po : qo + (list == 2 ? a.G * CG : 0);
-    const float count = list == 2 ? 0.f : 1.f;  // (the low parts' l is the high parts')
-#pragma unroll 1
-    for (int i = sp; i < n; i += U * SPLIT) {
-      float2 w[U];
-      float4 v[U];
-      float mn = s.m;
+  for (int i = sp; i < n1; i += V * SPLIT) {
+    float2 w[V];
+    float4 v[V], lo[V];
+    float mn = s.m;
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int e = i + k * SPLIT;
-        const int64_t at = static_cast<int64_t>(min(e, n - 1)) * step;
-        w[k] = ml[at];
-        v[k] = o[at * CG];
-        if (e >= n) w[k].x = -INFINITY;
-      }
+    for (int k = 0; k < V; ++k) {
+      const int e = i + k * SPLIT;
+      const int64_t at = static_cast<int64_t>(min(e, n1 - 1)) * a.H * 8;
+      w[k] = sml[at];
+      v[k] = qo[at * CG];
+      lo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e >= n1) w[k].x = -INFINITY;
+    }
+    if (packed) {
 #pragma unroll
-      for (int k = 0; k < U; ++k) mn = fmaxf(mn, w[k].x);
-      if (mn == -INFINITY) continue;
-      s.raise(mn);
+      for (int k = 0; k < V; ++k)
+        lo[k] = qo[(static_cast<int64_t>(min(i + k * SPLIT, n1 - 1)) * a.H * 8 + a.G) * CG];
+    }
 #pragma unroll
-      for (int k = 0; k < U; ++k) s.add(w[k].x, w[k].y * count, v[k]);
+    for (int k = 0; k < V; ++k) mn = fmaxf(mn, w[k].x);
+    if (mn == -INFINITY) continue;
+    s.raise(mn);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      v[k].x += lo[k].x;
+      v[k].y += lo[k].y;
+      v[k].z += lo[k].z;
+      v[k].w += lo[k].w;
+      s.add(w[k].x, w[k].y, v[k]);
     }
   }
   if (a.res_k != nullptr) s = add_tail<D, SPLIT>(a, s, b, h, gq, rl, cg, sp, live ? a.ws_ctx[b] % kBlockSize : 0);
