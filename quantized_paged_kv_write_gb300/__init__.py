@@ -461,6 +461,18 @@ def kvq_prefetch_blocks(host_pool: dict, src_blocks: torch.Tensor, dst_blocks: t
         raise KvqError(st, "kvq_prefetch_blocks")
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor of a call's own, allocated on the stream that the call runs on:
+    its memory is neither still in use on another one, nor given away while the
+    call runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def allocate_pool(num_blocks: int, device="cuda") -> dict:
     """A block pool with every block free, block 0 first in line: free_list
     int32 [num_blocks], free_count int32 [1], ref_counts int32 [num_blocks]."""
@@ -496,11 +508,11 @@ def kvq_assign_blocks(new_lens: torch.Tensor, context_lens: torch.Tensor, block_
         if t is not None and t.shape != (rows,):
             raise ValueError(f"{what} must be [R]")
     if token_offsets is None:
-        token_offsets = torch.empty(rows + 1, dtype=torch.int32, device=dev)
+        token_offsets = _empty(rows + 1, torch.int32, dev, stream)
     if slot_mapping is None:
-        slot_mapping = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+        slot_mapping = _empty(max_tokens, torch.int64, dev, stream)
     if positions is None:
-        positions = torch.empty(max_tokens, dtype=torch.int32, device=dev)
+        positions = _empty(max_tokens, torch.int32, dev, stream)
     if token_offsets.shape != (rows + 1,) or slot_mapping.shape != (max_tokens,) or positions.shape != (max_tokens,):
         raise ValueError("token_offsets must be [R + 1], slot_mapping and positions [max_tokens]")
     st = lib.kvq_assign_blocks(_ptr(new_lens, torch.int32, "new_lens"), rows,
@@ -570,12 +582,12 @@ def kvq_prefix_decode(q: torch.Tensor, fmt: CacheFormat, cache: dict, block_tabl
             raise ValueError(f"residual k and v must be {list(want)}")
         rk, rv = _ptr(residual["k"], torch.bfloat16, "residual k"), _ptr(residual["v"], torch.bfloat16, "residual v")
     if out is None:
-        out = torch.empty((bsz, hq, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty((bsz, hq, d), torch.bfloat16, q.device, stream)
     elif tuple(out.shape) != (bsz, hq, d):
         raise ValueError("out must have the shape of q")
     if workspace is None:
         nbytes = kvq_prefix_decode_workspace_size(fmt, bsz, hq, max_context_len, groups)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     cf = fmt.as_c()
     caches, scales = _caches(cache)
     st = lib.kvq_prefix_decode(_ptr(q, torch.bfloat16, "q"), bsz, hq, ctypes.byref(cf), caches, scales,

@@ -399,6 +399,30 @@ def test_calls_in_a_row_share_a_workspace():
     a.check(want[0, 3], ctx=a.ctx - 3)
 
 
+def test_a_call_allocates_on_its_own_stream(monkeypatch):
+    """Outputs and workspaces that a call makes belong to the stream it runs on
+    (given as a Stream or a raw handle)."""
+    s = Batch(groups=[(300, [310, 320, 333])], seed=20)
+    want, args = s.run(), s.args()
+    side, plain, where = torch.cuda.Stream(), torch.empty, []
+
+    def empty(*a, **k):
+        where.append(torch.cuda.current_stream().cuda_stream)
+        return plain(*a, **k)
+    i32 = args[4].clone()
+    pool, tables = kvq.allocate_pool(40), torch.full((3, 9), -1, dtype=torch.int32, device="cuda")
+    ctx, one = torch.zeros_like(i32), torch.ones_like(i32)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "empty", empty)
+    for stream in (side, side.cuda_stream):
+        out = kvq.kvq_prefix_decode(*args, stream=stream)
+        got = kvq.kvq_assign_blocks(one, ctx, tables, pool, 3, stream=stream)
+        side.synchronize()
+        assert torch.equal(out, want) and int(got[0][-1]) == 3
+        torch.cuda.synchronize()
+    assert len(where) == 10 and set(where) == {side.cuda_stream}
+
+
 def test_more_tiles_than_counted_are_refused():
     s = Batch(groups=[(100, [110, 120])], seed=19)
     q, fmt, cache, tables, ctx, _, starts, prefix, _ = s.args()
