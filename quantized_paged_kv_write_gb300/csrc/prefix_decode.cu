@@ -15,7 +15,7 @@
 // launched while the one before runs; one after the other they took 7 to 12 us
 // more.  27 sequences, 32 query heads on 8, FP8, 32003 shared positions and
 // 1000 of each one's own: plan 4 us, attention 34, then 14 for the suffixes
-// (55 MB) and 15 for the merge, 70 in all.
+// (55 MB) and 11 for the merge, 66 in all.
 #include <limits.h>
 
 #include <atomic>
@@ -267,10 +267,10 @@ __global__ void __launch_bounds__(kMergeRows *SPLIT *D / 4, 1024 / (kMergeRows *
   const bool live = row < a.B * a.G;
   const int b = live ? row / a.G : 0, gq = live ? row - b * a.G : 0;
 
-  // ---- the row's partials: first what the plan says, which is complete before
-  // the kernel before this one starts (ended before the prefix kernel or the
-  // split went on): CTAs are on their SMs some microseconds before the partials
-  // are there, and this is ~4700 cycles of dependent loads and cold code
+  // ---- the row's partials.  First what the plan says: it has ended by the time
+  // this kernel can start, as the kernels before go on only after it.  CTAs are
+  // on their SMs some microseconds before the partials are there, and this is
+  // ~4700 cycles of dependent loads and cold code.
   const int gi = live ? a.ws_group[b] : -1;
   int n0 = 0, n1 = 0;
   const float2 *pml = reinterpret_cast<const float2 *>(a.ws_ml), *sml = reinterpret_cast<const float2 *>(a.sfx_ml);
