@@ -172,7 +172,10 @@ __global__ void __launch_bounds__(kPoolThreads) assign_blocks_kernel(const Assig
     blk[B] = nblk;
   }
   __syncthreads();
-  cluster_arrive();  // this CTA has read what the call updates in place
+  // No CTA writes anything before every CTA has checked: all come to one verdict,
+  // in pools whose counts are wrong too.
+  cluster_arrive();
+  cluster_wait();
 
   const int tid = rank * kPoolThreads + threadIdx.x, nth = nct * kPoolThreads;
   // ---- offsets, slots and positions
@@ -243,7 +246,6 @@ __global__ void __launch_bounds__(kPoolThreads) assign_blocks_kernel(const Assig
       if (in) a.ref_counts[id] = 1;
     }
   }
-  cluster_wait();
   if (ok) {
     for (int b = tid; b < B; b += nth) a.ctx[b] = ctx[b] + tok[b + 1] - tok[b];
     if (tid == 0) *a.free_count = f - nblk;
