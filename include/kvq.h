@@ -356,11 +356,13 @@ typedef struct {
  *     for every block that [context_lens[r], context_lens[r] + new_lens[r])
  *       enters: pop one from free_list, its count is 1;
  *     context_lens[r] += new_lens[r].
- * All or nothing: with an argument out of range (KVQ_DEVERR_CONTEXT_RANGE,
- * KVQ_DEVERR_BLOCK_RANGE), too few free blocks or too many tokens
- * (KVQ_DEVERR_CAPACITY), or a row that would append into a block whose count
- * is not 1 (KVQ_DEVERR_POOL_STATE), the bit is set, no row, table or pool
- * entry changes, token_offsets are 0 and the slots are -1.
+ * All or nothing: with an argument out of range (KVQ_DEVERR_CONTEXT_RANGE), a
+ * table entry outside [0, num_blocks) among the blocks to be shared or
+ * continued (KVQ_DEVERR_BLOCK_RANGE), too few free blocks or too many tokens
+ * (KVQ_DEVERR_CAPACITY), a free count or a block to be popped out of range, or a
+ * row that would append into a block whose count is not 1
+ * (KVQ_DEVERR_POOL_STATE), the bit is set, no row, table or pool entry changes,
+ * token_offsets are 0 and the slots are -1.
  *
  * kvq_release_blocks -- every row keeps its first keep_lens[r] tokens (0: it
  * is done; context_lens[r] or more: nothing changes) and gives back the

@@ -48,6 +48,12 @@ def assign_blocks(pool, new_lens, context_lens, tables, max_tokens, prefix_rows=
             if not 0 <= last < len(pool.refs) or pool.refs[last] != 1:
                 ok = False
         need += -(-(start[r] + n) // BLOCK) - -(-start[r] // BLOCK)
+    blocks = range(len(pool.refs))
+    for r in range(rows):
+        if ok and prefix_rows is not None and prefix_rows[r] >= 0:  # blocks that it would share
+            ok = all(int(x) in blocks for x in tables[prefix_rows[r], :start[r] // BLOCK])
+    if ok and need <= len(pool.free):                                # blocks that it would take
+        ok = all(x in blocks for x in pool.free[len(pool.free) - need:])
     if not ok or need > len(pool.free) or sum(int(n) for n in new_lens) > max_tokens:
         return False, np.zeros(rows + 1, np.int32), np.full(max_tokens, -1, np.int64), np.full(max_tokens, -1, np.int32)
     offsets, slots, positions = [0], [], []

@@ -107,11 +107,41 @@ __device__ __forceinline__ int row_of(const int *off, int rows, int i) {
 // ---------------------------------------------------------------------------
 // assign
 // ---------------------------------------------------------------------------
+// visit(first row of a strip, column, ids) for this CTA's part of the blocks that
+// rows share.  A thread has one column of kStrip rows: rows behind the same prefix
+// read its entry once.  INT_MIN: the row shares nothing there.  A unit is every
+// other 1024 columns of a strip.
+template <typename Visit>
+__device__ __forceinline__ void shared_columns(const AssignArgs &a, const int *ctx, uint32_t rank, uint32_t nct, Visit visit) {
+  const int B = a.rows, M = a.max_blocks;
+#pragma unroll 1
+  for (int unit = rank; unit / 2 * kStrip < B; unit += nct) {
+    const int b0 = unit / 2 * kStrip;
+    int from[kStrip], k[kStrip], most = 0;
+#pragma unroll
+    for (int u = 0; u < kStrip; ++u) {
+      const int b = min(b0 + u, B - 1);
+      from[u] = __ldg(a.prefix_rows + b);
+      k[u] = b0 + u < B && from[u] >= 0 ? ctx[b] / kBlockSize : 0;
+      most = max(most, k[u]);
+    }
+#pragma unroll 1
+    for (int i = (unit & 1) * kPoolThreads + threadIdx.x; i < most; i += 2 * kPoolThreads) {
+      int id[kStrip];
+#pragma unroll
+      for (int u = 0; u < kStrip; ++u)
+        id[u] = i < k[u] ? max(__ldcg(a.tables + static_cast<int64_t>(from[u]) * M + i), INT_MIN + 1) : INT_MIN;
+      visit(b0, i, id);
+    }
+  }
+}
+
 // Shared: tok[rows + 1], blk[rows + 1], ctx[rows] (contexts after sharing).
 __global__ void __launch_bounds__(kPoolThreads) assign_blocks_kernel(const AssignArgs a) {
   extern __shared__ int sm[];
   __shared__ long long wx[kPoolWarps];
   __shared__ int wy[kPoolWarps];
+  __shared__ int refused;
   const int B = a.rows, M = a.max_blocks;
   int *tok = sm, *blk = sm + B + 1, *ctx = sm + 2 * (B + 1);
   const uint32_t rank = cluster_rank(), nct = cluster_size();
@@ -164,20 +194,37 @@ __global__ void __launch_bounds__(kPoolThreads) assign_blocks_kernel(const Assig
   }
   if (f < 0 || f > a.num_blocks) bad |= KVQ_DEVERR_POOL_STATE;
   else if (cblk > f || ctok > a.max_tokens) bad |= KVQ_DEVERR_CAPACITY;
-  if (bad && rank == 0) set_error(a.err, bad);
-  const bool ok = !__syncthreads_or(bad != 0);
-  const int ntok = ok ? static_cast<int>(ctok) : 0, nblk = ok ? cblk : 0;
-  if (threadIdx.x == 0) {
-    tok[B] = ntok;
-    blk[B] = nblk;
+  const int tid = rank * kPoolThreads + threadIdx.x, nth = nct * kPoolThreads;
+  if (!__syncthreads_or(bad != 0)) {
+    // ---- the blocks that the call would share and take, the CTAs each a part
+    if (a.prefix_rows != nullptr)
+      shared_columns(a, ctx, rank, nct, [&](int, int, const int (&id)[kStrip]) {
+#pragma unroll
+        for (int u = 0; u < kStrip; ++u)
+          if (id[u] != INT_MIN && (id[u] < 0 || id[u] >= a.num_blocks)) bad |= KVQ_DEVERR_BLOCK_RANGE;
+      });
+#pragma unroll 4
+    for (int i = tid; i < cblk; i += nth) {
+      const int id = __ldg(a.free_list + (f - 1 - i));
+      if (id < 0 || id >= a.num_blocks) bad |= KVQ_DEVERR_POOL_STATE;
+    }
   }
-  __syncthreads();
-  // No CTA writes anything before every CTA has checked: all come to one verdict,
-  // in pools whose counts are wrong too.
+  if (bad) set_error(a.err, bad);
+  // No CTA writes anything before every CTA has checked, and one that has found
+  // something holds all of them back.
+  const bool any = __syncthreads_or(bad != 0);
+  if (threadIdx.x == 0) {
+    refused = any;
+    tok[B] = static_cast<int>(ctok);
+    blk[B] = cblk;
+  }
   cluster_arrive();
   cluster_wait();
+  const int lane = threadIdx.x & 31;
+  const bool ok = !__any_sync(0xffffffffu, lane < static_cast<int>(nct) && ld_cluster_s32(&refused, lane) != 0);
+  cluster_arrive();  // no CTA exits while another may still read its word
+  const int ntok = ok ? static_cast<int>(ctok) : 0, nblk = ok ? cblk : 0;
 
-  const int tid = rank * kPoolThreads + threadIdx.x, nth = nct * kPoolThreads;
   // ---- offsets, slots and positions
   for (int b = tid; b <= B; b += nth) a.token_offsets[b] = ok ? tok[b] : 0;
 #pragma unroll 1
@@ -198,58 +245,35 @@ __global__ void __launch_bounds__(kPoolThreads) assign_blocks_kernel(const Assig
     for (int u = 0; u < kFlight; ++u) {
       const unsigned int t = t0 + u * nth;
       if (t >= static_cast<unsigned int>(a.max_tokens)) break;
-      a.slots[t] = id[u] >= 0 && id[u] < a.num_blocks ? static_cast<int64_t>(id[u]) * kBlockSize + pos[u] % kBlockSize : -1;
+      a.slots[t] = id[u] >= 0 ? static_cast<int64_t>(id[u]) * kBlockSize + pos[u] % kBlockSize : -1;
       if (a.positions != nullptr) a.positions[t] = pos[u];
     }
   }
   if (ok) {
-    // ---- shared blocks, then new ones
-    if (a.prefix_rows != nullptr) {
-      // A thread has one column of kStrip rows: rows behind the same prefix read
-      // its entry once, and its count goes up once for all of them.  A unit is
-      // every other 1024 columns of a strip.
-#pragma unroll 1
-      for (int unit = rank; unit / 2 * kStrip < B; unit += nct) {
-        const int b0 = unit / 2 * kStrip;
-        int from[kStrip], k[kStrip], most = 0;
+    // ---- shared blocks (rows behind the same prefix raise its count once), then
+    // new ones
+    if (a.prefix_rows != nullptr)
+      shared_columns(a, ctx, rank, nct, [&](int b0, int i, const int (&id)[kStrip]) {
+        int run = 0;
 #pragma unroll
         for (int u = 0; u < kStrip; ++u) {
-          const int b = min(b0 + u, B - 1);
-          from[u] = __ldg(a.prefix_rows + b);
-          k[u] = b0 + u < B && from[u] >= 0 ? ctx[b] / kBlockSize : 0;
-          most = max(most, k[u]);
+          ++run;
+          if (id[u] != INT_MIN) a.tables[static_cast<int64_t>(b0 + u) * M + i] = id[u];
+          if (u + 1 < kStrip && id[u + 1] == id[u]) continue;
+          if (id[u] != INT_MIN) atomicAdd(a.ref_counts + id[u], run);
+          run = 0;
         }
-#pragma unroll 1
-        for (int i = (unit & 1) * kPoolThreads + threadIdx.x; i < most; i += 2 * kPoolThreads) {
-          int id[kStrip];
-#pragma unroll
-          for (int u = 0; u < kStrip; ++u) id[u] = i < k[u] ? max(__ldcg(a.tables + static_cast<int64_t>(from[u]) * M + i), INT_MIN + 1) : INT_MIN;
-          int run = 0;
-#pragma unroll
-          for (int u = 0; u < kStrip; ++u) {
-            if (i < k[u]) a.tables[static_cast<int64_t>(b0 + u) * M + i] = id[u];
-            ++run;
-            if (u + 1 < kStrip && id[u + 1] == id[u]) continue;
-            if (id[u] >= 0 && id[u] < a.num_blocks) atomicAdd(a.ref_counts + id[u], run);
-            else if (id[u] != INT_MIN) set_error(a.err, KVQ_DEVERR_BLOCK_RANGE);
-            run = 0;
-          }
-        }
-      }
-    }
+      });
     for (int i = tid; i < nblk; i += nth) {
       const int b = row_of(blk, B, i);
       const int id = __ldg(a.free_list + (f - 1 - i));
-      const bool in = id >= 0 && id < a.num_blocks;
-      if (!in) set_error(a.err, KVQ_DEVERR_POOL_STATE);
-      a.tables[static_cast<int64_t>(b) * M + blocks_of(ctx[b]) + i - blk[b]] = in ? id : -1;
-      if (in) a.ref_counts[id] = 1;
+      a.tables[static_cast<int64_t>(b) * M + blocks_of(ctx[b]) + i - blk[b]] = id;
+      a.ref_counts[id] = 1;
     }
-  }
-  if (ok) {
     for (int b = tid; b < B; b += nth) a.ctx[b] = ctx[b] + tok[b + 1] - tok[b];
     if (tid == 0) *a.free_count = f - nblk;
   }
+  cluster_wait();
 }
 
 // ---------------------------------------------------------------------------

@@ -55,3 +55,21 @@ def test_random_runs_never_lose_or_share_a_block_by_mistake():
         assert len(set(used.tolist())) == len(used) and sorted(used.tolist() + pool.free) == list(range(nb))
         assert (np.bincount(used, minlength=nb) == pool.refs).all()
         assert ((tables >= 0).sum(1) == -(-ctx // 16)).all()
+
+
+def test_a_bad_entry_in_what_is_shared_or_taken_refuses_the_call():
+    for where in ("shared", "free"):
+        pool = oracle.Pool(range(8), 8)
+        ctx, tables = np.array([0, 0]), np.full((2, 4), -1)
+        assert oracle.assign_blocks(pool, [40, 0], ctx, tables, 40)[0]
+        if where == "shared":
+            tables[0, 1] = 8
+        else:
+            pool.free[-1] = -3
+        before = (list(pool.free), ctx.copy(), tables.copy(), pool.refs.copy())
+        ok, off, slots, _ = oracle.assign_blocks(pool, [0, 3], ctx, tables, 3, [-1, 0], [0, 2])
+        assert not ok and not off.any() and (slots == -1).all()
+        assert pool.free == before[0] and (ctx == before[1]).all() and (tables == before[2]).all()
+        assert (pool.refs == before[3]).all()
+        if where == "shared":                        # as far as the good entries go
+            assert oracle.assign_blocks(pool, [0, 3], ctx, tables, 3, [-1, 0], [0, 1])[0]
