@@ -39,10 +39,11 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 __device__ __forceinline__ void cluster_arrive() {
-  __syncwarp();  // the aligned form wants the warp together
+  __syncwarp();  // the aligned forms want the warp together
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+  __syncwarp();  // (there may be loops of different lengths since the arrival)
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ int ld_cluster_s32(const int *smem, uint32_t rank) {
