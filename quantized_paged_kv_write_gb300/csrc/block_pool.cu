@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kPoolThreads) assign_blocks_kernel(const Assig
   const int B = a.rows, M = a.max_blocks;
   int *tok = sm, *blk = sm + B + 1, *ctx = sm + 2 * (B + 1);
   const uint32_t rank = cluster_rank(), nct = cluster_size();
-  const int f = __ldg(a.free_count);
+  const int f = __ldcg(a.free_count);  // (written at the end: not through the read-only path)
 
   // ---- check the rows and sum tokens and blocks
   unsigned int bad = 0;
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kPoolThreads) release_blocks_kernel(const Rele
   int *off = sm, *first = sm + B + 1;  // first released block of the row
   const uint32_t rank = cluster_rank(), nct = cluster_size();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int f = __ldg(a.free_count);
+  const int f = __ldcg(a.free_count);  // (written at the end: not through the read-only path)
   const bool pool_ok = f >= 0 && f <= a.num_blocks;
   if (!pool_ok && rank == 0 && threadIdx.x == 0) set_error(a.err, KVQ_DEVERR_POOL_STATE);
 
