@@ -375,8 +375,10 @@ typedef struct {
  *
  * Each is one launch; it may be captured and replayed.  The pool, tables and
  * lengths are read and written by one call at a time (order calls on streams).
- * num_rows <= 8192, num_rows * max_blocks_per_seq < 2^31.  Pointers of int32
- * arrays need 4-byte, of slot_mapping 8-byte alignment.
+ * num_rows <= 8192, max_blocks_per_seq < 2^27 and num_rows *
+ * max_blocks_per_seq <= 2^31 - 2^16, else KVQ_ERR_UNSUPPORTED: a row's positions
+ * and the table's entries count in 32 bits.  Pointers of int32 arrays need
+ * 4-byte, of slot_mapping 8-byte alignment.
  */
 int kvq_assign_blocks(const int32_t *new_lens, int32_t num_rows, int32_t *context_lens,
                       int32_t *block_tables, int32_t max_blocks_per_seq, kvq_block_pool pool,

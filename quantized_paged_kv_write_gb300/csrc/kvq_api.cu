@@ -582,13 +582,18 @@ int kvq_prefetch_blocks(const kvq_format *fmt, kvq_caches host_caches, kvq_scale
   return launch_prefetch(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
+// The kernels count a row's positions and the tables' entries in 32 bits, and
+// step past the last entry by less than 2^16.
+static bool table_fits(int32_t rows, int32_t max_blocks) {
+  return max_blocks < (1 << 27) && static_cast<int64_t>(rows) * max_blocks <= (int64_t(1) << 31) - (1 << 16);
+}
+
 static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 static int check_pool(int32_t num_rows, const int32_t *lens, const int32_t *context_lens, const int32_t *block_tables,
                       int32_t max_blocks, const kvq_block_pool &pool) {
   if (num_rows < 0 || max_blocks < 1 || pool.num_blocks < 0) return KVQ_ERR_INVALID_ARG;
-  if (num_rows > 8192 || static_cast<int64_t>(num_rows) * max_blocks >= (int64_t(1) << 31) ||
-      pool.num_blocks >= (int64_t(1) << 31))
+  if (num_rows > 8192 || !table_fits(num_rows, max_blocks) || pool.num_blocks >= (int64_t(1) << 31))
     return KVQ_ERR_UNSUPPORTED;
   if (num_rows > 0 && (!lens || !context_lens || !block_tables)) return KVQ_ERR_INVALID_ARG;
   if (!pool.free_count || (pool.num_blocks > 0 && (!pool.free_list || !pool.ref_counts))) return KVQ_ERR_INVALID_ARG;

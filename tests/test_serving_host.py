@@ -85,3 +85,10 @@ def test_pool_and_lengths_must_agree_in_the_binding():
         kvq.kvq_release_blocks(i, i, t[:2], pool)
     with pytest.raises(ValueError):                                                 # not CUDA tensors
         kvq.kvq_release_blocks(i, i, t, pool)
+
+
+@pytest.mark.parametrize("rows,width", [(1, 1 << 27), (1, (1 << 31) - 1), (15, 1 << 27), (16, (1 << 27) - 1),
+                                        (8192, (1 << 18) - 7)])
+def test_tables_whose_positions_pass_32_bits_are_refused(lib, rows, width):
+    assert _assign(lib, rows=rows, width=width) == kvq.KVQ_ERR_UNSUPPORTED
+    assert lib.kvq_release_blocks(BUF, rows, BUF, BUF, width, _pool(), None) == kvq.KVQ_ERR_UNSUPPORTED
