@@ -502,7 +502,8 @@ def kvq_assign_blocks(new_lens: torch.Tensor, context_lens: torch.Tensor, block_
     prefix_rows[r] >= 0 starts with that row's first prefix_blocks[r] blocks."""
     lib = load_library()
     rows, dev = int(new_lens.shape[0]), block_tables.device
-    if context_lens.shape != (rows,) or block_tables.dim() != 2 or block_tables.shape[0] != rows:
+    if (new_lens.shape != (rows,) or context_lens.shape != (rows,) or block_tables.dim() != 2
+            or block_tables.shape[0] != rows):
         raise ValueError("new_lens and context_lens must be [R] and block_tables [R, max_blocks]")
     for t, what in ((prefix_rows, "prefix_rows"), (prefix_blocks, "prefix_blocks")):
         if t is not None and t.shape != (rows,):
@@ -535,7 +536,8 @@ def kvq_release_blocks(keep_lens: torch.Tensor, context_lens: torch.Tensor, bloc
     are updated in place."""
     lib = load_library()
     rows = int(keep_lens.shape[0])
-    if context_lens.shape != (rows,) or block_tables.dim() != 2 or block_tables.shape[0] != rows:
+    if (keep_lens.shape != (rows,) or context_lens.shape != (rows,) or block_tables.dim() != 2
+            or block_tables.shape[0] != rows):
         raise ValueError("keep_lens and context_lens must be [R] and block_tables [R, max_blocks]")
     st = lib.kvq_release_blocks(_ptr(keep_lens, torch.int32, "keep_lens"), rows,
                                 _ptr(context_lens, torch.int32, "context_lens"),

@@ -92,3 +92,13 @@ def test_pool_and_lengths_must_agree_in_the_binding():
 def test_tables_whose_positions_pass_32_bits_are_refused(lib, rows, width):
     assert _assign(lib, rows=rows, width=width) == kvq.KVQ_ERR_UNSUPPORTED
     assert lib.kvq_release_blocks(BUF, rows, BUF, BUF, width, _pool(), None) == kvq.KVQ_ERR_UNSUPPORTED
+
+
+def test_lengths_of_two_columns_are_refused_by_the_binding():
+    torch = pytest.importorskip("torch")
+    i, t = torch.zeros(3, dtype=torch.int32), torch.zeros((3, 2), dtype=torch.int32)
+    pool = kvq.allocate_pool(4, device="cpu")
+    with pytest.raises(ValueError, match=r"new_lens and context_lens must be \[R\]"):
+        kvq.kvq_assign_blocks(t, i, t, pool, 4)
+    with pytest.raises(ValueError, match=r"keep_lens and context_lens must be \[R\]"):
+        kvq.kvq_release_blocks(t, i, t, pool)
