@@ -468,7 +468,8 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        # (torch takes handle 0, the default stream, for "any stream")
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
