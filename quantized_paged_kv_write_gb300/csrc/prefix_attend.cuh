@@ -1005,10 +1005,12 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem,
       begun = true;
       // ---- p = 2^(z - m + 8): plainly t c - RN(m c - 8) in one FMA; beyond
       // |m c| = 2^10 the rounding of m c would show in the exponent, so the
-      // careful form takes (t - m) c + 8
+      // careful form takes (t - m) c + 8.  c 2^-eb underflows for tiny queries
+      // against tiny scales, and a masked -inf times 0 would be NaN: there 2^-126
+      // stands for it (|t| < 2^38, so all that z loses is below 2^-88).
       auto exponentials = [&](auto tag) {
         constexpr bool careful = decltype(tag)::value;
-        const float ref = m == -INFINITY ? 0.f : m, mu = kBias - ref * c, ck = c * k0;
+        const float ref = m == -INFINITY ? 0.f : m, mu = kBias - ref * c, ck = fmaxf(c * k0, 0x1p-126f);
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll 1
         for (int cc = 0; cc < kTile / 32; ++cc) {

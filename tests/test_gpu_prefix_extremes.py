@@ -1,7 +1,12 @@
-"""kvq_prefix_decode at the ends of what its arguments allow."""
+"""kvq_prefix_decode at the ends of its operands' ranges, against float64 attention
+under the softmax-weighted bound of tests/_prefix_bound.py."""
+import numpy as np
 import pytest
 import torch
 
+import oracle
+from tests import _helpers as H
+from tests import _prefix_bound as bound
 from tests import test_gpu_prefix_decode as base
 
 pytestmark = pytest.mark.gpu
@@ -19,6 +24,54 @@ def _lib():
     kvq = base.kvq = m
     yield
     assert kvq.kvq_device_errors() == 0
+
+
+def rows_of(s, b, h):
+    """q [d], k and v [n, d] of one row in float64, in the cache's basis."""
+    n = int(s.ctx[b])
+    t = np.arange(n)
+    kv = h // (s.hq // s.hkv)
+    k, v = (oracle.dequantize_cache_rows(s.oc, w, s.table[b][t // 16], t % 16)[:, kv] for w in "kv")
+    q = oracle.bf16_bits_to_f32(H.bits(s.q[b])).astype(np.float64)
+    if s.oc.rotation is not None:
+        q = oracle.rotate_query_fp64(q, s.oc.rotation)
+    return q[h], k, v
+
+
+def check(s, out, skip=()):
+    """Every row but those in `skip` inside its bound."""
+    got = out.float().cpu().numpy().astype(np.float64)
+    worst = 0.0
+    for b in range(len(s.ctx)):
+        for h in range(s.hq):
+            if (b, h) in skip:
+                continue
+            if s.ctx[b] == 0:
+                assert (got[b, h] == 0).all()
+                continue
+            o, err = bound.row_bound(*rows_of(s, b, h), rotated=s.oc.rotation is not None)
+            if s.oc.rotation is not None:
+                o, err = oracle.unrotate_output_fp64(o[None], s.oc.rotation)[0], np.full_like(err, err.sum() / s.d)
+            miss = np.abs(got[b, h] - o) / bound.rounded(o, err)
+            assert np.isfinite(got[b, h]).all() and miss.max() <= 1.0, (b, h, miss.max())
+            worst = max(worst, float(miss.max()))
+    print(f"[prefix] error / weighted bound {worst:.3f}")
+
+
+@pytest.mark.parametrize("k", ["int8", "fp8", "int4", "int8c"])
+@pytest.mark.parametrize("down", [30, 41, 50, 100])
+def test_tiny_queries_against_tiny_scales(k, down):
+    """Scores that vanish beside masked positions (the prefix ends inside a
+    tile): the mean of V, no NaN."""
+    s = base.Batch(k, "int8", groups=[(200, [201, 230, 150, 210, 199])], seed=32)
+    s.cache["k_scale"] *= 2.0 ** -down
+    s.oc.scales["k"] = s.cache["k_scale"].cpu().numpy()
+    s.q[0] = 0
+    s.q[1] *= 2.0 ** -90
+    s.q[2] *= 2.0 ** -60
+    s.q[3] *= 2.0 ** down                               # (scores of the usual size)
+    s.q[4, ::2] = 0
+    check(s, s.run())
 
 
 def test_the_default_stream_given_by_its_handle(monkeypatch):
