@@ -831,7 +831,7 @@ __device__ __noinline__ float stage_queries(const PrefixArgs &a, int from, uint3
     // 2^er brings m into [2^14, 2^15) (a subnormal m counts as 2^-127).  Below
     // 2^-86 the scores vanish anyway: er <= 100 keeps 2^er and c normal floats.
     const int er = min(14 + 127 - static_cast<int>(mb >> 23), 100);
-    const float f = pow2i(er);
+    const float f = mb < 0x7F800000u ? pow2i(er) : NAN;  // (an infinite row: no score is a number)
     if (lane == r) c = pow2i(-er);
     uint32_t h[CPL / 2];
 #pragma unroll
@@ -1060,9 +1060,11 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem,
     }
     __syncwarp();
     tmem_fence_after();
+    // Scores that are no numbers make l NaN and leave m alone: a state of any finite
+    // m carries it through the merge.
+    const float mz = l != l ? 0.f : m == -INFINITY ? m : m * c - kBias;
     // The scores' products are behind either B_O too, so Q is free to be written.
-    store_partial<D>(a, s, smem + L::q, tmem + lanes + 256, wg, live, r, m == -INFINITY ? m : m * c - kBias, l,
-                     F == kNoScale ? 0.f : pow2i(-F));
+    store_partial<D>(a, s, smem + L::q, tmem + lanes + 256, wg, live, r, mz, l, F == kNoScale ? 0.f : pow2i(-F));
     tmem_fence_before();
     // no warpgroup goes on while the other one reads O, or Q's place
     if (!s.two) asm volatile("bar.sync 1, 256;" ::: "memory");

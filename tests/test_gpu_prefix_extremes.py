@@ -74,6 +74,21 @@ def test_tiny_queries_against_tiny_scales(k, down):
     check(s, s.run())
 
 
+def test_non_finite_queries_stay_in_their_rows():
+    """A row that holds NaN or infinity comes back NaN, also where it ends inside
+    the prefix; the others are as they should be, and a padded row is 0 whatever it holds."""
+    s = base.Batch("fp8", "int8", groups=[(200, [150, 201, 0, 230, 333])], seed=33)
+    s.q[0, 1, 5] = float("nan")
+    s.q[1, 0] = float("nan")
+    s.q[2] = float("nan")
+    s.q[3, 2, 0] = float("inf")
+    s.q[4, 7, 127] = float("-inf")
+    out = s.run()
+    bad = [(0, 1), (1, 0), (3, 2), (4, 7)]
+    assert all(torch.isnan(out[b, h]).all() for b, h in bad)
+    check(s, out, skip=bad)
+
+
 def test_the_default_stream_given_by_its_handle(monkeypatch):
     """Handle 0 is the default stream: what the call makes is allocated there."""
     s = base.Batch(groups=[(300, [310, 320, 333])], seed=34)
