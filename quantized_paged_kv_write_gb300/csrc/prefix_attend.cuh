@@ -859,7 +859,11 @@ __device__ __noinline__ void store_partial(const PrefixArgs &a, const Segment &s
   } else {
     float4 *const x = reinterpret_cast<float4 *>(exchange);
     x[128 * wg + r] = make_float4(m, l, back, 0.f);
+    // each warpgroup has waited for its own products: the barrier passes on that
+    // they are complete
+    tmem_fence_before();
     asm volatile("bar.sync 1, 256;" ::: "memory");
+    tmem_fence_after();
     const float4 y0 = x[r], y1 = x[128 + r];
     m = fmaxf(y0.x, y1.x);
     // (a stream without weight, -inf, may have left anything in its O)
@@ -1067,7 +1071,10 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem,
     store_partial<D>(a, s, smem + L::q, tmem + lanes + 256, wg, live, r, mz, l, F == kNoScale ? 0.f : pow2i(-F));
     tmem_fence_before();
     // no warpgroup goes on while the other one reads O, or Q's place
-    if (!s.two) asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (!s.two) {
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      tmem_fence_after();
+    }
     x += tiles;
     n0 += tiles;
   }
