@@ -267,11 +267,12 @@ __global__ void __launch_bounds__(kMergeRows *SPLIT *D / 4, 1024 / (kMergeRows *
   const bool live = row < a.B * a.G;
   const int b = live ? row / a.G : 0, gq = live ? row - b * a.G : 0;
 
-  // ---- the row's partials.  First what the plan says: it has ended by the time
-  // this kernel can start, as the kernels before go on only after it.  CTAs are
-  // on their SMs some microseconds before the partials are there, and this is
-  // ~4700 cycles of dependent loads and cold code.
+  // ---- the row's partials.  What the plan says is read after the wait too: that
+  // it has ended by the time this kernel can start does not make it visible here
+  // (reading it before the wait took 1 us off a call).
+  grid_wait();
   const int gi = live ? a.ws_group[b] : -1;
+  const int total = a.sfx_cum[a.B], s0 = a.sfx_cum[b], s1 = live ? a.sfx_cum[b + 1] : 0;
   int n0 = 0, n1 = 0;
   const float2 *pml = reinterpret_cast<const float2 *>(a.ws_ml), *sml = reinterpret_cast<const float2 *>(a.sfx_ml);
   const float4 *po = reinterpret_cast<const float4 *>(a.ws_o), *qo = reinterpret_cast<const float4 *>(a.sfx_o);
@@ -286,8 +287,6 @@ __global__ void __launch_bounds__(kMergeRows *SPLIT *D / 4, 1024 / (kMergeRows *
     pml += slot + prow;
     po += static_cast<int64_t>(slot) * CG + cg * g.rows + prow;
   }
-  grid_wait();
-  const int total = a.sfx_cum[a.B], s0 = a.sfx_cum[b], s1 = live ? a.sfx_cum[b + 1] : 0;
   RowState s;
 #pragma unroll 1
   for (int i = sp; i < n0; i += U * SPLIT) {
