@@ -367,4 +367,16 @@ __device__ __forceinline__ float pow2i(int k) { return __int_as_float((k + 127) 
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A word in memory by which one kernel hands its results to a later one that does
+// not wait for the kernels between: all of a CTA's writes, a barrier of its
+// threads, then one thread's release; a thread that reads the token sees them.
+__device__ __forceinline__ void release_token(unsigned long long *word, unsigned long long token) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(word), "l"(token) : "memory");
+}
+__device__ __forceinline__ bool acquire_token(const unsigned long long *word, unsigned long long token) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(word) : "memory");
+  return v == token;
+}
+
 }  // namespace kvq

@@ -2,6 +2,8 @@
 // decoding, tensor-map encoding and kernel launches.  Nothing here computes
 // on the host; every step of the path runs in the kernels.
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 #include <mutex>
 #include <unordered_map>
 
@@ -657,7 +659,7 @@ int kvq_release_blocks(const int32_t *keep_lens, int32_t num_rows, int32_t *cont
 // plan and the prefix partials, each 256-aligned.
 struct PrefixWs {
   WsLayout sfx;
-  size_t groups, seqs, o, ml, total;
+  size_t groups, seqs, ready, o, ml, total;
 };
 
 static PrefixWs prefix_ws(int B, int Hq, int H, int D, int groups, int sfx_ctas, int ctas) {
@@ -667,10 +669,22 @@ static PrefixWs prefix_ws(int B, int Hq, int H, int D, int groups, int sfx_ctas,
   const size_t rows = 2 * static_cast<size_t>(B) * Hq + static_cast<size_t>(kPrefixRows) * ctas;
   w.groups = al(w.sfx.total);
   w.seqs = w.groups + al((static_cast<size_t>(groups) + 1) * sizeof(PrefixGroup));
-  w.o = w.seqs + al(4 * static_cast<size_t>(B) * sizeof(int));
+  w.ready = w.seqs + al(4 * static_cast<size_t>(B) * sizeof(int));
+  w.o = w.ready + al(sizeof(unsigned long long));
   w.ml = w.o + al(rows * D * sizeof(float));
   w.total = w.ml + al(rows * 2 * sizeof(float));
   return w;
+}
+
+// A word that no other call has and that a fresh workspace does not hold by
+// chance: a counter from the clock on, its bits mixed (xor-shifts and products by
+// odd numbers, which lose nothing).
+static unsigned long long call_token() {
+  static std::atomic<unsigned long long> next{
+      static_cast<unsigned long long>(std::chrono::system_clock::now().time_since_epoch().count())};
+  unsigned long long x = next.fetch_add(1, std::memory_order_relaxed);
+  for (int i = 0; i < 3; ++i) x = (x ^ (x >> 31)) * 0x9E3779B97F4A7C15ull;
+  return x ^ (x >> 31);
 }
 
 // CTAs of the prefix kernel: one per SM.
@@ -755,6 +769,8 @@ int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
   p.ws_ctx = p.ws_limit + batch;
   p.ws_off = p.ws_ctx + batch;
   p.ws_group = p.ws_off + batch;
+  p.ready = reinterpret_cast<unsigned long long *>(ws + wl.ready);
+  p.token = call_token();
   p.ws_o = reinterpret_cast<float *>(ws + wl.o);
   p.ws_ml = reinterpret_cast<float *>(ws + wl.ml);
   p.sfx_o = reinterpret_cast<float *>(ws + wl.sfx.o_off);
@@ -807,6 +823,8 @@ int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
 
   const bool prefix = num_groups > 0 && max_prefix_len >= kBlockSize;
   a.overlap = prefix ? 2 : 1;
+  a.ready = p.ready;
+  a.token = p.token;
   if (launch_prefix_plan(p, s) != cudaSuccess) return KVQ_ERR_CUDA;
   if (prefix && launch_prefix_attend(D, kf, vf, p, maps, s) != cudaSuccess) return KVQ_ERR_CUDA;
   if (launch_decode(D, kf, vf, a, plan, maps, s) != cudaSuccess) return KVQ_ERR_CUDA;

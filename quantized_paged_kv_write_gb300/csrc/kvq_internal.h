@@ -61,8 +61,11 @@ struct DecodeArgs {
   bool split_only = false;
   // In what order it is launched: 0 plainly; 1 while the kernel before it, which
   // writes ctx and tab_off, may still run; 2 while the kernel before it may still
-  // run, and ctx and tab_off are from an earlier one that has ended.
+  // run, and ctx and tab_off are from an earlier one that has ended and left
+  // `token` in `ready`.
   int overlap = 0;
+  const unsigned long long *ready = nullptr;
+  unsigned long long token = 0;
 };
 
 // Launches kern so that it may start while the stream's kernel before it still
@@ -188,6 +191,7 @@ struct PrefixArgs {
   int *ws_limit;                 // [B] shared positions that the sequence attends to
   int *ws_ctx, *ws_off;          // [B] suffix length, first suffix block
   int *ws_group;                 // [B] group or -1
+  unsigned long long *ready, token;  // the plan leaves the call's token here, the merge takes it out
   float *ws_o, *ws_ml;           // prefix partials: by (unit, CTA, stream) [D / 4][rows][4], and [rows, 2]
   const float *sfx_o, *sfx_ml;   // suffix partials (DecodeArgs::ws_o, ws_ml)
   const int *sfx_cum;            // suffix block counts, prefix sums

@@ -329,7 +329,9 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
 
   // Launched before the kernel before it has ended (a.overlap): the next one may
   // start when these CTAs have, and this grid ends after the one before, which
-  // at least one thread of every CTA waits for.
+  // at least one thread of every CTA waits for.  Lengths and table offsets are
+  // visible after the wait for the kernel that wrote them, or (overlap 2, another
+  // kernel between) once its token is seen; there is no waiting for the token.
   if (a.overlap == 1) grid_wait();
   grid_release();
   if (threadIdx.x == 0) {
@@ -342,6 +344,7 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
   // block counts per sequence (invalid contexts count as empty); eight loads of
   // a lane in flight, as their latency is most of a short call's start
   if (warp == 0) {
+    if (a.overlap == 2 && !acquire_token(a.ready, a.token)) grid_wait();
     constexpr int U = 8;
     int carry = 0;
     if (lane == 0) cum[0] = 0;

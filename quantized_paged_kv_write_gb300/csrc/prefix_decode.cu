@@ -161,6 +161,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
     a.ws_ctx[b] = c >= S ? c - S : c - cached;
     a.ws_off[b] = c >= S ? S / kBlockSize : 0;
   }
+  __syncthreads();
+  if (threadIdx.x == 0) release_token(a.ready, a.token);
 }
 
 // ---------------------------------------------------------------------------
@@ -271,6 +273,8 @@ __global__ void __launch_bounds__(kMergeRows *SPLIT *D / 4, 1024 / (kMergeRows *
   // it has ended by the time this kernel can start does not make it visible here
   // (reading it before the wait took 1 us off a call).
   grid_wait();
+  // the suffix's CTAs have read the token: none is left to the workspace's next call
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ready = 0;
   const int gi = live ? a.ws_group[b] : -1;
   const int total = a.sfx_cum[a.B], s0 = a.sfx_cum[b], s1 = live ? a.sfx_cum[b + 1] : 0;
   int n0 = 0, n1 = 0;
