@@ -749,7 +749,7 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
   int g = g0;
   int b = seq_of(cum, B, g0);
   int j = g0 - cum[b];
-  int ctx_b = __ldg(a.ctx + b);
+  int ctx_b = __ldcg(a.ctx + b);  // (written while this grid may be running)
   int gend = min(cum[b + 1], g1);  // where the current sequence piece ends
   start_segment(b);
 
@@ -1253,7 +1253,7 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
         ++b;
         while (cum[b + 1] == cum[b]) ++b;
         j = 0;
-        ctx_b = __ldg(a.ctx + b);
+        ctx_b = __ldcg(a.ctx + b);
         gend = min(cum[b + 1], g1);
         start_segment(b);
       }
