@@ -198,6 +198,8 @@ int kvq_decode_workspace_size(const kvq_format *fmt, int32_t batch, int32_t num_
  *
  *   q_bf16        [batch, num_q_heads, head_dim] BF16
  *   block_tables  [batch, max_blocks_per_seq] int32 physical block ids
+ *                 (max_blocks_per_seq < 2^27, in every call that takes one,
+ *                 else KVQ_ERR_UNSUPPORTED: positions count in 32 bits)
  *   context_lens  [batch] int32, tokens attended per sequence (0 -> out = 0)
  *   max_context_len  host-side upper bound of context_lens (sizes the work
  *                 split; a larger device value sets KVQ_DEVERR_CONTEXT_RANGE
@@ -376,8 +378,7 @@ typedef struct {
  * Each is one launch; it may be captured and replayed.  The pool, tables and
  * lengths are read and written by one call at a time (order calls on streams).
  * num_rows <= 8192, max_blocks_per_seq < 2^27 and num_rows *
- * max_blocks_per_seq <= 2^31 - 2^16, else KVQ_ERR_UNSUPPORTED: a row's positions
- * and the table's entries count in 32 bits.  Pointers of int32 arrays need
+ * max_blocks_per_seq <= 2^31 - 2^16, else KVQ_ERR_UNSUPPORTED.  Pointers of int32 arrays need
  * 4-byte, of slot_mapping 8-byte alignment.
  */
 int kvq_assign_blocks(const int32_t *new_lens, int32_t num_rows, int32_t *context_lens,

@@ -354,6 +354,9 @@ int kvq_decode_workspace_size(const kvq_format *fmt, int32_t batch, int32_t num_
   return KVQ_OK;
 }
 
+// The kernels count a sequence's positions in 32 bits.
+constexpr int32_t kMaxRowBlocks = 1 << 27;
+
 // The decode entry points with a caller workspace; k_new / v_new non-null
 // fuse the write of each sequence's new token (kvq_write_decode).
 static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, const kvq_format *fmt,
@@ -385,7 +388,8 @@ static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
       (reinterpret_cast<uintptr_t>(context_lens) & 3u))
     return KVQ_ERR_INVALID_ARG;
   if (max_blocks_per_seq < 1 || max_context_len < 0) return KVQ_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(batch) * max_blocks_per_seq >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  if (max_blocks_per_seq >= kMaxRowBlocks || static_cast<int64_t>(batch) * max_blocks_per_seq >= (int64_t(1) << 31))
+    return KVQ_ERR_UNSUPPORTED;
   if (fmt->num_blocks < 1 || fmt->num_blocks >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   const int H = fmt->num_kv_heads, D = fmt->head_dim, G = num_q_heads / H;
   DecodePlan plan;
@@ -494,7 +498,8 @@ int kvq_kivi_append(const void *k_new_bf16, const void *v_new_bf16, int32_t batc
       !aligned16(scales.v_scale) || (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
       (reinterpret_cast<uintptr_t>(context_lens) & 3u))
     return KVQ_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(batch) * max_blocks_per_seq >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  if (max_blocks_per_seq >= kMaxRowBlocks || static_cast<int64_t>(batch) * max_blocks_per_seq >= (int64_t(1) << 31))
+    return KVQ_ERR_UNSUPPORTED;
   unsigned int *err = nullptr;
   if (error_word(&err) != cudaSuccess) return KVQ_ERR_CUDA;
   KiviAppendArgs a;
@@ -584,10 +589,9 @@ int kvq_prefetch_blocks(const kvq_format *fmt, kvq_caches host_caches, kvq_scale
   return launch_prefetch(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
-// The kernels count a row's positions and the tables' entries in 32 bits, and
-// step past the last entry by less than 2^16.
+// ... and step past a pool table's last entry by less than 2^16.
 static bool table_fits(int32_t rows, int32_t max_blocks) {
-  return max_blocks < (1 << 27) && static_cast<int64_t>(rows) * max_blocks <= (int64_t(1) << 31) - (1 << 16);
+  return max_blocks < kMaxRowBlocks && static_cast<int64_t>(rows) * max_blocks <= (int64_t(1) << 31) - (1 << 16);
 }
 
 static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -718,6 +722,7 @@ int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
                       const int32_t *prefix_lens, int32_t num_groups, int32_t max_prefix_len, const void *res_k_bf16,
                       const void *res_v_bf16, void *out_bf16, void *workspace, size_t workspace_bytes,
                       kvq_stream_t stream) {
+  if (max_blocks_per_seq >= kMaxRowBlocks) return KVQ_ERR_UNSUPPORTED;
   int kf = 0, vf = 0, sms = 0;
   DecodePlan plan;
   int st = prefix_plan(fmt, batch, num_q_heads, num_groups, &kf, &vf, &plan, &sms);

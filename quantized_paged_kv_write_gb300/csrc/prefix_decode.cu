@@ -43,6 +43,7 @@ __device__ __noinline__ int cta_of(int x, int T, int P) {
 // plan
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
+constexpr int kMaxShared = INT_MAX - 255;  // so that the last tile's end counts in 32 bits, too
 
 // One CTA: a chain of dependent loads and a few barriers.  The records of up to
 // kPlanGroups groups stay in shared memory between the steps.
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixA
     if (lane == 0) {
       // no further than the longest sequence: past it nothing was written; a
       // prefix of one sequence is that sequence's own
-      const int S = range && len && en - st >= 2 ? min(pl, most) / kBlockSize * kBlockSize : 0;
+      const int S = range && len && en - st >= 2 ? min(min(pl, most), kMaxShared) / kBlockSize * kBlockSize : 0;
       const int R = S > 0 ? (en - st) * a.G : 0;
       PrefixGroup r;
       r.start = st;

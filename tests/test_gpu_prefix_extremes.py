@@ -89,6 +89,30 @@ def test_non_finite_queries_stay_in_their_rows():
     check(s, out, skip=bad)
 
 
+def test_the_longest_context():
+    """2^31 - 16 positions, all in one block: its 16 tokens' softmax.  FP32 sums of
+    2^31 terms: a stream of a CTA (one of 304) adds 2^24 / 304 tiles, eight times
+    each, every addition off by up to 2^-23 of what it has: 441505 2^-23 = 0.053 of A
+    for the outputs, an eighth of it for l."""
+    width, d = 2 ** 27 - 1, 64
+    fmt = kvq.cache_format(base.INT8, base.INT8, 1, d, 1)
+    cache = kvq.allocate_cache(fmt)
+    gen = torch.Generator(device="cuda").manual_seed(35)
+    x = torch.randn((2, 16, 1, d), generator=gen, device="cuda").to(torch.bfloat16)
+    q = torch.randn((2, 2, d), generator=gen, device="cuda").to(torch.bfloat16)
+    kvq.kvq_quantize_write(x[0], x[1], torch.arange(16, device="cuda"), fmt, cache)
+    table = torch.zeros((2, width), dtype=torch.int32, device="cuda")
+    n = 16 * width
+    i32 = lambda y: torch.tensor(y, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = kvq.kvq_prefix_decode(q, fmt, cache, table, i32([n, n]), n, i32([0, 2]), i32([2 ** 31 - 1]), 2 ** 31 - 1)
+    torch.cuda.synchronize()
+    k, v = ((cache[w + "_cache"].view(torch.int8).double() * cache[w + "_scale"].double()[..., None])[0, :, 0]
+            for w in "kv")
+    p = torch.softmax(q.double() @ k.t() / d ** 0.5, -1)
+    want, a = p @ v, p @ v.abs()
+    assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + (0.053 * 9 / 8 + 2.0 ** -9) * a).all()
+
+
 def test_the_default_stream_given_by_its_handle(monkeypatch):
     """Handle 0 is the default stream: what the call makes is allocated there."""
     s = base.Batch(groups=[(300, [310, 320, 333])], seed=34)

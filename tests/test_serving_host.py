@@ -102,3 +102,16 @@ def test_lengths_of_two_columns_are_refused_by_the_binding():
         kvq.kvq_assign_blocks(t, i, t, pool, 4)
     with pytest.raises(ValueError, match=r"keep_lens and context_lens must be \[R\]"):
         kvq.kvq_release_blocks(t, i, t, pool)
+
+
+def test_decodes_refuse_tables_whose_positions_pass_32_bits(lib):
+    c, s = kvq._Caches(BUF, BUF), kvq._Scales(BUF, BUF)
+    f, g = _fmt(), _fmt(k_gran=2)
+    for width in (1 << 27, (1 << 28) + 5, (1 << 31) - 1):
+        assert _decode(lib, batch=1, width=width) == kvq.KVQ_ERR_UNSUPPORTED
+        assert lib.kvq_paged_decode(BUF, 1, 32, ctypes.byref(f), c, s, BUF, width, BUF, 64, BUF, BUF, 1 << 20,
+                                    None) == kvq.KVQ_ERR_UNSUPPORTED
+        assert lib.kvq_kivi_decode(BUF, 1, 32, ctypes.byref(g), c, s, BUF, width, BUF, 64, BUF, BUF, BUF, BUF, 1 << 20,
+                                   None) == kvq.KVQ_ERR_UNSUPPORTED
+        assert lib.kvq_kivi_append(BUF, BUF, 1, ctypes.byref(g), c, s, BUF, width, BUF, BUF, BUF,
+                                   None) == kvq.KVQ_ERR_UNSUPPORTED
