@@ -1,5 +1,6 @@
-"""kvq_prefix_decode at the ends of its operands' ranges, against float64 attention
-under the softmax-weighted bound of tests/_prefix_bound.py."""
+"""kvq_prefix_decode on long prefixes and at the ends of its operands' ranges, against
+float64 attention under the softmax-weighted bound of tests/_prefix_bound.py, which
+sees a lost tile."""
 import numpy as np
 import pytest
 import torch
@@ -56,6 +57,16 @@ def check(s, out, skip=()):
             assert np.isfinite(got[b, h]).all() and miss.max() <= 1.0, (b, h, miss.max())
             worst = max(worst, float(miss.max()))
     print(f"[prefix] error / weighted bound {worst:.3f}")
+
+
+@pytest.mark.parametrize("k,v,hq,hkv,prefix,n,rot", [
+    ("fp8", "fp8", 8, 2, 5003, 3, False), ("int8", "int8", 4, 1, 5003, 40, False), ("int8c", "int4g", 16, 2, 4999, 4, False),
+    ("int2c", "int2g", 8, 1, 4100, 3, False), ("int4", "int4g", 8, 1, 3001, 3, True), ("fp8", "int4g", 8, 1, 2900, 40, False),
+    ("int8", "fp8", 6, 3, 500, 5, False)])
+def test_long_prefixes_under_the_weighted_bound(k, v, hq, hkv, prefix, n, rot):
+    s = base.Batch(k, v, hq=hq, hkv=hkv, groups=[(prefix, [prefix + 3 * i for i in range(n)])], rot=rot, seed=31,
+                   outliers=False)
+    check(s, s.run())
 
 
 @pytest.mark.parametrize("k", ["int8", "fp8", "int4", "int8c"])
