@@ -256,6 +256,19 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor of a call's own, allocated on the stream that the call runs on:
+    its memory is neither still in use on another one, nor given away while the
+    call runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        # (torch takes handle 0, the default stream, for "any stream")
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _caches(c: dict) -> tuple:
     return (_Caches(_ptr(c["k_cache"], torch.uint8, "k_cache"), _ptr(c["v_cache"], torch.uint8, "v_cache")),
             _Scales(_ptr(c["k_scale"], torch.float32, "k_scale"), _ptr(c["v_scale"], torch.float32, "v_scale")))
@@ -312,10 +325,10 @@ def kvq_paged_decode(q: torch.Tensor, fmt: CacheFormat, cache: dict, block_table
     if d != fmt.head_dim:
         raise ValueError("q head_dim does not match the cache format")
     if out is None:
-        out = torch.empty((bsz, hq, d), dtype=torch.float32, device=q.device)
+        out = _empty((bsz, hq, d), torch.float32, q.device, stream)
     if workspace is None:
         nbytes = kvq_decode_workspace_size(fmt, bsz, hq, max_context_len)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     if block_tables.dim() != 2 or block_tables.shape[0] != bsz or context_lens.shape != (bsz,):
         raise ValueError("block_tables must be [B, max_blocks] and context_lens [B]")
     cf = fmt.as_c()
@@ -346,10 +359,10 @@ def kvq_write_decode(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, 
     if tuple(k_new.shape) != want or tuple(v_new.shape) != want:
         raise ValueError(f"k_new and v_new must be {list(want)}")
     if out is None:
-        out = torch.empty((bsz, hq, d), dtype=torch.float32, device=q.device)
+        out = _empty((bsz, hq, d), torch.float32, q.device, stream)
     if workspace is None:
         nbytes = kvq_decode_workspace_size(fmt, bsz, hq, max_context_len)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     if block_tables.dim() != 2 or block_tables.shape[0] != bsz or context_lens.shape != (bsz,):
         raise ValueError("block_tables must be [B, max_blocks] and context_lens [B]")
     cf = fmt.as_c()
@@ -422,10 +435,10 @@ def kvq_kivi_decode(q: torch.Tensor, fmt: CacheFormat, cache: dict, block_tables
     lib = load_library()
     bsz, hq, d = (int(x) for x in q.shape)
     if out is None:
-        out = torch.empty((bsz, hq, d), dtype=torch.float32, device=q.device)
+        out = _empty((bsz, hq, d), torch.float32, q.device, stream)
     if workspace is None:
         nbytes = kvq_decode_workspace_size(fmt, bsz, hq, max_context_len)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     cf = fmt.as_c()
     caches, scales = _caches(cache)
     st = lib.kvq_kivi_decode(_ptr(q, torch.bfloat16, "q"), bsz, hq, ctypes.byref(cf), caches, scales,
@@ -459,19 +472,6 @@ def kvq_prefetch_blocks(host_pool: dict, src_blocks: torch.Tensor, dst_blocks: t
                                  n, caches, scales, _stream(stream))
     if st != KVQ_OK:
         raise KvqError(st, "kvq_prefetch_blocks")
-
-
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """A tensor of a call's own, allocated on the stream that the call runs on:
-    its memory is neither still in use on another one, nor given away while the
-    call runs."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        # (torch takes handle 0, the default stream, for "any stream")
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def allocate_pool(num_blocks: int, device="cuda") -> dict:
