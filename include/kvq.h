@@ -420,7 +420,10 @@ int kvq_release_blocks(const int32_t *keep_lens, int32_t num_rows, int32_t *cont
  * their row's largest are exact); products, softmax statistics and partial
  * outputs are FP32, and the output is rounded once to BF16 (2^-8).
  * A group of fewer than two sequences shares nothing and costs what
- * kvq_paged_decode costs.  A prefix_lens entry outside [0, max_prefix_len]
+ * kvq_paged_decode costs.  Any other is shared, however short its prefix, which
+ * has a fixed cost: kvq_paged_decode is the faster call below about 2000 shared
+ * positions with 2 to 8 sequences, 1000 with 32 and 500 with 128 (FP8 and INT4,
+ * 32 query heads on 8).  A prefix_lens entry outside [0, max_prefix_len]
  * (KVQ_DEVERR_CONTEXT_RANGE) and groups out of order
  * (KVQ_DEVERR_GROUP_RANGE) are decoded without sharing; other errors as
  * kvq_paged_decode.  num_groups <= 8192 (0: group_starts, prefix_lens may be

@@ -9,12 +9,14 @@
 //
 // What bounds it: latency.  A decode step of 256 rows moves 7 KB.  So each
 // call is one launch of one thread-block cluster: every CTA scans all rows
-// into its own shared memory (two running sums), the CTAs share the writing,
-// and a cluster barrier orders the in-place updates after everybody's reads,
-// where a second launch or a counter in memory would cost more than the work.
-// Measured: 5.8 us for one token of 256 rows, 9.6 us for 64 x 4097 tokens (3.1 MB
-// written), 12 us for giving back 256 rows' drafts, 9 and 35 us for taking up
-// and giving back 64 rows behind 2048 shared blocks.
+// into its own shared memory (two running sums), the CTAs share the rest of the
+// checks and the writing, and a cluster barrier orders the in-place updates after
+// everybody's reads, where a second launch or a counter in memory would cost more
+// than the work.  Measured: 6.4 us for one token of 256 rows, 11.8 us for 64 x
+// 4097 tokens (3.1 MB written), 12 us for giving back 256 rows' drafts, 12.6 and
+// 35 us for taking up and giving back 64 rows behind 2048 shared blocks.  Of this
+// the look at all blocks to be shared or taken before the first write is 0.5, 2
+// and 4 us of the three assignments.
 #include <limits.h>
 
 #include "common.cuh"
@@ -533,7 +535,9 @@ cudaError_t launch_cluster(void (*kern)(const Args), const Args &a, int ctas, si
 
 // One CTA per 4096 items of work, up to the largest cluster: scattered accesses
 // to the counts bound large calls, and so the SMs that make them (release of 64
-// rows behind 2048 shared blocks: 8 CTAs 73 us, 16 CTAs 41 us).
+// rows behind 2048 shared blocks, all of them given back: 8 CTAs 73 us, 16 CTAs
+// 41 us).  What a release gives back is known on the device only: the host counts
+// the tables' width, so that a rollback in a wide table takes the large form too.
 int cluster_for(int64_t items) {
   int c = 1;
   while (c < 16 && static_cast<int64_t>(c) * 4096 < items) c *= 2;

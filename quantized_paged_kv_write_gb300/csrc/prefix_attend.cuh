@@ -29,7 +29,7 @@
 // P overwrites S in tensor memory and is the A operand of the second product.
 //
 // What bounds it.  27 sequences, 32 query heads on 8, FP8 K and V, 32003 shared
-// positions: 34 us, 66 MB of codes and scales at 1.9 TB/s.  A tile takes ~3450
+// positions: 35 us, 66 MB of codes and scales at 1.9 TB/s.  A tile takes ~3450
 // cycles of an SM, of which the converters' chains (load, decode, scale, store)
 // are busy for ~3100; twice the converter warps at fewer registers gained
 // nothing (36 us).  100 sequences, 64 query heads on 8, INT2 K and V, 65536
