@@ -414,11 +414,12 @@ int kvq_release_blocks(const int32_t *keep_lens, int32_t num_rows, int32_t *cont
  *                 GPU (streams, captured graphs) need two
  *
  * The result is kvq_paged_decode's (kvq_kivi_decode's with a tail) but for
- * the prefix's operands: queries, probabilities and scaled codes enter the
- * matrix products as f16, rounded once (at most a relative 2^-11 each, with
- * the row's or tile's power of two taken out; BF16 queries down to 2^-32 of
- * their row's largest are exact); products, softmax statistics and partial
- * outputs are FP32, and the output is rounded once to BF16 (2^-8).
+ * the prefix's operands: probabilities, V codes times their scales, per-channel K
+ * codes times theirs and rotated queries enter the matrix products as f16,
+ * rounded once (at most a relative 2^-11 each, with the row's or tile's power of
+ * two taken out).  Other queries (BF16, down to 2^-32 of their row's largest) and
+ * per-token K codes are exact; products, scales of scores, softmax statistics and
+ * partial outputs are FP32, and the output is rounded once to BF16 (2^-8).
  * A group of fewer than two sequences shares nothing and costs what
  * kvq_paged_decode costs.  Any other is shared, however short its prefix, which
  * has a fixed cost: kvq_paged_decode is the faster call below about 2000 shared

@@ -4,17 +4,20 @@
 // Mathematics.  For the rows of a unit (256 or 128 (sequence, query head)
 // pairs of one kv head) and a tile of 128 shared positions:
 //   S = Q' K'^T          f16 operands, FP32 accumulators in tensor memory
-//   z = S 2^-eb c        c the row's factor (z in log2 units)
+//   t = S s 2^eb         scales per position; scales per channel are in K'
+//   z = t 2^-eb c        c the row's factor (z in log2 units)
 //   p = 2^(z - m + 8), l += p, O += p V'
 // Q' = q 2^er in f16 (the row's largest in [2^14, 2^15): a BF16 q is exact
-// down to 2^-32 of it).  K' = code * s 2^eb and V' = code * s 2^F, each rounded to
-// f16 once: scales per position multiplied into the scores and probabilities
-// instead would keep the codes exact, but every thread then reads all 128 of
-// them from shared memory, whose bandwidth bounds the kernel (the products read
-// their operands there).  Powers of two keep K' and V' below 2^15: eb by tile; F
-// falls when a tile's scales need it and O follows, as it does when m is
-// raised (only past m + 6, so p <= 2^14).  p is rounded to f16 once; l sums the
-// unrounded p.
+// down to 2^-32 of it; a rotated one is rounded once).  K' is the codes themselves
+// where a position has one scale: it multiplies the score in FP32, and t goes back
+// to where S was.  A rounding of K' would move a score by up to 2^-11 of sum |q k|,
+// which the softmax raises: with K outliers, whole tenths of an output (K' = code *
+// s in f16 was 2 % slower for 27 sequences, FP8, 2 to 10 % faster for 256 and 64
+// sequences, whose softmax is the longer chain).  With scales per channel K' = code
+// * s 2^eb, and V' = code * s 2^F, are rounded to f16 once.  Powers of two keep t
+// in range and K' and V' below 2^15: eb by tile; F falls when a tile's scales need
+// it and O follows, as it does when m is raised (only past m + 6, so p <= 2^14).
+// p is rounded to f16 once; l sums the unrounded p.
 //
 // Roles, one CTA per SM: two softmax warpgroups (thread = row), two
 // warpgroups that turn codes into f16 tiles in shared memory (one K, one V),
@@ -85,7 +88,7 @@ struct Smem {
   static constexpr uint32_t HALF = 128 * 128;           // 64 channels of 128 rows
   static constexpr uint32_t TILE = HALF * (D / 64);
   static constexpr uint32_t CHAN = kTileBlocks * D * 2; // one part (high or low) of the channel scales
-  static constexpr uint32_t POS = kTile * 4;            // scales per position, f16 pairs (high, low)
+  static constexpr uint32_t POS = kTile * 4;            // scales per position, f16 pairs (high, low) or FP32
   static constexpr uint32_t GRP = POS * (D / 32);       // and per position and group
   static constexpr uint32_t k = 0;                      // [2] stages
   static constexpr uint32_t v = k + 2 * TILE;           // [2] stages
@@ -96,7 +99,9 @@ struct Smem {
   static constexpr uint32_t tmem = bars + 56 * 8;       // tensor memory address, then the abort flag
   static constexpr uint32_t factors = tmem + 16;        // [128] row factors
   static constexpr uint32_t segment = factors + 512;    // the CTA's first segment
-  static constexpr uint32_t scales = segment + 96;      // [2] scales of K, then [2] of V, as f16 pairs
+  // scales of K: [2] f16 pairs per channel, or [kMeta] FP32 per position; then
+  // [2] of V, f16 pairs
+  static constexpr uint32_t scales = segment + 96;
   static_assert(scales % 16 == 0, "small arrays");
 };
 
@@ -113,7 +118,7 @@ inline Layout layout_of(bool chan, bool group, bool two, int krow, int vrow) {
   using L = Smem<D>;
   Layout y;
   y.small = L::q + (two ? 2 : 1) * L::TILE;
-  y.vscales = chan ? 4 * L::CHAN : 2 * L::POS;
+  y.vscales = chan ? 4 * L::CHAN : kMeta * L::POS;
   y.ring[0] = (y.small + L::scales + y.vscales + 2 * (group ? L::GRP : L::POS) + 1023) & ~1023u;
   // Units of up to 8 KB, fewer to wait for; of 4 KB where two row tiles leave
   // little room.  As many as fit, shared out by the bytes of a row.
@@ -369,10 +374,7 @@ __device__ __forceinline__ void convert_k_role(uint32_t base, const Layout &y, c
         const uint32_t p = scales + st * 2 * L::CHAN + (blk * D + 8 * piece) * 2;
         const uint4 hi = lds128(p);
         apply_scales<KC::code>(r, hi, KC::code == C_INT2 ? hi : lds128(p + L::CHAN));
-      } else {
-        const ScalePair z(lds32(scales + st * L::POS + (f.k0 + F::STEP * i) * 4));
-        apply_scales<KC::code>(r, z.hi, z.lo);
-      }
+      }  // (scales per position: the softmax has them)
     });
     fence_proxy_async_shared();
     __syncwarp();
@@ -522,8 +524,9 @@ __device__ __forceinline__ void load_role(const PrefixArgs &a, const CUtensorMap
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
-// Two warps: the scales of K 2^eb and of V 2^F as pairs of f16 (high and low
-// part), for the converters; F, the block mask and 2^-eb, for the softmax.  Lane
+// Two warps: the scales of K 2^eb, per position in FP32 for the softmax or per
+// channel, and of V 2^F as pairs of f16 (high and low part), for the converters; F,
+// the block mask and 2^-eb, for the softmax.  Lane
 // l has the positions 4 l .. 4 l + 3.  Tile n is written while the loads of n + 1
 // are under way, and the ids of n + 2; one copy of each part.
 
@@ -593,9 +596,8 @@ __device__ __forceinline__ void scale_k_role(const PrefixArgs &a, uint32_t base,
           if constexpr (LOW) sts64(p + 256 * i + L::CHAN, l0, l1);
         }
       } else {
-        uint32_t z[4];
-        pair_scales<LOW>(sk[0], f, z);
-        sts128(to + st * L::POS + 16 * lane, z[0], z[1], z[2], z[3]);
+        sts128(to + n % kMeta * L::POS + 16 * lane, __float_as_uint(sk[0][0] * f), __float_as_uint(sk[0][1] * f),
+               __float_as_uint(sk[0][2] * f), __float_as_uint(sk[0][3] * f));
       }
       if (lane == 0) sts32(small + L::info + (n % kMeta) * 16 + 8, __float_as_uint(pow2i(-eb)));
       __syncwarp();
@@ -900,7 +902,8 @@ __device__ __noinline__ void store_partial(const PrefixArgs &a, const Segment &s
   if (live && (s.two || wg == 0)) *reinterpret_cast<float2 *>(a.ws_ml + (slot + r) * 2) = make_float2(m, l);
 }
 
-template <int D>
+// SCALED: a scale per position, which the scores take; else K' has them.
+template <int D, bool SCALED>
 __device__ __forceinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem, const Layout &y0, const Waiter &wait,
                                              uint32_t tmem, const Segments &sg, int x, int x1) {
   using L = Smem<D>;
@@ -938,7 +941,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem,
     const int limit = live ? __ldcg(a.ws_limit + b) : s.g.shared;
     const int nearest = __reduce_min_sync(0xffffffffu, limit);
 
-    float m = -INFINITY, l = 0.f;  // m as a value of t
+    float m = -INFINITY, l = 0.f;  // m as a value of t 2^-eb
     int F = kNoScale;
     bool begun = false, huge = false;
     for (int k = s.two ? 0 : wg; k < tiles; k += s.two ? 1 : 2) {
@@ -948,6 +951,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem,
       ++ns;
       tmem_fence_after();
       const uint4 info = lds128(base + y0.small + L::info + slot * 16);
+      const uint32_t scales = base + y0.small + L::scales + slot * L::POS;
       const int Ft = static_cast<int>(info.x);
       const float k0 = __uint_as_float(info.z);
       const int seen = limit - (s.t0 + k) * kTile;  // positions of the tile that the row attends to
@@ -956,7 +960,7 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem,
       // unrolled, the roles' code does not fit the instruction caches, and
       // fetching it bounds the kernel.
       //
-      // ---- the row's largest t = S 2^-eb (masked scores become -inf in place)
+      // ---- t in place of S (masked: -inf), and the row's largest t 2^-eb
       float top = -INFINITY;
       auto largest = [&](auto tag) {
         constexpr bool MASK = decltype(tag)::value;
@@ -966,20 +970,33 @@ __device__ __forceinline__ void softmax_role(const PrefixArgs &a, uint8_t *smem,
           uint32_t w[32];
           tmem_ld32(S + 32 * cc, w);
           tmem_wait_ld(w);
+          if constexpr (SCALED) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const uint4 z = lds128(scales + 4 * (32 * cc + e));
+              float a0, a1, a2, a3;
+              mul_f32x2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]), __uint_as_float(z.x), __uint_as_float(z.y), a0, a1);
+              mul_f32x2(__uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]), __uint_as_float(z.z), __uint_as_float(z.w), a2, a3);
+              w[e] = __float_as_uint(a0);
+              w[e + 1] = __float_as_uint(a1);
+              w[e + 2] = __float_as_uint(a2);
+              w[e + 3] = __float_as_uint(a3);
+            }
+          }
           if constexpr (MASK) {
             const uint32_t in = info.y >> (2 * cc);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (32 * cc + e >= seen || !((in >> (e / kBlockSize)) & 1u)) w[e] = 0xFF800000u;
-            tmem_st32(S + 32 * cc, w);
           }
+          if constexpr (MASK || SCALED) tmem_st32(S + 32 * cc, w);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             t0 = max3(t0, __uint_as_float(w[e]), __uint_as_float(w[e + 1]));
             t1 = max3(t1, __uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]));
           }
         }
-        if constexpr (MASK) tmem_wait_st();
+        if constexpr (MASK || SCALED) tmem_wait_st();
         top = fmaxf(t0, t1) * k0;
       };
       if (masked) largest(std::true_type{}); else largest(std::false_type{});
@@ -1135,7 +1152,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = warp == kLoadWarp ? 0 : 1;
     load_role(a, r ? &vmap : &kmap, r ? vrow : krow, r, base, y, wait, sg, x, x1);
   } else if (warp >= kSoftmaxWarp) {
-    softmax_role<D>(a, smem, y, wait, tmem, sg, x, x1);
+    if (chan) softmax_role<D, false>(a, smem, y, wait, tmem, sg, x, x1);
+    else softmax_role<D, true>(a, smem, y, wait, tmem, sg, x, x1);
   } else if (warp >= kVWarp) {
     if (vf == V_INT8_TOK) convert_v_role<D, V_INT8_TOK>(base, y, wait, tiles);
     else if (vf == V_FP8_TOK) convert_v_role<D, V_FP8_TOK>(base, y, wait, tiles);

@@ -50,7 +50,7 @@ def check(s, out, skip=()):
             if s.ctx[b] == 0:
                 assert (got[b, h] == 0).all()
                 continue
-            o, err = bound.row_bound(*rows_of(s, b, h), rotated=s.oc.rotation is not None)
+            o, err = bound.row_bound(*rows_of(s, b, h), roundings=int(s.fmt.k_gran == "block_channel" or s.oc.rotation is not None))
             if s.oc.rotation is not None:
                 o, err = oracle.unrotate_output_fp64(o[None], s.oc.rotation)[0], np.full_like(err, err.sum() / s.d)
             miss = np.abs(got[b, h] - o) / bound.rounded(o, err)
@@ -66,6 +66,16 @@ def check(s, out, skip=()):
 def test_long_prefixes_under_the_weighted_bound(k, v, hq, hkv, prefix, n, rot):
     s = base.Batch(k, v, hq=hq, hkv=hkv, groups=[(prefix, [prefix + 3 * i for i in range(n)])], rot=rot, seed=31,
                    outliers=False)
+    check(s, s.run())
+
+
+@pytest.mark.parametrize("k,v,d,rows", [("fp8", "fp8", 128, 20), ("int8", "int8", 128, 40), ("int4", "int4g", 128, 20),
+                                        ("int8", "fp8", 64, 40), ("fp8", "int4g", 64, 20), ("int4", "int8", 64, 20)])
+def test_per_token_k_codes_are_exact_under_outliers(k, v, d, rows):
+    """Scores of hundreds, from outlier channels and tokens: a rounding of K would
+    move them by tenths."""
+    s = base.Batch(k, v, hq=16, hkv=2, d=d, groups=[(600, [600 + 5 * i for i in range(rows)])], seed=36)
+    s.q *= 4
     check(s, s.run())
 
 
