@@ -32,17 +32,18 @@
 // P overwrites S in tensor memory and is the A operand of the second product.
 //
 // What bounds it.  27 sequences, 32 query heads on 8, FP8 K and V, 32003 shared
-// positions: 35 us, 66 MB of codes and scales at 1.9 TB/s.  A tile takes ~3450
-// cycles of an SM, of which the converters' chains (load, decode, scale, store)
-// are busy for ~3100; twice the converter warps at fewer registers gained
-// nothing (36 us).  100 sequences, 64 query heads on 8, INT2 K and V, 65536
-// positions: 264 us, 0.81 PFLOP/s, a two-row-tile step in ~4450 cycles, 2080 of
-// them products; the rest is the chain S - softmax - P V of a warpgroup, whose
-// single S buffer (tensor memory is full: two S, two O) keeps its next S waiting
-// for its P V.  Halves of S to overlap them made products of 64 columns, which
-// shared memory's bandwidth slows (288 us).  Measured on the way: out-of-line
-// roles, which reload their parameters after every barrier, 46 instead of 41 us
-// (first shape); one load warp for both rings 41 instead of 34 us.
+// positions: 35 us, 66 MB of codes and scales at 1.9 TB/s.  A tile takes ~3500
+// cycles of an SM, most of them the converters' chains (load, decode, V: scale,
+// store); twice the converter warps at fewer registers gained nothing.  100
+// sequences, 64 query heads on 8, INT2 K and V, 65536 positions: 254 us, 0.85
+// PFLOP/s, a two-row-tile step in ~4280 cycles, 2080 of them products; the rest is
+// the chain S - softmax - P V of a warpgroup, whose single S buffer (tensor memory
+// is full: two S, two O) keeps its next S waiting for its P V.  Halves of S to
+// overlap them made products of 64 columns, which shared memory's bandwidth slows
+// (9 % more time).  Measured on the way: out-of-line roles, which reload their
+// parameters after every barrier, 46 instead of 41 us (first shape); one load warp
+// for both rings 41 instead of 34 us; scales read again for the exponentials
+// instead of t stored 64.0 instead of 61.9 us for the whole call.
 #pragma once
 
 #include <limits.h>

@@ -15,7 +15,7 @@
 // launched while the one before runs; one after the other they took 7 to 12 us
 // more.  27 sequences, 32 query heads on 8, FP8, 32003 shared positions and
 // 1000 of each one's own: plan 4 us, attention 35, then 14 for the suffixes
-// (55 MB) and 12 for the merge, 65 in all.
+// (55 MB) and 12 for the merge, 66 in all.
 #include <limits.h>
 
 #include <atomic>
