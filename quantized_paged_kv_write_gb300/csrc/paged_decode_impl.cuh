@@ -384,8 +384,10 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
 
   const int total = cum[B];
   const int c = blockIdx.x;
-  int P = a.nctas;
-  if (a.blocks_per_cta > 0) P = min(P, max(1, (total + a.blocks_per_cta - 1) / a.blocks_per_cta));
+  // no CTA between two that have blocks is left without one: the reduce reads
+  // the partials of all of them
+  const int per = max(1, a.blocks_per_cta);
+  const int P = min(a.nctas, max(1, (total + per - 1) / per));
   if (c >= P) {
     grid_wait();
     return;
@@ -1283,7 +1285,7 @@ __global__ void __launch_bounds__(256) decode_reduce_kernel(const DecodeArgs a, 
   float mx = -INFINITY;
   if (c1b > c0b) {
     const int total = cum[a.B];
-    const int P = a.nctas;
+    const int P = min(a.nctas, total);  // as the split
     // CTA holding global block x: min(P - 1, floor(((x + 1) P - 1) / total))
     auto cta_of = [&](int x) -> int {
       const int64_t v = ((static_cast<int64_t>(x) + 1) * P - 1) / total;
