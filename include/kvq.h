@@ -111,7 +111,8 @@ enum {
                                          range, a block given back more often than held,
                                          an append into a block that other rows share      */
   KVQ_DEVERR_GROUP_RANGE = 1u << 7    /* kvq_prefix_decode: group_starts out of order or
-                                         outside [0, batch]                               */
+                                         outside [0, batch]; kvq_prompt_attention:
+                                         seq_offsets likewise in [0, num_tokens]          */
 };
 
 /* Layout of one layer's paged cache.  Supported combinations:
@@ -442,6 +443,125 @@ int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads,
                       int32_t num_groups, int32_t max_prefix_len, const void *res_k_bf16,
                       const void *res_v_bf16, void *out_bf16, void *workspace,
                       size_t workspace_bytes, kvq_stream_t stream);
+
+/*
+ * kvq_prompt_attention -- causal attention over packed prompts: what a prefill
+ * computes next to writing its K and V (kvq_quantize_write).
+ *
+ *   q_bf16        [num_tokens, num_q_heads, head_dim] BF16, tokens q_stride
+ *                 elements apart (a token's heads are contiguous; q, k and v may
+ *                 be parts of one projection's rows)
+ *   k_bf16, v_bf16  [num_tokens, num_kv_heads, head_dim] BF16, tokens k_stride
+ *                 and v_stride elements apart
+ *   seq_offsets   [num_seqs + 1] int32, non-decreasing, in [0, num_tokens]:
+ *                 sequence s is the tokens [seq_offsets[s], seq_offsets[s + 1])
+ *   max_seq_len   host-side upper bound of the sequences' lengths
+ *   out_bf16      [num_tokens, num_q_heads, head_dim] BF16 (written)
+ *   lse           [num_tokens, num_q_heads] FP32, the natural logarithm of the
+ *                 softmax's sum (written), or NULL
+ *   workspace     device buffer of at least
+ *                 kvq_prompt_attention_workspace_size() bytes, 256-byte aligned;
+ *                 two calls that may overlap on the GPU need two
+ *
+ * out is softmax(q k^T / sqrt(head_dim)) V over the tokens of the row's own
+ * sequence up to its own; query head h reads kv head h / (num_q_heads /
+ * num_kv_heads).  Products of BF16 operands accumulate in FP32; scores, softmax
+ * statistics and partial outputs are FP32; a probability is rounded to BF16 once
+ * (relative to its row's largest so far) and the output once.  A sequence's
+ * values must be finite; tokens of other sequences and rows outside every
+ * sequence may hold anything.  Rows of out and lse outside every sequence are
+ * left as they were.
+ *
+ * seq_offsets out of order or range set KVQ_DEVERR_GROUP_RANGE, and nothing is
+ * written; a sequence longer than max_seq_len sets KVQ_DEVERR_CONTEXT_RANGE and
+ * its rows are left as they were.  num_seqs <= 8192, num_tokens, max_seq_len and
+ * strides <= 2^24, else KVQ_ERR_UNSUPPORTED; num_kv_heads 1 to 8, ratio 1 to 8,
+ * head_dim 64 or 128, as in the cache.  Strides are multiples of 8.
+ */
+int kvq_prompt_attention_workspace_size(int32_t num_seqs, int32_t max_seq_len, int32_t num_q_heads,
+                                        int32_t num_kv_heads, size_t *bytes);
+int kvq_prompt_attention(const void *q_bf16, int64_t q_stride, const void *k_bf16, int64_t k_stride,
+                         const void *v_bf16, int64_t v_stride, const int32_t *seq_offsets,
+                         int32_t num_seqs, int64_t num_tokens, int32_t max_seq_len,
+                         int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                         void *out_bf16, float *lse, void *workspace, size_t workspace_bytes,
+                         kvq_stream_t stream);
+
+/*
+ * kvq_weigh_decode -- kvq_paged_decode that also adds up how much attention each
+ * cached token gets, for kvq_evict_tokens.
+ *
+ *   weights       [batch, num_kv_heads, weights_stride] FP32: entry (b, h, t),
+ *                 t < context_lens[b], goes up by the sum over the query heads of
+ *                 kv head h of softmax(q k^T / sqrt(head_dim))_t; the entries
+ *                 from context_lens[b] on are left as they were (updated)
+ *   weights_stride  >= max_context_len
+ *   workspace     at least kvq_weigh_decode_workspace_size() bytes (the scores
+ *                 of every position that max_context_len allows)
+ *   other arguments and errors as kvq_paged_decode, and out is the same bit for bit
+ * K must be per-(token, head), as for an eviction (else KVQ_ERR_UNSUPPORTED).
+ *
+ * Each weight is formed in FP32 from the scores of the decode and added once, in
+ * the order of the query heads: no atomics, so a call's result does not depend on
+ * scheduling.  A sequence that the decode leaves out, and a block that it skips,
+ * add nothing.  A token's weight starts at what its entry holds when the token
+ * is appended: 0 after an eviction; a row that begins anew, or whose last tokens
+ * were taken back without an eviction, has its entries cleared by the caller.
+ */
+int kvq_weigh_decode_workspace_size(const kvq_format *fmt, int32_t batch, int32_t num_q_heads,
+                                    int32_t max_context_len, size_t *bytes);
+int kvq_weigh_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, const kvq_format *fmt,
+                     kvq_caches caches, kvq_scales scales, const int32_t *block_tables,
+                     int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t max_context_len,
+                     float *weights, int64_t weights_stride, float *out, void *workspace,
+                     size_t workspace_bytes, kvq_stream_t stream);
+
+/*
+ * kvq_evict_tokens -- every row gives up the cached tokens that got the least
+ * attention, each kv head its own, and the rest moves together, so that
+ * kvq_release_blocks(kept_lens, ...) can give the freed blocks back.
+ *
+ *   keep_lens     [num_rows] int32: tokens k that the row keeps; a row of n =
+ *                 context_lens[r] <= k tokens stays as it is
+ *   recent_lens   [num_rows] int32: its last w = min(recent_lens[r], k) tokens
+ *                 are kept whatever their weights
+ *   pinned_lens   [num_rows] int32 or NULL (0): and its first p =
+ *                 min(pinned_lens[r], k - w) (attention sinks, a shared prompt)
+ *   context_lens, block_tables, fmt, caches, scales  the rows' cache (codes and
+ *                 scales updated; the tables and lengths are only read)
+ *   ref_counts    [num_blocks] of the block pool, or NULL: a row that would
+ *                 write into a block whose count is not 1 is left as it is
+ *   weights       [num_rows, num_kv_heads, max_positions] FP32 (updated)
+ *   kept_lens     [num_rows] int32: min(n, k), or n where the row was left as it
+ *                 is (written): the keep_lens of the kvq_release_blocks to follow
+ *   workspace     device buffer of at least kvq_evict_workspace_size() bytes,
+ *                 256-byte aligned
+ *
+ * Each kv head keeps, besides those p and w, the k - w - p heaviest of the tokens
+ * [p, n - w): by weight, ties to the lower position; NaN counts as the heaviest.
+ * Kept tokens below k - w stay in place; those in [k - w, n - w) go, in order, to
+ * the places in [p, k - w) that evicted ones leave; the last w become [k - w, k)
+ * in their order.  (A head's position then says nothing about a token's age,
+ * but the last w stay the last w; the softmax does not ask.)  Weights move along,
+ * entries [k, n) become 0.  Codes and scales move byte for byte, so K has to have
+ * per-token scales (else KVQ_ERR_UNSUPPORTED).
+ *
+ * A negative length or a context past max_positions or the table sets
+ * KVQ_DEVERR_CONTEXT_RANGE, a block id outside [0, num_blocks) among the row's
+ * KVQ_DEVERR_BLOCK_RANGE, a shared block KVQ_DEVERR_POOL_STATE; the row is left
+ * as it is.  Blocks [p / 16, (k + 15) / 16) are written.  Rows must not share the
+ * blocks that are written (ref_counts checks it).  num_rows <= 8192 and table
+ * sizes as kvq_assign_blocks; num_rows == 0 is a no-op.
+ */
+int kvq_evict_workspace_size(int32_t num_rows, int32_t num_kv_heads, int32_t max_positions,
+                             size_t *bytes);
+int kvq_evict_tokens(const int32_t *keep_lens, const int32_t *recent_lens,
+                     const int32_t *pinned_lens, int32_t num_rows, const int32_t *context_lens,
+                     const int32_t *block_tables, int32_t max_blocks_per_seq,
+                     const kvq_format *fmt, kvq_caches caches, kvq_scales scales,
+                     const int32_t *ref_counts, float *weights, int32_t max_positions,
+                     int32_t *kept_lens, void *workspace, size_t workspace_bytes,
+                     kvq_stream_t stream);
 
 /*
  * kvq_device_errors -- synchronize `stream`, then return the sticky device

@@ -50,6 +50,7 @@ from .quantize import (  # noqa: F401
 from .attention import paged_decode_fp64, paged_decode_one_fp64, attention_fp64  # noqa: F401
 from . import arithmetic  # noqa: F401
 from .offload import prefetch_blocks  # noqa: F401
+from .serving import prompt_attention_fp64, attention_weights_fp64, evict_tokens  # noqa: F401
 from .block_pool import Pool, assign_blocks, release_blocks  # noqa: F401
 from .kivi import kivi_append, kivi_decode_fp64  # noqa: F401
 from .rotation import (  # noqa: F401

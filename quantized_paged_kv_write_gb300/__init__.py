@@ -47,6 +47,8 @@ EXPORTED_SYMBOLS = (
     "kvq_device_errors", "kvq_status_string", "kvq_version", "kvq_paged_decode_noalloc",
     "kvq_write_decode", "kvq_prefetch_blocks", "kvq_kivi_append", "kvq_kivi_decode", "kvq_build_id",
     "kvq_assign_blocks", "kvq_release_blocks", "kvq_prefix_decode", "kvq_prefix_decode_workspace_size",
+    "kvq_prompt_attention", "kvq_prompt_attention_workspace_size", "kvq_weigh_decode",
+    "kvq_weigh_decode_workspace_size", "kvq_evict_tokens", "kvq_evict_workspace_size",
 )
 
 # size of the static scratch of kvq_paged_decode_noalloc (include/kvq.h)
@@ -129,6 +131,22 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.kvq_prefix_decode.argtypes = [vp, i32, i32, fmtp, _Caches, _Scales, vp, i32, vp, i32, vp, vp, i32, i32,
                                           vp, vp, vp, vp, ctypes.c_size_t, vp]
         lib.kvq_prefix_decode.restype = ctypes.c_int
+        sizep = ctypes.POINTER(ctypes.c_size_t)
+        lib.kvq_prompt_attention_workspace_size.argtypes = [i32, i32, i32, i32, sizep]
+        lib.kvq_prompt_attention_workspace_size.restype = ctypes.c_int
+        lib.kvq_prompt_attention.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i64, i32, i32, i32, i32, vp, vp, vp,
+                                             ctypes.c_size_t, vp]
+        lib.kvq_prompt_attention.restype = ctypes.c_int
+        lib.kvq_weigh_decode_workspace_size.argtypes = [fmtp, i32, i32, i32, sizep]
+        lib.kvq_weigh_decode_workspace_size.restype = ctypes.c_int
+        lib.kvq_weigh_decode.argtypes = [vp, i32, i32, fmtp, _Caches, _Scales, vp, i32, vp, i32, vp, i64, vp, vp,
+                                         ctypes.c_size_t, vp]
+        lib.kvq_weigh_decode.restype = ctypes.c_int
+        lib.kvq_evict_workspace_size.argtypes = [i32, i32, i32, sizep]
+        lib.kvq_evict_workspace_size.restype = ctypes.c_int
+        lib.kvq_evict_tokens.argtypes = [vp, vp, vp, i32, vp, vp, i32, fmtp, _Caches, _Scales, vp, vp, i32, vp, vp,
+                                         ctypes.c_size_t, vp]
+        lib.kvq_evict_tokens.restype = ctypes.c_int
         lib.kvq_device_errors.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32, vp]
         lib.kvq_device_errors.restype = ctypes.c_int
         lib.kvq_status_string.argtypes = [i32]
@@ -603,6 +621,164 @@ def kvq_prefix_decode(q: torch.Tensor, fmt: CacheFormat, cache: dict, block_tabl
     if st != KVQ_OK:
         raise KvqError(st, "kvq_prefix_decode")
     return out
+
+
+def _rows(t: torch.Tensor, what: str) -> tuple:
+    """Pointer and token stride of BF16 [N, heads, d] whose tokens may lie apart
+    (a part of a projection's rows)."""
+    if isinstance(t, torch.Tensor) and t.dim() == 3:
+        n, heads, d = t.shape
+        if t.numel() and t.stride(2) == 1 and (heads == 1 or t.stride(1) == d) and (n == 1 or t.stride(0) >= heads * d):
+            return _ptr(t[0], torch.bfloat16, what), int(t.stride(0)) if n > 1 else heads * d
+        if not t.numel():
+            return _ptr(t, torch.bfloat16, what), max(heads * d, 8)
+        raise ValueError(f"{what}: a token's heads must be contiguous")
+    return _ptr(t, torch.bfloat16, what), 0
+
+
+def kvq_prompt_attention_workspace_size(num_seqs: int, max_seq_len: int, num_q_heads: int, num_kv_heads: int) -> int:
+    lib = load_library()
+    out = ctypes.c_size_t(0)
+    st = lib.kvq_prompt_attention_workspace_size(int(num_seqs), int(max_seq_len), int(num_q_heads), int(num_kv_heads),
+                                                 ctypes.byref(out))
+    if st != KVQ_OK:
+        raise KvqError(st, "kvq_prompt_attention_workspace_size")
+    return int(out.value)
+
+
+def kvq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_offsets: torch.Tensor,
+                         max_seq_len: int, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention over packed prompts: q BF16 [N, H_q, d], k, v BF16 [N,
+    H_kv, d] (tokens may lie apart, as in a fused projection's output); sequence
+    s is the tokens [seq_offsets[s], seq_offsets[s + 1]) (int32 [S + 1]).
+    Returns BF16 [N, H_q, d]; fills lse FP32 [N, H_q] if given.  Rows outside
+    every sequence are left as they were."""
+    lib = load_library()
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [N, H_q, d], k and v [N, H_kv, d]")
+    n, hq, d = (int(x) for x in q.shape)
+    hkv = int(k.shape[1])
+    if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
+        raise ValueError("seq_offsets must be [S + 1]")
+    seqs = int(seq_offsets.shape[0]) - 1
+    if out is None:
+        out = _empty((n, hq, d), torch.bfloat16, q.device, stream)
+    elif tuple(out.shape) != (n, hq, d):
+        raise ValueError("out must have the shape of q")
+    if lse is not None and tuple(lse.shape) != (n, hq):
+        raise ValueError("lse must be [N, H_q]")
+    if workspace is None:
+        nbytes = kvq_prompt_attention_workspace_size(seqs, max_seq_len, hq, hkv)
+        workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    st = lib.kvq_prompt_attention(qp, qs, kp, ks, vp, vs, _ptr(seq_offsets, torch.int32, "seq_offsets"), seqs, n,
+                                  int(max_seq_len), hq, hkv, d, _ptr(out, torch.bfloat16, "out"),
+                                  None if lse is None else _ptr(lse, torch.float32, "lse"),
+                                  _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream))
+    if st != KVQ_OK:
+        raise KvqError(st, "kvq_prompt_attention")
+    return out
+
+
+def kvq_weigh_decode_workspace_size(fmt: CacheFormat, batch: int, num_q_heads: int, max_context_len: int) -> int:
+    lib = load_library()
+    out = ctypes.c_size_t(0)
+    cf = fmt.as_c()
+    st = lib.kvq_weigh_decode_workspace_size(ctypes.byref(cf), int(batch), int(num_q_heads), int(max_context_len),
+                                             ctypes.byref(out))
+    if st != KVQ_OK:
+        raise KvqError(st, "kvq_weigh_decode_workspace_size")
+    return int(out.value)
+
+
+def kvq_weigh_decode(q: torch.Tensor, fmt: CacheFormat, cache: dict, block_tables: torch.Tensor,
+                     context_lens: torch.Tensor, max_context_len: int, weights: torch.Tensor,
+                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """kvq_paged_decode, adding each cached token's attention weight to weights
+    FP32 [B, H_kv, positions] (positions >= max_context_len): the sum over the
+    query heads of its kv head.  Returns out FP32 [B, H_q, d]."""
+    lib = load_library()
+    bsz, hq, d = (int(x) for x in q.shape)
+    if d != fmt.head_dim:
+        raise ValueError("q head_dim does not match the cache format")
+    if block_tables.dim() != 2 or block_tables.shape[0] != bsz or context_lens.shape != (bsz,):
+        raise ValueError("block_tables must be [B, max_blocks] and context_lens [B]")
+    if weights.dim() != 3 or tuple(weights.shape[:2]) != (bsz, fmt.num_kv_heads):
+        raise ValueError("weights must be [B, H_kv, positions]")
+    if out is None:
+        out = _empty((bsz, hq, d), torch.float32, q.device, stream)
+    elif tuple(out.shape) != (bsz, hq, d):
+        raise ValueError("out must have the shape of q")
+    if workspace is None:
+        nbytes = kvq_weigh_decode_workspace_size(fmt, bsz, hq, max_context_len)
+        workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
+    cf = fmt.as_c()
+    caches, scales = _caches(cache)
+    st = lib.kvq_weigh_decode(_ptr(q, torch.bfloat16, "q"), bsz, hq, ctypes.byref(cf), caches, scales,
+                              _ptr(block_tables, torch.int32, "block_tables"), int(block_tables.shape[1]),
+                              _ptr(context_lens, torch.int32, "context_lens"), int(max_context_len),
+                              _ptr(weights, torch.float32, "weights"), int(weights.shape[2]),
+                              _ptr(out, torch.float32, "out"), _ptr(workspace, torch.uint8, "workspace"),
+                              int(workspace.numel()), _stream(stream))
+    if st != KVQ_OK:
+        raise KvqError(st, "kvq_weigh_decode")
+    return out
+
+
+def kvq_evict_workspace_size(num_rows: int, num_kv_heads: int, max_positions: int) -> int:
+    lib = load_library()
+    out = ctypes.c_size_t(0)
+    st = lib.kvq_evict_workspace_size(int(num_rows), int(num_kv_heads), int(max_positions), ctypes.byref(out))
+    if st != KVQ_OK:
+        raise KvqError(st, "kvq_evict_workspace_size")
+    return int(out.value)
+
+
+def kvq_evict_tokens(keep_lens: torch.Tensor, context_lens: torch.Tensor, block_tables: torch.Tensor, fmt: CacheFormat,
+                     cache: dict, weights: torch.Tensor, recent_lens: torch.Tensor,
+                     pinned_lens: Optional[torch.Tensor] = None, pool: Optional[dict] = None,
+                     kept_lens: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Every row and kv head keeps keep_lens[r] tokens (int32 [R]): the last
+    recent_lens[r], the first pinned_lens[r], and the heaviest others by weights
+    FP32 [R, H_kv, positions].  The cache and weights are updated in place; the
+    pool's counts show blocks that other rows use.  Returns kept_lens int32 [R],
+    what kvq_release_blocks takes to give the freed blocks back."""
+    lib = load_library()
+    rows = int(keep_lens.shape[0])
+    for t, what in ((keep_lens, "keep_lens"), (recent_lens, "recent_lens"), (pinned_lens, "pinned_lens"),
+                    (context_lens, "context_lens"), (kept_lens, "kept_lens")):
+        if t is not None and t.shape != (rows,):
+            raise ValueError(f"{what} must be [R]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != rows:
+        raise ValueError("block_tables must be [R, max_blocks]")
+    if weights.dim() != 3 or tuple(weights.shape[:2]) != (rows, fmt.num_kv_heads):
+        raise ValueError("weights must be [R, H_kv, positions]")
+    positions = int(weights.shape[2])
+    refs = None
+    if pool is not None:
+        if int(pool["ref_counts"].numel()) != fmt.num_blocks:
+            raise ValueError("the pool's ref_counts must be [num_blocks]")
+        refs = _ptr(pool["ref_counts"], torch.int32, "ref_counts")
+    if kept_lens is None:
+        kept_lens = _empty(rows, torch.int32, block_tables.device, stream)
+    if workspace is None:
+        nbytes = kvq_evict_workspace_size(rows, fmt.num_kv_heads, positions)
+        workspace = _empty(max(nbytes, 256), torch.uint8, block_tables.device, stream)
+    cf = fmt.as_c()
+    caches, scales = _caches(cache)
+    st = lib.kvq_evict_tokens(_ptr(keep_lens, torch.int32, "keep_lens"), _ptr(recent_lens, torch.int32, "recent_lens"),
+                              None if pinned_lens is None else _ptr(pinned_lens, torch.int32, "pinned_lens"), rows,
+                              _ptr(context_lens, torch.int32, "context_lens"),
+                              _ptr(block_tables, torch.int32, "block_tables"), int(block_tables.shape[1]),
+                              ctypes.byref(cf), caches, scales, refs, _ptr(weights, torch.float32, "weights"), positions,
+                              _ptr(kept_lens, torch.int32, "kept_lens"), _ptr(workspace, torch.uint8, "workspace"),
+                              int(workspace.numel()), _stream(stream))
+    if st != KVQ_OK:
+        raise KvqError(st, "kvq_evict_tokens")
+    return kept_lens
 
 
 def kvq_device_errors(clear: bool = True, stream=None) -> int:

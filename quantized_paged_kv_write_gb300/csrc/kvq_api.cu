@@ -147,6 +147,21 @@ WsLayout ws_layout(int B, int H, int D, int max_ctas) {
   return w;
 }
 
+// A decode that adds up attention weights needs the scores of every block that
+// max_context_len allows, and each row's maximum and sum, behind that.
+struct WeighWs {
+  size_t z_off, norm_off, total;
+};
+
+WeighWs weigh_ws(const WsLayout &wl, int B, int Hq, int max_context) {
+  const size_t blocks = static_cast<size_t>(B) * ((static_cast<size_t>(max_context) + kBlockSize - 1) / kBlockSize);
+  WeighWs w;
+  w.z_off = wl.total;
+  w.norm_off = w.z_off + blocks * Hq * kBlockSize * sizeof(float);
+  w.total = w.norm_off + ((static_cast<size_t>(B) * Hq * sizeof(float2) + 255) & ~size_t(255));
+  return w;
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
@@ -359,12 +374,13 @@ constexpr int32_t kMaxRowBlocks = 1 << 27;
 
 // The decode entry points with a caller workspace; k_new / v_new non-null
 // fuse the write of each sequence's new token (kvq_write_decode).
+// `weights` non-null adds up attention weights (kvq_weigh_decode).
 static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, const kvq_format *fmt,
                       kvq_caches caches, kvq_scales scales, const int32_t *block_tables,
                       int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t max_context_len,
                       float *out, void *workspace, size_t workspace_bytes, kvq_stream_t stream,
                       const void *k_new, const void *v_new, const void *res_k = nullptr,
-                      const void *res_v = nullptr) {
+                      const void *res_v = nullptr, float *weights = nullptr, int64_t weights_stride = 0) {
   int kf = 0, vf = 0;
   int st = check_decode_shape(fmt, batch, num_q_heads, &kf, &vf);
   if (st != KVQ_OK) return st;
@@ -373,6 +389,7 @@ static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
     if (kf != K_INT8_CHAN && kf != K_INT2_CHAN) return KVQ_ERR_UNSUPPORTED;  // the tail belongs to per-channel K
     if (!res_k || !res_v || !aligned16(res_k) || !aligned16(res_v)) return KVQ_ERR_INVALID_ARG;
   }
+  if (weights != nullptr && (kf == K_INT8_CHAN || kf == K_INT2_CHAN)) return KVQ_ERR_UNSUPPORTED;
   const bool fused = k_new != nullptr || v_new != nullptr;
   if (fused) {
     if (kf == K_INT8_CHAN || kf == K_INT2_CHAN) return KVQ_ERR_UNSUPPORTED;  // per-channel K blocks take no appends
@@ -395,7 +412,8 @@ static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
   DecodePlan plan;
   if (plan_decode(D, kf, vf, H, G, batch, fmt->rotation != 0, &plan) != cudaSuccess) return KVQ_ERR_CUDA;
   const WsLayout wl = ws_layout(batch, H, D, plan.max_ctas);
-  if (workspace_bytes < wl.total) return KVQ_ERR_WORKSPACE;
+  const WeighWs ww = weigh_ws(wl, batch, num_q_heads, max_context_len);
+  if (workspace_bytes < (weights != nullptr ? ww.total : wl.total)) return KVQ_ERR_WORKSPACE;
   unsigned int *err = nullptr;
   if (error_word(&err) != cudaSuccess) return KVQ_ERR_CUDA;
 
@@ -445,9 +463,29 @@ static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
     a.ks_w = scales.k_scale;
     a.vs_w = scales.v_scale;
   }
-  return launch_decode(D, kf, vf, a, plan, maps, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? KVQ_OK
-             : KVQ_ERR_CUDA;
+  if (weights != nullptr) {
+    a.ws_z = reinterpret_cast<float *>(ws + ww.z_off);
+    a.ws_norm = reinterpret_cast<float2 *>(ws + ww.norm_off);
+  }
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (launch_decode(D, kf, vf, a, plan, maps, s) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (weights == nullptr) return KVQ_OK;
+  WeighArgs w;
+  w.z = a.ws_z;
+  w.norm = a.ws_norm;
+  w.cum = a.ws_cum;
+  w.tables = block_tables;
+  w.ctx = context_lens;
+  w.weights = weights;
+  w.stride = weights_stride;
+  w.num_blocks = fmt->num_blocks;
+  w.B = batch;
+  w.H = H;
+  w.G = G;
+  w.max_blocks = max_blocks_per_seq;
+  int sms = 0;
+  if ((st = sm_count(&sms)) != KVQ_OK) return st;
+  return launch_weigh(w, sms, s) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 int kvq_paged_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, const kvq_format *fmt,
@@ -478,6 +516,28 @@ int kvq_kivi_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, cons
   return run_decode(q_bf16, batch, num_q_heads, fmt, caches, scales, block_tables, max_blocks_per_seq,
                     context_lens, max_context_len, out, workspace, workspace_bytes, stream, nullptr, nullptr,
                     res_k_bf16, res_v_bf16);
+}
+
+int kvq_weigh_decode_workspace_size(const kvq_format *fmt, int32_t batch, int32_t num_q_heads,
+                                    int32_t max_context_len, size_t *bytes) {
+  const int st = kvq_decode_workspace_size(fmt, batch, num_q_heads, max_context_len, bytes);
+  if (st != KVQ_OK) return st;
+  WsLayout wl = {};
+  wl.total = *bytes;
+  *bytes = weigh_ws(wl, batch, num_q_heads, max_context_len).total;
+  return KVQ_OK;
+}
+
+int kvq_weigh_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, const kvq_format *fmt,
+                     kvq_caches caches, kvq_scales scales, const int32_t *block_tables,
+                     int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t max_context_len,
+                     float *weights, int64_t weights_stride, float *out, void *workspace, size_t workspace_bytes,
+                     kvq_stream_t stream) {
+  if (!weights || (reinterpret_cast<uintptr_t>(weights) & 3u) || weights_stride < max_context_len)
+    return KVQ_ERR_INVALID_ARG;
+  return run_decode(q_bf16, batch, num_q_heads, fmt, caches, scales, block_tables, max_blocks_per_seq,
+                    context_lens, max_context_len, out, workspace, workspace_bytes, stream, nullptr, nullptr,
+                    nullptr, nullptr, weights, weights_stride);
 }
 
 int kvq_kivi_append(const void *k_new_bf16, const void *v_new_bf16, int32_t batch, const kvq_format *fmt,
@@ -657,6 +717,169 @@ int kvq_release_blocks(const int32_t *keep_lens, int32_t num_rows, int32_t *cont
   a.rows = num_rows;
   a.max_blocks = max_blocks_per_seq;
   return launch_release_blocks(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+// Workspace of an eviction: a record and two lists for each (row, kv head).  A
+// token moves into a place that another one leaves: at most half of them do.
+static size_t evict_ws(int rows, int heads, int64_t max_positions, size_t *list) {
+  const size_t n = static_cast<size_t>(rows) * heads;
+  *list = (n * sizeof(EvictMeta) + 255) & ~size_t(255);
+  return *list + n * 2 * (max_positions / 2) * sizeof(int);
+}
+
+static int check_evict(int32_t num_rows, int32_t num_kv_heads, int32_t max_positions) {
+  if (num_rows < 0 || num_kv_heads < 1 || max_positions < 0) return KVQ_ERR_INVALID_ARG;
+  return num_rows > 8192 || num_kv_heads > 8 ? KVQ_ERR_UNSUPPORTED : KVQ_OK;
+}
+
+int kvq_evict_workspace_size(int32_t num_rows, int32_t num_kv_heads, int32_t max_positions, size_t *bytes) {
+  const int st = check_evict(num_rows, num_kv_heads, max_positions);
+  if (st != KVQ_OK) return st;
+  if (!bytes) return KVQ_ERR_INVALID_ARG;
+  size_t list;
+  *bytes = evict_ws(num_rows, num_kv_heads, max_positions, &list);
+  return KVQ_OK;
+}
+
+int kvq_evict_tokens(const int32_t *keep_lens, const int32_t *recent_lens, const int32_t *pinned_lens,
+                     int32_t num_rows, const int32_t *context_lens, const int32_t *block_tables,
+                     int32_t max_blocks_per_seq, const kvq_format *fmt, kvq_caches caches, kvq_scales scales,
+                     const int32_t *ref_counts, float *weights, int32_t max_positions, int32_t *kept_lens,
+                     void *workspace, size_t workspace_bytes, kvq_stream_t stream) {
+  int kf = 0, vf = 0;
+  int st = decode_format(fmt, &kf, &vf);
+  if (st != KVQ_OK) return st;
+  if (kf == K_INT8_CHAN || kf == K_INT2_CHAN) return KVQ_ERR_UNSUPPORTED;  // a token's codes depend on its block
+  if ((st = check_evict(num_rows, fmt->num_kv_heads, max_positions)) != KVQ_OK) return st;
+  if (max_blocks_per_seq < 1) return KVQ_ERR_INVALID_ARG;
+  if (!table_fits(num_rows, max_blocks_per_seq) || fmt->num_blocks >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  if (num_rows == 0) return KVQ_OK;
+  if (!keep_lens || !recent_lens || !context_lens || !block_tables || !weights || !kept_lens || !workspace ||
+      !caches.k_cache || !caches.v_cache || !scales.k_scale || !scales.v_scale)
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned4(keep_lens) || !aligned4(recent_lens) || !aligned4(pinned_lens) || !aligned4(context_lens) ||
+      !aligned4(block_tables) || !aligned4(ref_counts) || !aligned4(weights) || !aligned4(kept_lens) ||
+      !aligned16(caches.k_cache) || !aligned16(caches.v_cache) || !aligned16(scales.k_scale) ||
+      !aligned16(scales.v_scale) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return KVQ_ERR_INVALID_ARG;
+  size_t list;
+  if (workspace_bytes < evict_ws(num_rows, fmt->num_kv_heads, max_positions, &list)) return KVQ_ERR_WORKSPACE;
+  EvictArgs a;
+  if (error_word(&a.err) != cudaSuccess) return KVQ_ERR_CUDA;
+  a.keep = keep_lens;
+  a.recent = recent_lens;
+  a.pinned = pinned_lens;
+  a.ctx = context_lens;
+  a.tables = block_tables;
+  a.refs = ref_counts;
+  a.weights = weights;
+  a.kept = kept_lens;
+  a.kc = static_cast<uint8_t *>(caches.k_cache);
+  a.vc = static_cast<uint8_t *>(caches.v_cache);
+  a.ks = scales.k_scale;
+  a.vs = scales.v_scale;
+  a.ws_meta = static_cast<EvictMeta *>(workspace);
+  a.ws_list = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + list);
+  a.num_blocks = fmt->num_blocks;
+  a.stride = max_positions;
+  a.rows = num_rows;
+  a.H = fmt->num_kv_heads;
+  a.max_blocks = max_blocks_per_seq;
+  a.max_len = static_cast<int>(std::min<int64_t>(max_positions, static_cast<int64_t>(max_blocks_per_seq) * kBlockSize));
+  a.cap = max_positions / 2;
+  a.krow = kf == K_INT4_TOK ? fmt->head_dim / 2 : fmt->head_dim;
+  a.vrow = vf == V_INT4_G32 ? fmt->head_dim / 2 : vf == V_INT2_G32 ? fmt->head_dim / 4 : fmt->head_dim;
+  a.vgroups = vf == V_INT4_G32 || vf == V_INT2_G32 ? fmt->head_dim / 32 : 1;
+  int sms = 0;
+  if ((st = sm_count(&sms)) != KVQ_OK) return st;
+  return launch_evict(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+// Work of a prompt attention: units of so many tokens, and the places of the plan.
+struct PromptWs {
+  int unit, levels;
+  size_t seq, level, place, total;
+};
+
+static PromptWs prompt_ws(int seqs, int max_seq, int G) {
+  auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
+  PromptWs w;
+  w.unit = 2 * (128 / G);
+  w.levels = std::max(1, static_cast<int>((static_cast<int64_t>(max_seq) + w.unit - 1) / w.unit));
+  w.seq = al(sizeof(PromptHead));
+  w.level = w.seq + al(static_cast<size_t>(seqs) * sizeof(int2));
+  w.place = w.level + al((static_cast<size_t>(w.levels) + 1) * sizeof(int));
+  w.total = w.place + al((static_cast<size_t>(w.levels) + 1) * sizeof(int));
+  return w;
+}
+
+static int check_prompt(int32_t num_seqs, int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads) {
+  if (num_seqs < 0 || max_seq_len < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0)
+    return KVQ_ERR_INVALID_ARG;
+  return num_kv_heads > 8 || num_q_heads / num_kv_heads > 8 || num_seqs > 8192 || max_seq_len > (1 << 24)
+             ? KVQ_ERR_UNSUPPORTED
+             : KVQ_OK;
+}
+
+int kvq_prompt_attention_workspace_size(int32_t num_seqs, int32_t max_seq_len, int32_t num_q_heads,
+                                        int32_t num_kv_heads, size_t *bytes) {
+  const int st = check_prompt(num_seqs, max_seq_len, num_q_heads, num_kv_heads);
+  if (st != KVQ_OK) return st;
+  if (!bytes) return KVQ_ERR_INVALID_ARG;
+  *bytes = prompt_ws(num_seqs, max_seq_len, num_q_heads / num_kv_heads).total;
+  return KVQ_OK;
+}
+
+int kvq_prompt_attention(const void *q_bf16, int64_t q_stride, const void *k_bf16, int64_t k_stride,
+                         const void *v_bf16, int64_t v_stride, const int32_t *seq_offsets, int32_t num_seqs,
+                         int64_t num_tokens, int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_dim, void *out_bf16, float *lse, void *workspace, size_t workspace_bytes,
+                         kvq_stream_t stream) {
+  int st = check_prompt(num_seqs, max_seq_len, num_q_heads, num_kv_heads);
+  if (st != KVQ_OK) return st;
+  if (head_dim != 64 && head_dim != 128) return KVQ_ERR_UNSUPPORTED;
+  if (num_tokens < 0) return KVQ_ERR_INVALID_ARG;
+  const int64_t qrow = static_cast<int64_t>(num_q_heads) * head_dim, krow = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (q_stride < qrow || k_stride < krow || v_stride < krow || q_stride % 8 || k_stride % 8 || v_stride % 8)
+    return KVQ_ERR_INVALID_ARG;
+  if (num_tokens > (1 << 24) || q_stride > (1 << 24) || k_stride > (1 << 24) || v_stride > (1 << 24))
+    return KVQ_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || num_tokens == 0 || max_seq_len == 0) return KVQ_OK;
+  if (!q_bf16 || !k_bf16 || !v_bf16 || !seq_offsets || !out_bf16 || !workspace) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(out_bf16) ||
+      !aligned4(seq_offsets) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return KVQ_ERR_INVALID_ARG;
+  const int G = num_q_heads / num_kv_heads;
+  const PromptWs wl = prompt_ws(num_seqs, max_seq_len, G);
+  if (workspace_bytes < wl.total) return KVQ_ERR_WORKSPACE;
+  PromptArgs a;
+  if (error_word(&a.err) != cudaSuccess) return KVQ_ERR_CUDA;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.q = static_cast<const uint16_t *>(q_bf16);
+  a.k = static_cast<const uint16_t *>(k_bf16);
+  a.v = static_cast<const uint16_t *>(v_bf16);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.offsets = seq_offsets;
+  a.out = static_cast<uint16_t *>(out_bf16);
+  a.lse = lse;
+  a.ws_head = reinterpret_cast<PromptHead *>(ws);
+  a.ws_seq = reinterpret_cast<int2 *>(ws + wl.seq);
+  a.ws_level = reinterpret_cast<int *>(ws + wl.level);
+  a.ws_place = reinterpret_cast<int *>(ws + wl.place);
+  a.num_tokens = static_cast<int>(num_tokens);
+  a.num_seqs = num_seqs;
+  a.max_seq = max_seq_len;
+  a.Hq = num_q_heads;
+  a.H = num_kv_heads;
+  a.G = G;
+  a.unit = wl.unit;
+  a.levels = wl.levels;
+  int sms = 0;
+  if ((st = sm_count(&sms)) != KVQ_OK) return st;
+  return launch_prompt_attention(head_dim, a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK
+                                                                                                         : KVQ_ERR_CUDA;
 }
 
 // Workspace of the shared-prefix decode: the suffix's split decode, then the

@@ -66,6 +66,11 @@ struct DecodeArgs {
   int overlap = 0;
   const unsigned long long *ready = nullptr;
   unsigned long long token = 0;
+  // Decode that adds up attention weights (kvq_weigh_decode): the split leaves
+  // every score (log2 units) here, [block of the list][H][G][16] with token
+  // i + 4 k at 4 i + k, and the reduce each row's maximum and 1 / sum; else null.
+  float *ws_z = nullptr;
+  float2 *ws_norm = nullptr;   // [B, Hq]
 };
 
 // Launches kern so that it may start while the stream's kernel before it still
@@ -158,6 +163,64 @@ struct ReleaseArgs {
 };
 cudaError_t launch_assign_blocks(const AssignArgs &a, cudaStream_t stream);
 cudaError_t launch_release_blocks(const ReleaseArgs &a, cudaStream_t stream);
+
+// Attention weights out of a decode's scores (weigh.cu).
+struct WeighArgs {
+  const float *z;              // DecodeArgs::ws_z
+  const float2 *norm;          // DecodeArgs::ws_norm
+  const int *cum;              // DecodeArgs::ws_cum
+  const int32_t *tables, *ctx; // [B, max_blocks], [B]
+  float *weights;              // [B, H, stride]
+  int64_t stride, num_blocks;
+  int B, H, G, max_blocks;
+};
+cudaError_t launch_weigh(const WeighArgs &a, int sms, cudaStream_t stream);
+
+// Eviction by attention weight (evict.cu).
+struct EvictMeta {
+  int moves;                   // tokens that go to the places of evicted ones
+  int active;                  // 0: the row stays as it is
+  int keep, recent;
+};
+struct EvictArgs {
+  const int32_t *keep, *recent, *pinned;  // [rows]; pinned or null
+  const int32_t *ctx, *tables;            // [rows], [rows, max_blocks]
+  const int32_t *refs;                    // [num_blocks] or null
+  float *weights;                         // [rows, H, stride]
+  int32_t *kept;                          // [rows]
+  uint8_t *kc, *vc;
+  float *ks, *vs;
+  EvictMeta *ws_meta;                     // [rows * H]
+  int *ws_list;                           // [rows * H][2][cap]: places, then tokens
+  unsigned int *err;
+  int64_t num_blocks, stride;
+  int rows, H, max_blocks;
+  int max_len;                            // largest valid context
+  int cap;                                // moves of a (row, head) at most
+  int krow, vrow, vgroups;                // bytes of a row of codes; V scales of a row
+};
+cudaError_t launch_evict(const EvictArgs &a, int sms, cudaStream_t stream);
+
+// Causal attention over packed prompts (prompt_attention.cu).
+struct PromptHead {
+  int units;                   // units of work
+  int next;                    // the first one that no CTA has taken
+};
+struct PromptArgs {
+  const uint16_t *q, *k, *v;   // BF16 [num_tokens, heads, D], tokens `stride` elements apart
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *offsets;      // [num_seqs + 1]
+  uint16_t *out;               // BF16 [num_tokens, Hq, D]
+  float *lse;                  // [num_tokens, Hq] or null
+  PromptHead *ws_head;
+  int2 *ws_seq;                // [num_seqs] start and length, by tiles, most first
+  int *ws_level, *ws_place;    // [levels + 1] units before the tile index; places in ws_seq
+  unsigned int *err;
+  int num_tokens, num_seqs, max_seq;
+  int Hq, H, G;
+  int unit, levels;            // tokens of a unit, tiles of max_seq
+};
+cudaError_t launch_prompt_attention(int head_dim, const PromptArgs &a, int sms, cudaStream_t stream);
 
 // Decode over a prefix that the sequences of a group share (prefix_decode.cu).
 //

@@ -1111,6 +1111,12 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
           }
         }
 
+        if constexpr (!T::KCHAN) {
+          if (a.ws_z != nullptr && r < G)
+            *reinterpret_cast<float4 *>(a.ws_z + ((static_cast<int64_t>(g) * H + h) * G + r) * kBlockSize + 4 * i) =
+                make_float4(z[0] + m, z[1] + m, z[2] + m, z[3] + m);
+        }
+
         // ---- probabilities
         float p[4];
 #pragma unroll
@@ -1393,6 +1399,7 @@ __global__ void __launch_bounds__(256) decode_reduce_kernel(const DecodeArgs a, 
     }
   }
   const float inv = (L > 0.f) ? 1.f / L : 0.f;
+  if (a.ws_norm != nullptr && lane == 0) a.ws_norm[warp] = make_float2(mx, inv);
   float o[CPL];
 #pragma unroll
   for (int k = 0; k < CPL; ++k) o[k] = acc[k] * inv;
