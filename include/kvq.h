@@ -456,7 +456,7 @@ int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads,
  *   seq_offsets   [num_seqs + 1] int32, non-decreasing, in [0, num_tokens]:
  *                 sequence s is the tokens [seq_offsets[s], seq_offsets[s + 1])
  *   max_seq_len   host-side upper bound of the sequences' lengths
- *   out_bf16      [num_tokens, num_q_heads, head_dim] BF16 (written)
+ *   out_bf16      [num_tokens, num_q_heads, head_dim] BF16, 32-byte aligned (written)
  *   lse           [num_tokens, num_q_heads] FP32, the natural logarithm of the
  *                 softmax's sum (written), or NULL
  *   workspace     device buffer of at least

@@ -218,6 +218,21 @@ int encode_vscale_map(CUtensorMap *map, const float *base, int64_t nb, int H) {
   return r == CUDA_SUCCESS ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
+// 3-D map over BF16 rows [tokens, heads, D], tokens `stride` elements apart, with
+// a box of 64 channels of `h` heads of `t` tokens.
+int encode_rows_map(CUtensorMap *map, const void *base, int64_t tokens, int heads, int D, int64_t stride, int h, int t) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return KVQ_ERR_CUDA;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(h), static_cast<cuuint32_t>(t)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
 // The descriptors of one decode call.
 int encode_decode_maps_uncached(DecodeMaps *m, const kvq_caches &caches, const kvq_scales &scales, int64_t nb,
                                 int H, int D, int kf, int vf) {
@@ -846,8 +861,8 @@ int kvq_prompt_attention(const void *q_bf16, int64_t q_stride, const void *k_bf1
     return KVQ_ERR_UNSUPPORTED;
   if (num_seqs == 0 || num_tokens == 0 || max_seq_len == 0) return KVQ_OK;
   if (!q_bf16 || !k_bf16 || !v_bf16 || !seq_offsets || !out_bf16 || !workspace) return KVQ_ERR_INVALID_ARG;
-  if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(out_bf16) ||
-      !aligned4(seq_offsets) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) ||
+      (reinterpret_cast<uintptr_t>(out_bf16) & 31u) || !aligned4(seq_offsets) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return KVQ_ERR_INVALID_ARG;
   const int G = num_q_heads / num_kv_heads;
   const PromptWs wl = prompt_ws(num_seqs, max_seq_len, G);
@@ -876,10 +891,16 @@ int kvq_prompt_attention(const void *q_bf16, int64_t q_stride, const void *k_bf1
   a.G = G;
   a.unit = wl.unit;
   a.levels = wl.levels;
+  PromptMaps m;
+  if ((st = encode_rows_map(&m.q, q_bf16, num_tokens, num_q_heads, head_dim, q_stride, G, wl.unit / 2)) != KVQ_OK ||
+      (st = encode_rows_map(&m.k, k_bf16, num_tokens, num_kv_heads, head_dim, k_stride, 1, 128)) != KVQ_OK ||
+      (st = encode_rows_map(&m.v, v_bf16, num_tokens, num_kv_heads, head_dim, v_stride, 1, 128)) != KVQ_OK)
+    return st;
   int sms = 0;
   if ((st = sm_count(&sms)) != KVQ_OK) return st;
-  return launch_prompt_attention(head_dim, a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK
-                                                                                                         : KVQ_ERR_CUDA;
+  return launch_prompt_attention(head_dim, a, m, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? KVQ_OK
+             : KVQ_ERR_CUDA;
 }
 
 // Workspace of the shared-prefix decode: the suffix's split decode, then the

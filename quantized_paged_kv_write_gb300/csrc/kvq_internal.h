@@ -220,7 +220,13 @@ struct PromptArgs {
   int Hq, H, G;
   int unit, levels;            // tokens of a unit, tiles of max_seq
 };
-cudaError_t launch_prompt_attention(int head_dim, const PromptArgs &a, int sms, cudaStream_t stream);
+// Boxes of 64 channels: of a row tile's tokens and a kv head's query heads, and
+// of one head's tile of keys.
+struct PromptMaps {
+  CUtensorMap q, k, v;
+};
+cudaError_t launch_prompt_attention(int head_dim, const PromptArgs &a, const PromptMaps &maps, int sms,
+                                    cudaStream_t stream);
 
 // Decode over a prefix that the sequences of a group share (prefix_decode.cu).
 //

@@ -1,12 +1,30 @@
-// Causal attention over packed prompts.
+// Causal attention over packed prompts, on the fifth-generation tensor cores.
 //
 // What it computes: for token t of a sequence and query head h, which reads kv
 // head h / G (GQA, "KV Cache Quantization" glossary), over the sequence's
 // tokens j <= t:  z_j = q_t k_j / sqrt(d), out = sum softmax(z)_j v_j and
 // lse = ln sum exp(z_j).  It is the attention of the prefill whose K and V the
 // quantize-write stores ("Use Less Memory: Quantization and Offloading", §2.1).
+//
+// A unit of work is 2 x 128 rows of one kv head, row = (token, query head of the
+// group), against the sequence's keys in tiles of 128: each of two softmax
+// warpgroups (thread = row) has 128 rows, both use the tile's K and V.  Scores
+// S = Q K^T and outputs O += P V in tensor memory, P over S as the second
+// product's first operand.  The tensor core alternates between the warpgroups:
+// while one takes its exponentials, the other's P V and next S are computed.
+//   t = S c - mu, c = log2(e) / sqrt(d); p = 2^t, l += p
+// mu, the reference, is the row's maximum in log2 units; it is raised (and O and
+// l follow) only when a score passes it by kRaise, so p stays below 2^kRaise.
+// p is rounded to BF16, the type of V (the product's operands have one type); l
+// sums the unrounded p.
+#include <limits.h>
+
+#include <atomic>
+
 #include "common.cuh"
 #include "kvq_internal.h"
+#include "mbar_wait.cuh"
+#include "tcgen05.cuh"
 
 namespace kvq {
 namespace {
@@ -22,6 +40,7 @@ constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ int sums[kPlanThreads / 32];
+  grid_release();
   // offsets in order and in range, or nothing is computed
   bool order = true;
   for (int s = threadIdx.x; s < a.num_seqs; s += kPlanThreads) {
@@ -106,54 +125,484 @@ __device__ __forceinline__ Unit unit_at(const PromptArgs &a, int x) {
 }
 
 // ---------------------------------------------------------------------------
-// attention: one warp per row (token, query head)
+// attention
 // ---------------------------------------------------------------------------
+constexpr int kTile = 128;                     // keys of a tile, rows of a row tile
+constexpr int kLoadWarp = 0, kMmaWarp = 1, kPlanWarp = 2, kSoftmaxWarp = 4;
+constexpr int kThreads = 12 * 32;
+// Registers a thread: 168 at launch; the four single-warp roles give theirs to
+// the softmax (128 * 72 + 256 * 216 = 384 * 168).
+constexpr int kFewRegs = 72, kManyRegs = 216;
+constexpr float kRaise = 6.f;
+constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
 template <int D>
-__global__ void __launch_bounds__(256) prompt_attend_kernel(const PromptArgs a) {
-  constexpr int CPL = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float c = rsqrtf(static_cast<float>(D));
-  for (int x = blockIdx.x; x < a.ws_head->units; x += gridDim.x) {
-    const Unit u = unit_at(a, x);
-    const int rows = min(a.unit, u.len - u.t0) * a.G;
-    for (int r = warp; r < rows; r += 8) {
-      const int t = u.t0 + r / a.G, hq = u.h * a.G + r % a.G;
-      const int64_t row = u.start + t;
-      float q[CPL], o[CPL], m = -INFINITY, l = 0.f;
-      for (int e = 0; e < CPL; ++e) {
-        q[e] = c * __uint_as_float(static_cast<uint32_t>(a.q[row * a.q_stride + hq * D + lane * CPL + e]) << 16);
-        o[e] = 0.f;
-      }
-      for (int j = 0; j <= t; ++j) {
-        const uint16_t *k = a.k + (static_cast<int64_t>(u.start) + j) * a.k_stride + u.h * D + lane * CPL;
-        const uint16_t *v = a.v + (static_cast<int64_t>(u.start) + j) * a.v_stride + u.h * D + lane * CPL;
-        float z = 0.f;
-        for (int e = 0; e < CPL; ++e) z += q[e] * __uint_as_float(static_cast<uint32_t>(k[e]) << 16);
-        for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-        const float mn = fmaxf(m, z), keep = expf(m - mn), p = expf(z - mn);
-        l = l * keep + p;
-        for (int e = 0; e < CPL; ++e) o[e] = o[e] * keep + p * __uint_as_float(static_cast<uint32_t>(v[e]) << 16);
-        m = mn;
-      }
-      for (int e = 0; e < CPL; ++e) {
-        uint32_t w;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(0.f), "f"(o[e] / l));
-        a.out[(row * a.Hq + hq) * D + lane * CPL + e] = static_cast<uint16_t>(w);
-      }
-      if (a.lse != nullptr && lane == 0) a.lse[row * a.Hq + hq] = m + logf(l);
+struct Smem {
+  static constexpr uint32_t HALF = 128 * 128;           // 64 channels of 128 rows
+  static constexpr uint32_t TILE = HALF * (D / 64);
+  static constexpr int STAGES = D == 128 ? 2 : 4;       // places for tiles of K, and of V
+  static constexpr uint32_t q = 0;                      // [2] row tiles
+  static constexpr uint32_t k = q + 2 * TILE;
+  static constexpr uint32_t v = k + STAGES * TILE;
+  static constexpr uint32_t bars = v + STAGES * TILE;
+  static constexpr uint32_t tmem = bars + 64 * 8;       // tensor memory address, then the abort flag
+  static constexpr uint32_t units = tmem + 16;          // [2] {start, len, t0, h}; start -1: the end
+  static constexpr uint32_t bytes = units + 32;
+  static_assert(bytes <= 227 * 1024, "shared memory");
+};
+
+enum Bar : int {
+  B_Q = 0, B_QFREE = 1, B_S = 2, B_P = 4, B_O = 6, B_OFREE = 8, B_UNIT = 10, B_UNITFREE = 12, B_KFULL = 14,
+  B_KFREE = 18, B_VFULL = 22, B_VFREE = 26, B_END = 30, B_COUNT = 31
+};
+
+// What the roles need to know of a unit: tokens t0 .. and the tiles of keys of
+// each row tile (the first `step` tokens, and the next).
+struct Work {
+  int start, len, t0, h;
+  int tiles[2], all;
+  __device__ __forceinline__ Work(uint4 u, int step) {
+    start = static_cast<int>(u.x);
+    len = static_cast<int>(u.y);
+    t0 = static_cast<int>(u.z);
+    h = static_cast<int>(u.w);
+    tiles[0] = (min(len, t0 + step) + kTile - 1) / kTile;
+    tiles[1] = t0 + step < len ? (min(len, t0 + 2 * step) + kTile - 1) / kTile : 0;
+    all = max(tiles[0], tiles[1]);
+  }
+};
+
+// The units one after the other, as the plan warp hands them out.
+struct Units {
+  const InlineWaiter &wait;
+  uint32_t at;
+  int n = 0;
+  __device__ __forceinline__ Units(const InlineWaiter &w, uint32_t units) : wait(w), at(units) {}
+  __device__ __forceinline__ uint4 next() {
+    wait(B_UNIT + (n & 1), (n >> 1) & 1);
+    return lds128(at + 16 * (n & 1));
+  }
+  // (one lane of each warp that has read it)
+  __device__ __forceinline__ void done(int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&wait.bars[B_UNITFREE + (n & 1)]);
+    ++n;
+  }
+};
+
+__device__ __forceinline__ void plan_role(const PromptArgs &a, uint32_t units, const InlineWaiter &wait, int lane) {
+  const int total = a.ws_head->units;
+  for (int n = 0;; ++n) {
+    int x = 0;
+    if (lane == 0) x = atomicAdd(&a.ws_head->next, 1);
+    x = __shfl_sync(0xffffffffu, x, 0);
+    const bool end = x >= total;
+    Unit u = {-1, 0, 0, 0};
+    if (!end) u = unit_at(a, x);
+    wait(B_UNITFREE + (n & 1), ((n >> 1) & 1) ^ 1);
+    if (lane == 0) {
+      sts128(units + 16 * (n & 1), u.start, u.len, u.t0, u.h);
+      mbar_arrive(&wait.bars[B_UNIT + (n & 1)]);
     }
+    if (end) return;
+  }
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
+template <int D>
+__device__ __forceinline__ void load_role(const PromptArgs &a, const CUtensorMap *qm, const CUtensorMap *km,
+                                          const CUtensorMap *vm, uint32_t base, const InlineWaiter &wait, int lane) {
+  using L = Smem<D>;
+  const int step = a.unit / 2;
+  const uint32_t qbytes = step * a.G * D * 2;
+  Units units(wait, base + L::units);
+  int st = 0;
+  uint32_t ph = 1;  // of the places for K and V
+  for (;;) {
+    const uint4 u = units.next();
+    if (static_cast<int>(u.x) < 0) break;
+    const Work w(u, step);
+    wait(B_QFREE, (units.n & 1) ^ 1);
+    units.done(lane);
+    const bool go = lane == 0 && !*wait.abort;  // (after a wait that ran out nobody reads: no further copies)
+    if (go) {
+      uint64_t *bar = &wait.bars[B_Q];
+      const bool two = w.tiles[1] > 0;
+      mbar_arrive_expect_tx(bar, two ? 2 * qbytes : qbytes);
+#pragma unroll
+      for (int c = 0; c < D; c += 64) {
+        tma_load(base + L::q + c / 64 * L::HALF, qm, c, w.h * a.G, w.start + w.t0, bar);
+        if (two) tma_load(base + L::q + L::TILE + c / 64 * L::HALF, qm, c, w.h * a.G, w.start + w.t0 + step, bar);
+      }
+    }
+    for (int j = 0; j < w.all; ++j) {
+      wait(B_KFREE + st, ph);
+      if (go) {
+        mbar_arrive_expect_tx(&wait.bars[B_KFULL + st], L::TILE);
+#pragma unroll
+        for (int c = 0; c < D; c += 64)
+          tma_load(base + L::k + st * L::TILE + c / 64 * L::HALF, km, c, w.h, w.start + j * kTile, &wait.bars[B_KFULL + st]);
+      }
+      wait(B_VFREE + st, ph);
+      if (go) {
+        mbar_arrive_expect_tx(&wait.bars[B_VFULL + st], L::TILE);
+#pragma unroll
+        for (int c = 0; c < D; c += 64)
+          tma_load(base + L::v + st * L::TILE + c / 64 * L::HALF, vm, c, w.h, w.start + j * kTile, &wait.bars[B_VFULL + st]);
+      }
+      if (++st == L::STAGES) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+  }
+  // no copy in flight when the CTA exits: all places are read, or (a wait ran
+  // out) a millisecond goes by
+  if (*wait.abort) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000) {
+    }
+  }
+  for (int i = 0; i < L::STAGES; ++i) {
+    wait(B_KFREE + st, ph);
+    wait(B_VFREE + st, ph);
+    if (++st == L::STAGES) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+}
+
+// The whole warp walks the steps and one elected lane issues, so that what the
+// products take stays in uniform registers.
+template <int D>
+__device__ __forceinline__ void product_role(const PromptArgs &a, uint32_t base, const InlineWaiter &wait, uint32_t tmem_addr,
+                                             int lane) {
+  using L = Smem<D>;
+  constexpr uint32_t id_s = mma_idesc_bf16(128, kTile, false), id_o = mma_idesc_bf16(128, D, true);
+  const bool leader = elect_one();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_addr, 0);
+  const uint64_t dq = mma_desc(base + L::q, 16, 1024), dk = mma_desc(base + L::k, 16, 1024),
+                 dv = mma_desc(base + L::v, L::HALF, 1024);
+  const int step = a.unit / 2;
+  Units units(wait, base + L::units);
+  int ks = 0, vs = 0;            // places of the tiles of K and of V,
+  uint32_t kp = 0, vp = 0;       // and their parities
+  uint32_t np = 0, no = 0;       // bit i: parity of warpgroup i's steps, and of its units
+  for (;;) {
+    const uint4 u = units.next();
+    if (static_cast<int>(u.x) < 0) break;
+    const Work w(u, step);
+    wait(B_Q, units.n & 1);
+    units.done(lane);
+#pragma unroll 1
+    for (int j = -1; j < w.all; ++j) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool other = i == 0 && j < w.tiles[1];  // the other warpgroup uses this tile after this one
+        if (j >= 0 && j < w.tiles[i]) {
+          wait(B_P + i, (np >> i) & 1);
+          np ^= 1u << i;
+          if (j == 0) {
+            wait(B_OFREE + i, ((no >> i) & 1) ^ 1);
+            no ^= 1u << i;
+          }
+          if (i == 0 || w.tiles[0] <= j) {
+            wait(B_VFULL + vs, vp);
+            const int rows = w.len - j * kTile;
+            if (rows < kTile) {
+              // what lies behind the sequence may be anything, and 0 times it is not 0
+              const uint32_t to = base + L::v + vs * L::TILE;
+              for (int x = rows * 8 + lane; x < kTile * 8; x += 32)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) sts128(to + c * L::HALF + 16 * x, 0u, 0u, 0u, 0u);
+              fence_proxy_async_shared();
+            }
+          }
+          __syncwarp();
+          tmem_fence_after();
+          if (leader) {
+            const uint64_t v = dv + vs * (L::TILE / 16);
+            const uint32_t p = tmem + 128 * i, o = tmem + 256 + 128 * i;
+#pragma unroll
+            for (int e = 0; e < kTile / 16; ++e) mma_f16_ts(o, p + 8 * e, v + e * (2048 / 16), id_o, j > 0 || e > 0);
+            if (!other) mma_commit(&wait.bars[B_VFREE + vs]);
+            if (j + 1 == w.tiles[i]) mma_commit(&wait.bars[B_O + i]);
+          }
+          __syncwarp();
+          if (!other && ++vs == L::STAGES) {
+            vs = 0;
+            vp ^= 1;
+          }
+        }
+        if (j + 1 < w.tiles[i]) {
+          const bool more = i == 0 && j + 1 < w.tiles[1];
+          if (i == 0 || w.tiles[0] <= j + 1) wait(B_KFULL + ks, kp);
+          __syncwarp();
+          tmem_fence_after();
+          if (leader) {
+            const uint64_t q = dq + i * (L::TILE / 16), k = dk + ks * (L::TILE / 16);
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) {
+              const uint32_t off = ((e / 4) * L::HALF + (e % 4) * 32) / 16;
+              mma_f16_ss(tmem + 128 * i, q + off, k + off, id_s, e > 0);
+            }
+            mma_commit(&wait.bars[B_S + i]);
+            if (!more) {
+              mma_commit(&wait.bars[B_KFREE + ks]);
+              if (j + 2 == w.all) mma_commit(&wait.bars[B_QFREE]);
+            }
+          }
+          __syncwarp();
+          if (!more && ++ks == L::STAGES) {
+            ks = 0;
+            kp ^= 1;
+          }
+        }
+      }
+    }
+  }
+  // nothing in flight when tensor memory is given back
+  if (leader) mma_commit(&wait.bars[B_END]);
+  __syncwarp();
+  wait(B_END, 0);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// 32 bytes of global memory, 32-byte aligned.
+__device__ __forceinline__ void store_32(void *to, const uint32_t *r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+template <int D>
+__device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base, const InlineWaiter &wait, uint32_t tmem) {
+  using L = Smem<D>;
+  const int wg = (threadIdx.x >> 7) - kSoftmaxWarp / 4, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+  const uint32_t S = tmem + lanes + 128 * wg, O = tmem + lanes + 256 + 128 * wg;
+  const int step = a.unit / 2, r = 32 * warp + lane, rt = r / a.G, g = r - rt * a.G;
+  const int near = 32 * warp / a.G;  // the warp's first token
+  const float c = rsqrtf(static_cast<float>(D)) * kLog2E;
+  Units units(wait, base + L::units);
+  uint32_t ns = 0, no = 0;  // steps and units of this warpgroup so far
+  for (;;) {
+    const uint4 u = units.next();
+    if (static_cast<int>(u.x) < 0) break;
+    const Work w(u, step);
+    units.done(lane);
+    const int tiles = wg ? w.tiles[1] : w.tiles[0], t = w.t0 + wg * step + rt;
+    if (tiles == 0) continue;
+    const bool live = rt < step && t < w.len;
+    const int limit = live ? t + 1 : INT_MAX, nearest = w.t0 + wg * step + near + 1;
+    float mu = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < tiles; ++j) {
+      wait(B_S + wg, ns & 1);
+      ++ns;
+      __syncwarp();
+      tmem_fence_after();
+      uint32_t w0[32], w1[32], w2[32], w3[32];
+      tmem_ld32(S, w0);
+      tmem_ld32(S + 32, w1);
+      tmem_ld32(S + 64, w2);
+      tmem_ld32(S + 96, w3);
+      tmem_wait_ld(w0);
+      tmem_wait_ld(w1);
+      tmem_wait_ld(w2);
+      tmem_wait_ld(w3);
+      if (nearest < (j + 1) * kTile) {  // some row of the warp does not see the whole tile
+        const int seen = limit - j * kTile;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          if (e >= seen) w0[e] = 0xFF800000u;
+          if (32 + e >= seen) w1[e] = 0xFF800000u;
+          if (64 + e >= seen) w2[e] = 0xFF800000u;
+          if (96 + e >= seen) w3[e] = 0xFF800000u;
+        }
+      }
+      float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        x0 = max3(x0, __uint_as_float(w0[e]), __uint_as_float(w0[e + 1]));
+        x1 = max3(x1, __uint_as_float(w1[e]), __uint_as_float(w1[e + 1]));
+        x2 = max3(x2, __uint_as_float(w2[e]), __uint_as_float(w2[e + 1]));
+        x3 = max3(x3, __uint_as_float(w3[e]), __uint_as_float(w3[e + 1]));
+      }
+      const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * c;
+      // (each row for itself: what other rows of the warp hold changes nothing)
+      const bool raise = top > mu + kRaise || (mu == -INFINITY && top > mu);
+      if (__any_sync(0xffffffffu, raise)) {
+        const float keep = raise ? mu == -INFINITY ? 0.f : fast_exp2(mu - top) : 1.f;
+        if (raise) mu = top;
+        l *= keep;
+        if (j > 0) {
+#pragma unroll 1
+          for (int cc = 0; cc < D / 16; ++cc) {
+            uint32_t o[16];
+            tmem_ld16(O + 16 * cc, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+            tmem_st16(O + 16 * cc, o);
+          }
+        }
+      }
+      const float neg = mu == -INFINITY ? 0.f : -mu;
+      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+      auto exponentials = [&](uint32_t(&x)[32], uint32_t to) {
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          float a0, a1, a2, a3;
+          fma_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]), c, c, neg, neg, a0, a1);
+          fma_f32x2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), c, c, neg, neg, a2, a3);
+          a0 = fast_exp2(a0);
+          a1 = fast_exp2(a1);
+          a2 = fast_exp2(a2);
+          a3 = fast_exp2(a3);
+          add_f32x2(s0, s1, a0, a1, s0, s1);
+          add_f32x2(s2, s3, a2, a3, s2, s3);
+          p[e / 2] = f32x2_to_bf16x2(a0, a1);
+          p[e / 2 + 1] = f32x2_to_bf16x2(a2, a3);
+        }
+        tmem_st16(to, p);
+      };
+      exponentials(w0, S);
+      exponentials(w1, S + 16);
+      exponentials(w2, S + 32);
+      exponentials(w3, S + 48);
+      l += (s0 + s1) + (s2 + s3);
+      tmem_wait_st();
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&wait.bars[B_P + wg]);
+    }
+    // ---- the rows' outputs
+    wait(B_O + wg, no & 1);
+    ++no;
+    __syncwarp();
+    tmem_fence_after();
+    const int64_t row = static_cast<int64_t>(w.start + t) * a.Hq + w.h * a.G + g;
+    const float inv = 1.f / l;
+    const bool store = live && !*wait.abort;  // (after a wait that ran out the unit may be none)
+#pragma unroll
+    for (int cc = 0; cc < D / 32; ++cc) {
+      uint32_t o[32];
+      tmem_ld32(O + 32 * cc, o);
+      tmem_wait_ld(o);
+      uint32_t b[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        b[e] = f32x2_to_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+      if (store) {
+        store_32(a.out + row * D + 32 * cc, b);
+        store_32(a.out + row * D + 32 * cc + 16, b + 8);
+      }
+    }
+    if (store && a.lse != nullptr) a.lse[row] = (mu + log2f(l)) * kLn2;
+    tmem_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&wait.bars[B_OFREE + wg]);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PromptArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  using L = Smem<D>;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
+  const uint32_t base = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t *const tm = reinterpret_cast<uint32_t *>(smem + L::tmem);
+  if (warp == kLoadWarp) {
+    // arrivals per phase: 4 for a warpgroup's warps, 10 for all that read a unit, else 1
+    for (int i = lane; i < B_COUNT; i += 32) {
+      const bool four = (i >= B_P && i < B_P + 2) || (i >= B_OFREE && i < B_OFREE + 2);
+      mbar_init(&bars[i], four ? 4 : i >= B_UNITFREE && i < B_UNITFREE + 2 ? 10 : 1);
+    }
+    mbar_init_fence();
+    if (lane == 0) {
+      prefetch_tensormap(&qmap);
+      prefetch_tensormap(&kmap);
+      prefetch_tensormap(&vmap);
+      *reinterpret_cast<volatile uint32_t *>(tm + 1) = 0;
+      for (int i = 0; i < 2; ++i) sts128(base + L::units + 16 * i, 0xFFFFFFFFu, 0u, 0u, 0u);
+    }
+  }
+  __syncwarp();
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(tm), 512);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tm);
+  grid_wait();  // the plan
+  const InlineWaiter wait = {bars, tm + 1, a.err};
+  if (warp >= kSoftmaxWarp) {
+    more_registers<kManyRegs>();
+    softmax_role<D>(a, base, wait, tmem);
+  } else {
+    fewer_registers<kFewRegs>();
+    if (warp == kLoadWarp) load_role<D>(a, &qmap, &kmap, &vmap, base, wait, lane);
+    else if (warp == kMmaWarp) product_role<D>(a, base, wait, tmem, lane);
+    else if (warp == kPlanWarp) plan_role(a, base + L::units, wait, lane);
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tmem_fence_after();
+    tmem_free(tmem, 512);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_prompt_attention(int head_dim, const PromptArgs &a, int sms, cudaStream_t stream) {
+template <int D>
+static cudaError_t attend(const PromptArgs &a, const PromptMaps &m, int sms, cudaStream_t stream) {
+  auto kern = prompt_attend_kernel<D>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  static std::atomic<unsigned long long> done{0};  // devices whose limit is raised
+  if (!((done.load(std::memory_order_acquire) >> dev) & 1ull)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes)) != cudaSuccess)
+      return e;
+    done.fetch_or(1ull << dev, std::memory_order_acq_rel);
+  }
+  return launch_overlapped(kern, sms, kThreads, Smem<D>::bytes, stream, m.q, m.k, m.v, a);
+}
+
+cudaError_t launch_prompt_attention(int head_dim, const PromptArgs &a, const PromptMaps &m, int sms, cudaStream_t stream) {
   prompt_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (head_dim == 128) prompt_attend_kernel<128><<<8 * sms, 256, 0, stream>>>(a);
-  else prompt_attend_kernel<64><<<8 * sms, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return head_dim == 128 ? attend<128>(a, m, sms, stream) : attend<64>(a, m, sms, stream);
 }
 
 }  // namespace kvq

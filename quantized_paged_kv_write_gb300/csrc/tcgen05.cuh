@@ -75,6 +75,11 @@ constexpr uint32_t mma_idesc_f16(int m, int n, bool b_n_major) {
          (static_cast<uint32_t>(m / 16) << 24);
 }
 
+// The same for BF16 operands (type 1 in both fields).
+constexpr uint32_t mma_idesc_bf16(int m, int n, bool b_n_major) {
+  return mma_idesc_f16(m, n, b_n_major) | (1u << 7) | (1u << 10);
+}
+
 // Shared memory descriptor of a tile stored as rows of 128 bytes with the
 // 128-byte swizzle (16-byte chunk index ^ row % 8, 1024-byte aligned groups of
 // 8 rows): address and byte offsets in units of 16, version 1 (bits 46-48),
