@@ -744,7 +744,7 @@ static size_t evict_ws(int rows, int heads, int64_t max_positions, size_t *list)
 
 static int check_evict(int32_t num_rows, int32_t num_kv_heads, int32_t max_positions) {
   if (num_rows < 0 || num_kv_heads < 1 || max_positions < 0) return KVQ_ERR_INVALID_ARG;
-  return num_rows > 8192 || num_kv_heads > 8 ? KVQ_ERR_UNSUPPORTED : KVQ_OK;
+  return num_rows > 8192 || num_kv_heads > 8 || max_positions > (1 << 30) ? KVQ_ERR_UNSUPPORTED : KVQ_OK;
 }
 
 int kvq_evict_workspace_size(int32_t num_rows, int32_t num_kv_heads, int32_t max_positions, size_t *bytes) {

@@ -211,6 +211,25 @@ def test_ties_and_odd_weights(kind):
     Both("int8", "int8", 3, 64, [3001, 2990], seed=2, weights=w).evict([1500, 2900], [10, 200], [3, 0])
 
 
+@pytest.mark.parametrize("h,rows,length,kind", [(1, 1, 20000, "few"), (2, 3, 9001, "zero"), (4, 9, 8192, "rand"), (1, 70, 8192, "few"),
+                                                (8, 40, 8195, "few"), (2, 1, 33000, "rand"), (3, 1, 70001, "few")])
+def test_long_rows_with_ties(h, rows, length, kind):
+    """One CTA, a cluster of two, four and eight for each (row, head), several steps of a CTA."""
+    rng = np.random.default_rng(length)
+    w = np.zeros((rows, h, length), np.float32) if kind == "zero" else rng.integers(0, 4, (rows, h, length)).astype(np.float32)
+    if kind == "rand":
+        w = rng.random(w.shape).astype(np.float32) ** 5
+    ctx = [length] + [int(x) for x in rng.integers(0, 150, rows - 1)]
+    if rows < 10:
+        ctx[-1] = length - 77
+    keep = [length // 2 if n > 1000 else n // 2 for n in ctx]
+    s = Both("int8", "int8", h, 64, ctx, seed=7, weights=w)
+    s.evict(keep, [int(x) for x in rng.integers(0, 70, rows)], [int(x) for x in rng.integers(0, 40, rows)])
+    s.ctx = keep
+    s.dc = _i32(keep)
+    s.evict([max(0, n - 3) for n in keep], [1] * rows)
+
+
 def test_rows_that_are_refused_stay_as_they_are():
     s = Both("fp8", "v4", 2, 128, [100, 100, 100, 100, 100, 100], seed=3, length=112)
     refs = np.ones(s.fmt.num_blocks, np.int64)
