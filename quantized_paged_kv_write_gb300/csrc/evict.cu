@@ -11,6 +11,8 @@
 // Codes and scales move byte for byte ("PidokuInfra 12 KV Cache Quantization",
 // §5 Where the scales live: a scale for each token and head), so a head's token
 // keeps its values.  The pages have no eviction: it is this library's.
+#include <atomic>
+
 #include "common.cuh"
 #include "kvq_internal.h"
 
@@ -28,10 +30,12 @@ __device__ __forceinline__ unsigned order_of(float x) {
 // which tokens stay
 // ---------------------------------------------------------------------------
 // One cluster of CTAs per (row, kv head), each with an even part of the
-// candidates: the threshold by three passes over their weights (11, 11 and 10
-// bits, from the top; the CTAs add up their histograms), then the lists of places
-// and of tokens to go there.
+// candidates, each warp with an even part of that: the threshold by three passes
+// over their weights (11, 11 and 10 bits, from the top; the CTAs add up their
+// histograms), then what every warp has of larger and equal ones, then the lists
+// of places and of tokens to go there.
 constexpr int kBins = 2048;
+constexpr int kHeld = 16384;  // keys that a CTA holds at most: 64 KB, three CTAs an SM
 
 __device__ __forceinline__ unsigned cluster_rank() {
   unsigned x;
@@ -56,19 +60,6 @@ __device__ __forceinline__ uint4 remote128(uint32_t at, unsigned rank) {
   return v;
 }
 
-// The sum of a warp's `own` over the warps before this one; *all over all.
-template <int T>
-__device__ __forceinline__ unsigned warps_before(unsigned own, unsigned *sums, unsigned *all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0) sums[warp] = own;
-  __syncthreads();
-  const unsigned s = lane < T / 32 ? sums[lane] : 0u;
-  *all = __reduce_add_sync(0xffffffffu, s);
-  const unsigned before = __reduce_add_sync(0xffffffffu, lane < warp ? s : 0u);
-  __syncthreads();
-  return before;
-}
-
 // A lane has bits of four consecutive positions, the warp of 128: the number set
 // before this lane's.
 __device__ __forceinline__ unsigned lanes_before(unsigned bits) {
@@ -79,21 +70,24 @@ __device__ __forceinline__ unsigned lanes_before(unsigned bits) {
   return n;
 }
 
-// A step is up to T KV vectors of four weights, a warp's in one piece: vector u of
-// a lane is 32 behind its vector u - 1.  ONE: a step holds all candidates, which
-// stay in registers; else each pass reads them again (from L2, after the first).
-// CLUSTER: more than one CTA.
-template <int T, int KV, bool ONE, bool CLUSTER>
-__global__ void __launch_bounds__(T, 768 / T) evict_select_kernel(const EvictArgs a, const int ctas) {
-  static_assert(!(ONE && CLUSTER), "one step of one CTA");
-  static_assert(4 * KV <= 32, "a bit for each of a lane's weights");
+// What a warp or a CTA has: larger and equal keys below `end`, and from there on.
+struct Counts {
+  unsigned larger_low, equal_low, larger, equal;
+};
+
+// HELD: the keys stay in shared memory; else each pass makes them from the weights
+// again (in L2 after the first).  CLUSTER: more than one CTA.
+template <int T, bool HELD, bool CLUSTER>
+__global__ void __launch_bounds__(T, 1536 / T) evict_select_kernel(const EvictArgs a, const int ctas) {
+  constexpr int W = T / 32;
+  extern __shared__ uint4 held[];
   __shared__ __align__(16) unsigned hist[kBins];
-  __shared__ unsigned sums[32];
-  __shared__ __align__(16) unsigned counts[4];
-  __shared__ unsigned chosen, left, equals;
+  __shared__ unsigned sums[W];
+  __shared__ __align__(16) Counts counts[W + 1];  // the warps', and the CTA's
+  __shared__ unsigned chosen, left;
   grid_release();
   const int x = CLUSTER ? blockIdx.x / ctas : blockIdx.x, rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
-  const int r = x / a.H, h = x - r * a.H, tid = threadIdx.x;
+  const int r = x / a.H, h = x - r * a.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool reports = tid == 0 && rank == 0;
   const int n = __ldg(a.ctx + r), keep = __ldg(a.keep + r), recent = __ldg(a.recent + r);
   const int pinned = a.pinned != nullptr ? __ldg(a.pinned + r) : 0;
@@ -111,50 +105,66 @@ __global__ void __launch_bounds__(T, 768 / T) evict_select_kernel(const EvictArg
   // Vectors of four weights on 16-byte boundaries: vector v holds the positions
   // 4 v - skew .. + 3; those outside the candidates are masked.
   const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(weights) >> 2) & 3);
-  int v0 = (p + skew) / 4, v1 = (last + skew + 3) / 4;
-  if constexpr (CLUSTER) {
-    const int per = (v1 - v0 + ctas - 1) / ctas;
-    v0 = min(v1, v0 + rank * per);
-    v1 = min(v1, v0 + per);
-  }
-  // the keys of a step, 0 where there is no candidate
-  unsigned key[KV][4];
-  int su = 0, first = 0;  // vectors of a lane, and its first one
-  auto load = [&](int base) {
-    su = (min(v1 - base, T * KV) + T - 1) / T;
-    first = base + (tid >> 5) * 32 * su + (tid & 31);
-    float4 y[KV];
-#pragma unroll
-    for (int u = 0; u < KV; ++u) {
-      if (u >= su) break;
-      const int v = first + 32 * u, i = 4 * v - skew;
-      y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (v < v1 && i >= p && i + 4 <= last) {
-        y[u] = *reinterpret_cast<const float4 *>(weights + i);
-      } else if (v < v1) {
-        if (i >= p && i < last) y[u].x = weights[i];
-        if (i + 1 >= p && i + 1 < last) y[u].y = weights[i + 1];
-        if (i + 2 >= p && i + 2 < last) y[u].z = weights[i + 2];
-        if (i + 3 >= p && i + 3 < last) y[u].w = weights[i + 3];
-      }
+  const int all0 = (p + skew) / 4, all1 = (last + skew + 3) / 4, part = (all1 - all0 + ctas - 1) / ctas;
+  const int v0 = min(all1, all0 + rank * part), v1 = min(all1, v0 + part);
+  const int share = ((v1 - v0 + W - 1) / W + 31) / 32 * 32;  // whole rounds of a warp
+  const int w0 = min(v1, v0 + warp * share), w1 = min(v1, w0 + share);
+  auto load = [&](int v) {
+    const int i = 4 * v - skew;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i >= p && i + 4 <= last) {
+      y = *reinterpret_cast<const float4 *>(weights + i);
+    } else {
+      if (i >= p && i < last) y.x = weights[i];
+      if (i + 1 >= p && i + 1 < last) y.y = weights[i + 1];
+      if (i + 2 >= p && i + 2 < last) y.z = weights[i + 2];
+      if (i + 3 >= p && i + 3 < last) y.w = weights[i + 3];
     }
+    return y;
+  };
+  auto keys_of = [&](int v, const float4 &y) {
+    const int i = 4 * v - skew;
+    uint4 k = make_uint4(order_of(y.x), order_of(y.y), order_of(y.z), order_of(y.w));
+    if (i < p || i + 4 > last) {
+      if (i < p || i >= last) k.x = 0u;
+      if (i + 1 < p || i + 1 >= last) k.y = 0u;
+      if (i + 2 < p || i + 2 >= last) k.z = 0u;
+      if (i + 3 < p || i + 3 >= last) k.w = 0u;
+    }
+    return k;
+  };
+  // f(vector, its keys) for this warp's vectors in rounds of 32, four of a lane
+  // in flight; lanes past the end have keys 0
+  constexpr int U = 4;
+  auto each = [&](auto from, auto f) {
+#pragma unroll 1
+    for (int v = w0; v < w1; v += 32 * U) {
+      uint4 k[U];
+      from(v, k);
 #pragma unroll
-    for (int u = 0; u < KV; ++u) {
-      if (u >= su) break;
-      const int v = first + 32 * u, i = 4 * v - skew;
-      key[u][0] = order_of(y[u].x);
-      key[u][1] = order_of(y[u].y);
-      key[u][2] = order_of(y[u].z);
-      key[u][3] = order_of(y[u].w);
-      if (v >= v1 || i < p || i + 4 > last)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (v >= v1 || i + e < p || i + e >= last) key[u][e] = 0u;
+      for (int u = 0; u < U; ++u)
+        if (v + 32 * u < w1) f(v + 32 * u + lane, k[u]);
     }
   };
-  if constexpr (ONE) load(v0);
-  // (while they are under way) every block of the row, and nobody else's among
-  // those to be written
+  auto of_weights = [&](int v, uint4(&k)[U]) {
+    float4 y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) y[u] = v + 32 * u + lane < w1 ? load(v + 32 * u + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      k[u] = v + 32 * u + lane < w1 ? keys_of(v + 32 * u + lane, y[u]) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto of_held = [&](int v, uint4(&k)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      k[u] = v + 32 * u + lane < w1 ? held[v + 32 * u + lane - v0] : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto walk = [&](auto f) {
+    if constexpr (HELD) each(of_held, f);
+    else each(of_weights, f);
+  };
+  for (int i = tid; i < kBins; i += T) hist[i] = 0;
+  // every block of the row, and nobody else's among those to be written
   const int32_t *table = a.tables + static_cast<int64_t>(r) * a.max_blocks;
   bool bad = false, shared = false;
   for (int i = tid; i < (n + kBlockSize - 1) / kBlockSize; i += T) {
@@ -162,7 +172,6 @@ __global__ void __launch_bounds__(T, 768 / T) evict_select_kernel(const EvictArg
     if (id < 0 || id >= a.num_blocks) bad = true;
     else if (a.refs != nullptr && i >= p / kBlockSize && i * kBlockSize < keep && __ldg(a.refs + id) != 1) shared = true;
   }
-  for (int i = tid; i < kBins; i += T) hist[i] = 0;
   bad = __syncthreads_or(bad);
   shared = __syncthreads_or(shared);
   if (bad || shared) {
@@ -172,25 +181,36 @@ __global__ void __launch_bounds__(T, 768 / T) evict_select_kernel(const EvictArg
     return;
   }
   if (reports && h == 0) a.kept[r] = keep;
+  if (end == p) {  // none of the candidates stays: no places between what stays anyway
+    if (reports) *meta = {0, 1, keep, w};
+    return;
+  }
   // ---- the need-th largest key, and how many of its equals are kept
-  unsigned prefix = 0xFFFFFFFFu, need = end - p;  // (nothing needed: nothing is above)
-  bool partial = need == 0;                       // of the equals some stay and some go
-  if (need > 0) {
+  unsigned prefix = 0, need = end - p;
+  {
     unsigned mask = 0;
-    prefix = 0;
 #pragma unroll 1
     for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
       const unsigned digit = shift == 0 ? 1023u : 2047u;
-#pragma unroll 1
-      for (int base = v0; base < v1; base += T * KV) {
-        if constexpr (!ONE) load(base);
-#pragma unroll
-        for (int u = 0; u < KV; ++u) {
-          if (u >= su) break;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key[u][e] != 0u && (key[u][e] & mask) == prefix) atomicAdd(&hist[(key[u][e] >> shift) & digit], 1u);
-        }
+      auto count = [&](unsigned k) {
+        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
+      };
+      if (shift == 21) {
+        each(of_weights, [&](int v, const uint4 &k) {
+          if constexpr (HELD)
+            if (v < w1) held[v - v0] = k;
+          if (k.x != 0u) atomicAdd(&hist[k.x >> 21], 1u);
+          if (k.y != 0u) atomicAdd(&hist[k.y >> 21], 1u);
+          if (k.z != 0u) atomicAdd(&hist[k.z >> 21], 1u);
+          if (k.w != 0u) atomicAdd(&hist[k.w >> 21], 1u);
+        });
+      } else {
+        walk([&](int, const uint4 &k) {
+          count(k.x);
+          count(k.y);
+          count(k.z);
+          count(k.w);
+        });
       }
       sync_all<CLUSTER>();
       // digits from the largest: the one in which the need-th lies
@@ -200,36 +220,26 @@ __global__ void __launch_bounds__(T, 768 / T) evict_select_kernel(const EvictArg
       unsigned bin[PER], own = 0;
 #pragma unroll
       for (int k = 0; k < PER; ++k) bin[k] = 0;
-      if constexpr (CLUSTER) {
-#pragma unroll 1
-        for (int j = 0; j < ctas; ++j)
-#pragma unroll
-          for (int k = 0; k < PER; k += 4) {
-            const uint4 y = remote128(smem_u32(hist + b0 + k), j);
-            bin[k] += y.x;
-            bin[k + 1] += y.y;
-            bin[k + 2] += y.z;
-            bin[k + 3] += y.w;
-          }
-      } else {
+      for (int j = 0; j < (CLUSTER ? ctas : 1); ++j)
 #pragma unroll
         for (int k = 0; k < PER; k += 4) {
-          const uint4 y = *reinterpret_cast<const uint4 *>(hist + b0 + k);
-          bin[k] = y.x;
-          bin[k + 1] = y.y;
-          bin[k + 2] = y.z;
-          bin[k + 3] = y.w;
+          const uint4 y = CLUSTER ? remote128(smem_u32(hist + b0 + k), j) : *reinterpret_cast<const uint4 *>(hist + b0 + k);
+          bin[k] += y.x;
+          bin[k + 1] += y.y;
+          bin[k + 2] += y.z;
+          bin[k + 3] += y.w;
         }
-      }
 #pragma unroll
       for (int k = 0; k < PER; ++k) own += bin[k];
-      unsigned before = own, all;
+      unsigned before = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned y = __shfl_up_sync(0xffffffffu, before, o);
-        if ((tid & 31) >= o) before += y;
+        if (lane >= o) before += y;
       }
-      before += warps_before<T>(__shfl_sync(0xffffffffu, before, 31), sums, &all) - own;
+      if (lane == 31) sums[warp] = before;
+      __syncthreads();
+      before += __reduce_add_sync(0xffffffffu, lane < warp ? sums[min(lane, W - 1)] : 0u) - own;
       if (before < need && need <= before + own) {
         bool found = false;
 #pragma unroll
@@ -238,7 +248,6 @@ __global__ void __launch_bounds__(T, 768 / T) evict_select_kernel(const EvictArg
             found = true;
             chosen = b0 + k;
             left = need - before;
-            equals = bin[k];
           }
           before += bin[k];
         }
@@ -247,126 +256,91 @@ __global__ void __launch_bounds__(T, 768 / T) evict_select_kernel(const EvictArg
       prefix |= chosen << shift;
       mask |= digit << shift;
       need = left;
-      partial = need < equals;
       if (shift > 0) {
         for (int i = tid; i < kBins; i += T) hist[i] = 0;
         __syncthreads();
       }
     }
   }
-  // ---- what the CTAs before this one have
-  unsigned ties = 0;        // equals,
+  // ---- what the warps before this one have
+  Counts own = {0u, 0u, 0u, 0u};
+  walk([&](int v, const uint4 &k) {
+    const int low = end - (4 * v - skew);  // of the vector, below `end`
+    const unsigned key[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (key[e] > prefix) (e < low ? own.larger_low : own.larger) += 1u;
+      if (key[e] == prefix) (e < low ? own.equal_low : own.equal) += 1u;
+    }
+  });
+  own.larger_low = __reduce_add_sync(0xffffffffu, own.larger_low);
+  own.equal_low = __reduce_add_sync(0xffffffffu, own.equal_low);
+  own.larger = __reduce_add_sync(0xffffffffu, own.larger);
+  own.equal = __reduce_add_sync(0xffffffffu, own.equal);
+  if (lane == 0) counts[warp] = own;
+  __syncthreads();
+  unsigned ties = 0;        // equals before this warp,
   int holes = 0, late = 0;  // places and tokens
+  // takes one more part, the vectors [from, to)
+  auto pass = [&](const Counts &c, int from, int to) {
+    const unsigned stay = min(ties < need ? need - ties : 0u, c.equal_low + c.equal), low = min(stay, c.equal_low);
+    holes += max(0, min(end, 4 * to - skew) - max(p, 4 * from - skew)) - static_cast<int>(c.larger_low + low);
+    late += static_cast<int>(c.larger + stay - low);
+    ties += c.equal_low + c.equal;
+  };
   if constexpr (CLUSTER) {
-    if (tid < 4) counts[tid] = 0;
-    __syncthreads();
-    // larger and equal keys below `end`, and from there on
-    unsigned c[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 1
-    for (int base = v0; base < v1; base += T * KV) {
-      load(base);
-#pragma unroll
-      for (int u = 0; u < KV; ++u) {
-        if (u >= su) break;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool low = 4 * (first + 32 * u) - skew + e < end;
-          c[0] += key[u][e] > prefix && low;
-          c[1] += key[u][e] == prefix && low;
-          c[2] += key[u][e] > prefix && !low;
-          c[3] += key[u][e] == prefix && !low;
-        }
-      }
+    if (tid < 4) {
+      const unsigned *c = reinterpret_cast<const unsigned *>(counts) + tid;
+      unsigned s = 0;
+      for (int k = 0; k < W; ++k) s += c[4 * k];
+      reinterpret_cast<unsigned *>(counts + W)[tid] = s;
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const unsigned s = __reduce_add_sync(0xffffffffu, c[k]);
-      if ((tid & 31) == 0) atomicAdd(&counts[k], s);
-    }
-    sync_all<CLUSTER>();
-    const int per = ((last + skew + 3) / 4 - (p + skew) / 4 + ctas - 1) / ctas;
-#pragma unroll 1
+    sync_all<true>();
     for (int j = 0; j < rank; ++j) {
-      const uint4 y = remote128(smem_u32(counts), j);
-      const unsigned stay = min(ties < need ? need - ties : 0u, y.y + y.w), low = min(stay, y.y);
-      // the candidates below `end` of CTA j
-      const int from = max(p, 4 * ((p + skew) / 4 + j * per) - skew), to = min(end, 4 * ((p + skew) / 4 + (j + 1) * per) - skew);
-      holes += max(0, to - from) - static_cast<int>(y.x + low);
-      late += static_cast<int>(y.z + stay - low);
-      ties += y.y + y.w;
+      const uint4 y = remote128(smem_u32(counts + W), j);
+      pass({y.x, y.y, y.z, y.w}, min(all1, all0 + j * part), min(all1, all0 + (j + 1) * part));
     }
-    sync_all<CLUSTER>();  // nobody leaves while its counts are read
+    sync_all<true>();  // nobody leaves while its counts are read
   }
+#pragma unroll 1
+  for (int j = 0; j < warp; ++j) pass(counts[j], min(v1, v0 + j * share), min(v1, v0 + (j + 1) * share));
   // ---- the lists
   int *places = a.ws_list + static_cast<int64_t>(x) * 2 * a.cap, *tokens = places + a.cap;
-#pragma unroll 1
-  for (int base = v0; base < v1; base += T * KV) {
-    if constexpr (!ONE) load(base);
-    // bit 4 u + e: a candidate that stays
-    unsigned stay = 0, same = 0, in = 0, all;
+  walk([&](int v, const uint4 &k) {
+    const int i = 4 * v - skew;
+    const unsigned key[4] = {k.x, k.y, k.z, k.w};
+    unsigned stay = 0, same = 0, in = 0;
 #pragma unroll
-    for (int u = 0; u < KV; ++u) {
-      if (u >= su) break;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (key[u][e] >= prefix) stay |= 1u << (4 * u + e);
-        if (key[u][e] == prefix) same |= 1u << (4 * u + e);
-        if (key[u][e] != 0u) in |= 1u << (4 * u + e);
-      }
+    for (int e = 0; e < 4; ++e) {
+      if (key[e] > prefix) stay |= 1u << e;
+      if (key[e] == prefix) same |= 1u << e;
+      if (key[e] != 0u) in |= 1u << e;
     }
-    if (partial) {  // (uniform) equals past the need-th go
-      unsigned y = ties + warps_before<T>(__reduce_add_sync(0xffffffffu, __popc(same)), sums, &all);
-      ties += all;
+    if (__any_sync(0xffffffffu, same != 0u)) {  // equals up to the need-th
+      unsigned y = ties + lanes_before(same);
+      ties += __reduce_add_sync(0xffffffffu, __popc(same));
 #pragma unroll
-      for (int u = 0; u < KV; ++u) {
-        const unsigned bits = same >> (4 * u) & 15u;
-        if (u >= su) break;
-        if (!__any_sync(0xffffffffu, bits != 0u)) continue;
-        unsigned z = y + lanes_before(bits);
-        y += __reduce_add_sync(0xffffffffu, __popc(bits));
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (bits >> e & 1u)
-            if (z++ >= need) stay &= ~(1u << (4 * u + e));
-      }
+      for (int e = 0; e < 4; ++e)
+        if (same >> e & 1u)
+          if (y++ < need) stay |= 1u << e;
     }
-    unsigned hole = 0, goes = 0;
+    const unsigned below = (1u << max(0, min(4, end - i))) - 1u, hole = in & ~stay & below, goes = stay & ~below;
+    if (__any_sync(0xffffffffu, hole != 0u)) {
+      int *to = places + holes + lanes_before(hole);
+      holes += __reduce_add_sync(0xffffffffu, __popc(hole));
 #pragma unroll
-    for (int u = 0; u < KV; ++u) {
-      if (u >= su) break;
-      const int low = max(0, min(4, end - (4 * (first + 32 * u) - skew)));  // of the vector, below `end`
-      const unsigned below = ((1u << low) - 1u) << (4 * u), above = (15u << (4 * u)) & ~below;
-      hole |= in & ~stay & below;
-      goes |= stay & above;
+      for (int e = 0; e < 4; ++e)
+        if (hole >> e & 1u) *to++ = i + e;
     }
-    // places (low half) and tokens (high half), at most 4 T KV <= 2^13 of each in a step
-    const unsigned before =
-        warps_before<T>(__reduce_add_sync(0xffffffffu, __popc(hole) | __popc(goes) << 16), sums, &all);
-    int y = holes + static_cast<int>(before & 0xFFFFu), z = late + static_cast<int>(before >> 16);
+    if (__any_sync(0xffffffffu, goes != 0u)) {
+      int *to = tokens + late + lanes_before(goes);
+      late += __reduce_add_sync(0xffffffffu, __popc(goes));
 #pragma unroll
-    for (int u = 0; u < KV; ++u) {
-      if (u >= su) break;
-      const int i = 4 * (first + 32 * u) - skew;
-      const unsigned b = hole >> (4 * u) & 15u, c = goes >> (4 * u) & 15u;
-      if (__any_sync(0xffffffffu, b != 0u)) {
-        int *to = places + y + lanes_before(b);
-        y += __reduce_add_sync(0xffffffffu, __popc(b));
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (b >> e & 1u) *to++ = i + e;
-      }
-      if (__any_sync(0xffffffffu, c != 0u)) {
-        int *to = tokens + z + lanes_before(c);
-        z += __reduce_add_sync(0xffffffffu, __popc(c));
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (c >> e & 1u) *to++ = i + e;
-      }
+      for (int e = 0; e < 4; ++e)
+        if (goes >> e & 1u) *to++ = i + e;
     }
-    holes += static_cast<int>(all & 0xFFFFu);
-    late += static_cast<int>(all >> 16);
-  }
-  if (tid == 0 && rank == ctas - 1) *meta = {late, 1, keep, w};
+  });
+  if (tid == T - 1 && rank == ctas - 1) *meta = {late, 1, keep, w};
 }
 
 // ---------------------------------------------------------------------------
@@ -446,9 +420,9 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
   }
 }
 
-// The last w tokens of a (row, head), which may overlap their new places: one
-// CTA, in ascending order (a place is below its token), as many tokens at a time
-// as its registers hold.  Then weights past k.
+// The last w tokens of a (row, head), as many at a time as a CTA's registers hold.
+// Where they overlap their new places, one CTA takes them in ascending order (a
+// place is below its token); else its CTAs share them.  Weights past k become 0.
 constexpr int kShiftThreads = 256, kShiftPieces = 8;
 template <int LANES>
 __global__ void __launch_bounds__(kShiftThreads, 3) evict_shift_kernel(const EvictArgs a) {
@@ -460,9 +434,13 @@ __global__ void __launch_bounds__(kShiftThreads, 3) evict_shift_kernel(const Evi
   if (!meta.active) return;
   const int32_t *table = a.tables + static_cast<int64_t>(x / a.H) * a.max_blocks;
   const int n = __ldg(a.ctx + x / a.H), w = meta.recent, k = meta.keep, h = x % a.H;
+  const bool apart = n - k >= w;
+  const int ctas = apart ? gridDim.y : 1, y = blockIdx.y;
+  if (y >= ctas) return;
   float *weights = a.weights + static_cast<int64_t>(x) * a.stride;
 #pragma unroll 1
-  for (int base = 0; base < w; base += TOKENS) {
+  for (int64_t at = static_cast<int64_t>(y) * TOKENS; at < w; at += ctas * TOKENS) {
+    const int base = static_cast<int>(at);
     uint4 v[kShiftPieces];
     Rest rest[SCALARS];
 #pragma unroll
@@ -475,7 +453,7 @@ __global__ void __launch_bounds__(kShiftThreads, 3) evict_shift_kernel(const Evi
       const int i = base + u * kShiftThreads + tid;
       if (u * kShiftThreads + tid < TOKENS && i < w) rest[u] = load_rest(a, weights, slot_of(a, table, h, n - w + i), n - w + i);
     }
-    __syncthreads();
+    if (!apart) __syncthreads();
 #pragma unroll
     for (int u = 0; u < kShiftPieces; ++u) {
       const int i = base + (u * kShiftThreads + tid) / LANES;
@@ -484,11 +462,15 @@ __global__ void __launch_bounds__(kShiftThreads, 3) evict_shift_kernel(const Evi
 #pragma unroll
     for (int u = 0; u < SCALARS; ++u) {
       const int i = base + u * kShiftThreads + tid;
-      if (u * kShiftThreads + tid < TOKENS && i < w) store_rest(a, weights, slot_of(a, table, h, k - w + i), k - w + i, rest[u]);
+      if (u * kShiftThreads + tid < TOKENS && i < w) {
+        store_rest(a, weights, slot_of(a, table, h, k - w + i), k - w + i, rest[u]);
+        if (apart) weights[n - w + i] = 0.f;  // (its reader clears it)
+      }
     }
-    __syncthreads();
+    if (!apart) __syncthreads();
   }
-  for (int i = k + tid; i < n; i += kShiftThreads) weights[i] = 0.f;
+  const int end = apart ? n - w : n;
+  for (int64_t i = k + static_cast<int64_t>(y) * kShiftThreads + tid; i < end; i += ctas * kShiftThreads) weights[i] = 0.f;
 }
 
 template <int LANES>
@@ -498,34 +480,51 @@ cudaError_t move(const EvictArgs &a, int sms, cudaStream_t stream) {
   cudaError_t e = launch_overlapped(evict_move_kernel<LANES>, static_cast<int>(ctas < 1 ? 1 : ctas < 8 * sms ? ctas : 8 * sms),
                                     256, 0, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(evict_shift_kernel<LANES>, static_cast<int>(heads), kShiftThreads, 0, stream, a);
+  // CTAs for a (row, head): enough for all SMs, where its tokens can be shared
+  const int share = static_cast<int>(4 * sms / heads);
+  return launch_overlapped(evict_shift_kernel<LANES>, dim3(static_cast<unsigned>(heads), share < 1 ? 1 : share > 16 ? 16 : share),
+                           kShiftThreads, 0, stream, a);
 }
 
-cudaError_t select(const EvictArgs &a, int sms, cudaStream_t stream) {
-  const int heads = a.rows * a.H;
-  // (4 KV T positions from any of four alignments)
-  if (a.stride <= 8192 - 4) {
-    evict_select_kernel<256, 8, true, false><<<heads, 256, 0, stream>>>(a, 1);
-    return cudaGetLastError();
-  }
-  // few rows: a cluster for each, as long as two CTAs an SM hold them all
-  int ctas = 1;
-  while (ctas < 8 && 2 * ctas * heads <= 2 * sms) ctas *= 2;
-  if (ctas == 1) {
-    evict_select_kernel<256, 8, false, false><<<heads, 256, 0, stream>>>(a, 1);
-    return cudaGetLastError();
+template <int T, bool HELD, bool CLUSTER>
+cudaError_t select_with(const EvictArgs &a, int ctas, size_t bytes, cudaStream_t stream) {
+  auto kern = evict_select_kernel<T, HELD, CLUSTER>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  static std::atomic<unsigned long long> done{0};  // devices whose limit is raised
+  if (HELD && !((done.load(std::memory_order_acquire) >> dev) & 1ull)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * (kHeld / 4 + 2))) != cudaSuccess)
+      return e;
+    done.fetch_or(1ull << dev, std::memory_order_acq_rel);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(heads * ctas);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(a.rows * a.H * ctas);
+  cfg.blockDim = dim3(T);
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = ctas;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<256, 8, false, true>, a, ctas);
+  cfg.numAttrs = CLUSTER ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, a, ctas);
+}
+
+cudaError_t select(const EvictArgs &a, int sms, cudaStream_t stream) {
+  const int64_t heads = static_cast<int64_t>(a.rows) * a.H;
+  // CTAs that hold all keys, and more where few rows leave SMs without work
+  int ctas = 1;
+  while (ctas < 8 && (a.stride > static_cast<int64_t>(ctas) * kHeld || (2 * ctas * heads <= 2 * sms && a.stride > 2048 * ctas)))
+    ctas *= 2;
+  const int64_t keys = (a.stride + ctas - 1) / ctas;
+  if (keys > kHeld) return select_with<512, false, true>(a, ctas, 0, stream);
+  const size_t bytes = 16 * (static_cast<size_t>(a.stride / 4 + 2 + ctas - 1) / ctas);  // vectors of any alignment
+  if (keys <= 8192)
+    return ctas == 1 ? select_with<256, true, false>(a, 1, bytes, stream) : select_with<256, true, true>(a, ctas, bytes, stream);
+  return ctas == 1 ? select_with<512, true, false>(a, 1, bytes, stream) : select_with<512, true, true>(a, ctas, bytes, stream);
 }
 
 }  // namespace

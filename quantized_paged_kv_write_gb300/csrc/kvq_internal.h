@@ -76,10 +76,10 @@ struct DecodeArgs {
 // Launches kern so that it may start while the stream's kernel before it still
 // runs (that one says when, and kern waits for its results itself).
 template <typename... Params, typename... Args>
-cudaError_t launch_overlapped(void (*kern)(Params...), int ctas, int threads, size_t smem, cudaStream_t stream,
+cudaError_t launch_overlapped(void (*kern)(Params...), dim3 ctas, int threads, size_t smem, cudaStream_t stream,
                               const Args &...args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = ctas;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
