@@ -85,7 +85,6 @@ __global__ void __launch_bounds__(T, 1536 / T) evict_select_kernel(const EvictAr
   __shared__ unsigned sums[W];
   __shared__ __align__(16) Counts counts[W + 1];  // the warps', and the CTA's
   __shared__ unsigned chosen, left;
-  grid_release();
   const int x = CLUSTER ? blockIdx.x / ctas : blockIdx.x, rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
   const int r = x / a.H, h = x - r * a.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool reports = tid == 0 && rank == 0;
@@ -389,7 +388,6 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
   // the warps that share a (row, head), 32 tokens each in turn
   const int warps = gridDim.x * 8, per = max(1, warps / heads);
   grid_wait();  // the lists
-  grid_release();
   for (int it = blockIdx.x * 8 + (threadIdx.x >> 5); it < heads * per; it += warps) {
     const int x = it % heads, moves = a.ws_meta[x].moves;
     const int32_t *table = a.tables + static_cast<int64_t>(x / a.H) * a.max_blocks;
