@@ -20,10 +20,11 @@ namespace kvq {
 namespace {
 
 // Weights as unsigned numbers in the same order; -0 counts as 0, NaN as the
-// largest.  None is 0, which stands for a position that is no candidate.
+// largest (adding 0 leaves one NaN, 0x7FFFFFFF).  None is 0, which stands for a
+// position that is no candidate.
 __device__ __forceinline__ unsigned order_of(float x) {
   const unsigned b = __float_as_uint(x + 0.f);
-  return x != x ? 0xFFFFFFFFu : b ^ (static_cast<unsigned>(static_cast<int>(b) >> 31) | 0x80000000u);
+  return b ^ (static_cast<unsigned>(static_cast<int>(b) >> 31) | 0x80000000u);
 }
 
 // ---------------------------------------------------------------------------
@@ -58,6 +59,19 @@ __device__ __forceinline__ uint4 remote128(uint32_t at, unsigned rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(rank));
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(to));
   return v;
+}
+
+// hist[k >> shift & digit] += 1 if (k & mask) == want, without a branch; `base` is
+// the address of hist.
+__device__ __forceinline__ void count_if(uint32_t base, unsigned k, unsigned mask, unsigned want, int shift, unsigned digit) {
+  const uint32_t at = ((shift >= 2 ? k >> (shift - 2) : k << 2) & (digit << 2)) + base;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, %2;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(at), "r"(k & mask),
+               "r"(want)
+               : "memory");
+}
+__device__ __forceinline__ void count_valid(uint32_t base, unsigned k) {
+  const uint32_t at = (k >> 19 & 0x1FFCu) + base;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(at), "r"(k) : "memory");
 }
 
 // A lane has bits of four consecutive positions, the warp of 128: the number set
@@ -191,24 +205,22 @@ __global__ void __launch_bounds__(T, 1536 / T) evict_select_kernel(const EvictAr
 #pragma unroll 1
     for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
       const unsigned digit = shift == 0 ? 1023u : 2047u;
-      auto count = [&](unsigned k) {
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
-      };
+      const uint32_t bins = smem_u32(hist);
       if (shift == 21) {
         each(of_weights, [&](int v, const uint4 &k) {
           if constexpr (HELD)
             if (v < w1) held[v - v0] = k;
-          if (k.x != 0u) atomicAdd(&hist[k.x >> 21], 1u);
-          if (k.y != 0u) atomicAdd(&hist[k.y >> 21], 1u);
-          if (k.z != 0u) atomicAdd(&hist[k.z >> 21], 1u);
-          if (k.w != 0u) atomicAdd(&hist[k.w >> 21], 1u);
+          count_valid(bins, k.x);
+          count_valid(bins, k.y);
+          count_valid(bins, k.z);
+          count_valid(bins, k.w);
         });
       } else {
         walk([&](int, const uint4 &k) {
-          count(k.x);
-          count(k.y);
-          count(k.z);
-          count(k.w);
+          count_if(bins, k.x, mask, prefix, shift, digit);
+          count_if(bins, k.y, mask, prefix, shift, digit);
+          count_if(bins, k.z, mask, prefix, shift, digit);
+          count_if(bins, k.w, mask, prefix, shift, digit);
         });
       }
       sync_all<CLUSTER>();
@@ -265,11 +277,23 @@ __global__ void __launch_bounds__(T, 1536 / T) evict_select_kernel(const EvictAr
   Counts own = {0u, 0u, 0u, 0u};
   walk([&](int v, const uint4 &k) {
     const int low = end - (4 * v - skew);  // of the vector, below `end`
-    const unsigned key[4] = {k.x, k.y, k.z, k.w};
+    if (low >= 4 || low <= 0) {
+      const unsigned g = (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix),
+                     q = (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
+      if (low > 0) {
+        own.larger_low += g;
+        own.equal_low += q;
+      } else {
+        own.larger += g;
+        own.equal += q;
+      }
+    } else {
+      const unsigned key[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (key[e] > prefix) (e < low ? own.larger_low : own.larger) += 1u;
-      if (key[e] == prefix) (e < low ? own.equal_low : own.equal) += 1u;
+      for (int e = 0; e < 4; ++e) {
+        if (key[e] > prefix) (e < low ? own.larger_low : own.larger) += 1u;
+        if (key[e] == prefix) (e < low ? own.equal_low : own.equal) += 1u;
+      }
     }
   });
   own.larger_low = __reduce_add_sync(0xffffffffu, own.larger_low);
