@@ -12,6 +12,7 @@
 // §5 Where the scales live: a scale for each token and head), so a head's token
 // keeps its values.  The pages have no eviction: it is this library's.
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kvq_internal.h"
@@ -61,17 +62,18 @@ __device__ __forceinline__ uint4 remote128(uint32_t at, unsigned rank) {
   return v;
 }
 
-// hist[k >> shift & digit] += 1 if (k & mask) == want, without a branch; `base` is
-// the address of hist.
-__device__ __forceinline__ void count_if(uint32_t base, unsigned k, unsigned mask, unsigned want, int shift, unsigned digit) {
-  const uint32_t at = ((shift >= 2 ? k >> (shift - 2) : k << 2) & (digit << 2)) + base;
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, %2;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(at), "r"(k & mask),
-               "r"(want)
-               : "memory");
-}
-__device__ __forceinline__ void count_valid(uint32_t base, unsigned k) {
-  const uint32_t at = (k >> 19 & 0x1FFCu) + base;
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(at), "r"(k) : "memory");
+// hist[k >> SHIFT & (2^BITS - 1)] += 1 if (k & mask) == want (SHIFT 21: if k is not
+// 0), without a branch; `base` is the address of hist.
+template <int SHIFT, int BITS>
+__device__ __forceinline__ void count_key(uint32_t base, unsigned k, unsigned mask, unsigned want) {
+  constexpr unsigned DIGIT = ((1u << BITS) - 1u) << 2;
+  const uint32_t at = ((SHIFT >= 2 ? k >> (SHIFT - 2) : k << (2 - SHIFT)) & DIGIT) + base;
+  if constexpr (SHIFT == 21)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(at), "r"(k) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, %2;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(at), "r"(k & mask),
+                 "r"(want)
+                 : "memory");
 }
 
 // A lane has bits of four consecutive positions, the warp of 128: the number set
@@ -202,26 +204,23 @@ __global__ void __launch_bounds__(T, 1536 / T) evict_select_kernel(const EvictAr
   unsigned prefix = 0, need = end - p;
   {
     unsigned mask = 0;
-#pragma unroll 1
-    for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
-      const unsigned digit = shift == 0 ? 1023u : 2047u;
-      const uint32_t bins = smem_u32(hist);
-      if (shift == 21) {
+    const uint32_t bins = smem_u32(hist);
+    auto digit = [&](auto shift_tag, auto bits_tag) {
+      constexpr int SHIFT = decltype(shift_tag)::value, BITS = decltype(bits_tag)::value;
+      auto count = [&](const uint4 &k) {
+        count_key<SHIFT, BITS>(bins, k.x, mask, prefix);
+        count_key<SHIFT, BITS>(bins, k.y, mask, prefix);
+        count_key<SHIFT, BITS>(bins, k.z, mask, prefix);
+        count_key<SHIFT, BITS>(bins, k.w, mask, prefix);
+      };
+      if constexpr (SHIFT == 21) {
         each(of_weights, [&](int v, const uint4 &k) {
           if constexpr (HELD)
             if (v < w1) held[v - v0] = k;
-          count_valid(bins, k.x);
-          count_valid(bins, k.y);
-          count_valid(bins, k.z);
-          count_valid(bins, k.w);
+          count(k);
         });
       } else {
-        walk([&](int, const uint4 &k) {
-          count_if(bins, k.x, mask, prefix, shift, digit);
-          count_if(bins, k.y, mask, prefix, shift, digit);
-          count_if(bins, k.z, mask, prefix, shift, digit);
-          count_if(bins, k.w, mask, prefix, shift, digit);
-        });
+        walk([&](int, const uint4 &k) { count(k); });
       }
       sync_all<CLUSTER>();
       // digits from the largest: the one in which the need-th lies
@@ -264,14 +263,17 @@ __global__ void __launch_bounds__(T, 1536 / T) evict_select_kernel(const EvictAr
         }
       }
       sync_all<CLUSTER>();  // (and all CTAs have read the histograms)
-      prefix |= chosen << shift;
-      mask |= digit << shift;
+      prefix |= chosen << SHIFT;
+      mask |= ((1u << BITS) - 1u) << SHIFT;
       need = left;
-      if (shift > 0) {
+      if constexpr (SHIFT > 0) {
         for (int i = tid; i < kBins; i += T) hist[i] = 0;
         __syncthreads();
       }
-    }
+    };
+    digit(std::integral_constant<int, 21>{}, std::integral_constant<int, 11>{});
+    digit(std::integral_constant<int, 10>{}, std::integral_constant<int, 11>{});
+    digit(std::integral_constant<int, 0>{}, std::integral_constant<int, 10>{});
   }
   // ---- what the warps before this one have
   Counts own = {0u, 0u, 0u, 0u};
