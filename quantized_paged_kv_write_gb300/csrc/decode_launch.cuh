@@ -16,7 +16,7 @@ namespace detail {
 constexpr size_t kSmemPerCtaTarget = 112 * 1024;
 constexpr int kMaxStages = 6;
 
-template <int D, int KF, int VF, bool WIDE, int HT, bool ROT>
+template <int D, int KF, int VF, bool WIDE, int HT, bool ROT, bool SCORES>
 cudaError_t plan_one(int H, int B, DecodePlan *plan) {
   constexpr bool rot = ROT;
   using T = DecodeTraits<D, KF, VF>;
@@ -27,7 +27,7 @@ cudaError_t plan_one(int H, int B, DecodePlan *plan) {
   if (ns > kMaxStages) ns = kMaxStages;
   if (ns < 2) ns = 2;
   size_t smem = fixed + ns * sb;
-  auto kern = decode_split_kernel<D, KF, VF, WIDE, HT, ROT>;
+  auto kern = decode_split_kernel<D, KF, VF, WIDE, HT, ROT, SCORES>;
   int dev = 0, sms = 0, occ = 0, optin = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -58,10 +58,10 @@ cudaError_t plan_one(int H, int B, DecodePlan *plan) {
   return cudaSuccess;
 }
 
-template <int D, int KF, int VF, bool WIDE, int HT, bool ROT>
+template <int D, int KF, int VF, bool WIDE, int HT, bool ROT, bool SCORES>
 cudaError_t launch_one(const DecodeArgs &a, const DecodePlan &plan, const DecodeMaps &m, cudaStream_t stream) {
   if (a.nctas > 0) {
-    auto kern = decode_split_kernel<D, KF, VF, WIDE, HT, ROT>;
+    auto kern = decode_split_kernel<D, KF, VF, WIDE, HT, ROT, SCORES>;
     cudaError_t e;
     if (a.overlap != 0) {
       e = launch_overlapped(kern, a.nctas, plan.threads, plan.smem, stream, m.k, m.v, m.vs, a, plan.nstages);
@@ -77,76 +77,76 @@ cudaError_t launch_one(const DecodeArgs &a, const DecodePlan &plan, const Decode
   return cudaGetLastError();
 }
 
-template <int D, int KF, bool WIDE, int HT, bool ROT>
+template <int D, int KF, bool WIDE, int HT, bool ROT, bool SCORES>
 cudaError_t plan_vf_h(int vf, int H, int B, DecodePlan *plan) {
-  if (vf == V_INT8_TOK) return plan_one<D, KF, V_INT8_TOK, WIDE, HT, ROT>(H, B, plan);
-  if (vf == V_FP8_TOK) return plan_one<D, KF, V_FP8_TOK, WIDE, HT, ROT>(H, B, plan);
-  if (vf == V_INT4_G32) return plan_one<D, KF, V_INT4_G32, WIDE, HT, ROT>(H, B, plan);
+  if (vf == V_INT8_TOK) return plan_one<D, KF, V_INT8_TOK, WIDE, HT, ROT, SCORES>(H, B, plan);
+  if (vf == V_FP8_TOK) return plan_one<D, KF, V_FP8_TOK, WIDE, HT, ROT, SCORES>(H, B, plan);
+  if (vf == V_INT4_G32) return plan_one<D, KF, V_INT4_G32, WIDE, HT, ROT, SCORES>(H, B, plan);
   if constexpr (D == 128) {
-    if (vf == V_INT2_G32) return plan_one<D, KF, V_INT2_G32, WIDE, HT, ROT>(H, B, plan);
+    if (vf == V_INT2_G32) return plan_one<D, KF, V_INT2_G32, WIDE, HT, ROT, SCORES>(H, B, plan);
   }
   return cudaErrorInvalidValue;
 }
 
 // eight kv heads (Llama-3 8B / 70B layers) get a compile-time head count;
 // a rotated cache (per-token K only) runs with a runtime head count
-template <int D, int KF, bool WIDE>
+template <int D, int KF, bool WIDE, bool SCORES>
 cudaError_t plan_vf(int vf, int H, int B, bool rot, DecodePlan *plan) {
   if constexpr (KF != K_INT8_CHAN && KF != K_INT2_CHAN) {
-    if (rot) return plan_vf_h<D, KF, WIDE, 0, true>(vf, H, B, plan);
+    if (rot) return plan_vf_h<D, KF, WIDE, 0, true, SCORES>(vf, H, B, plan);
   }
-  return H == 8 ? plan_vf_h<D, KF, WIDE, 8, false>(vf, H, B, plan) : plan_vf_h<D, KF, WIDE, 0, false>(vf, H, B, plan);
+  return H == 8 ? plan_vf_h<D, KF, WIDE, 8, false, SCORES>(vf, H, B, plan) : plan_vf_h<D, KF, WIDE, 0, false, SCORES>(vf, H, B, plan);
 }
 
-template <int D, int KF, bool WIDE, int HT, bool ROT>
+template <int D, int KF, bool WIDE, int HT, bool ROT, bool SCORES>
 cudaError_t launch_vf_h(int vf, const DecodeArgs &a, const DecodePlan &plan, const DecodeMaps &m,
                         cudaStream_t stream) {
-  if (vf == V_INT8_TOK) return launch_one<D, KF, V_INT8_TOK, WIDE, HT, ROT>(a, plan, m, stream);
-  if (vf == V_FP8_TOK) return launch_one<D, KF, V_FP8_TOK, WIDE, HT, ROT>(a, plan, m, stream);
-  if (vf == V_INT4_G32) return launch_one<D, KF, V_INT4_G32, WIDE, HT, ROT>(a, plan, m, stream);
+  if (vf == V_INT8_TOK) return launch_one<D, KF, V_INT8_TOK, WIDE, HT, ROT, SCORES>(a, plan, m, stream);
+  if (vf == V_FP8_TOK) return launch_one<D, KF, V_FP8_TOK, WIDE, HT, ROT, SCORES>(a, plan, m, stream);
+  if (vf == V_INT4_G32) return launch_one<D, KF, V_INT4_G32, WIDE, HT, ROT, SCORES>(a, plan, m, stream);
   if constexpr (D == 128) {
-    if (vf == V_INT2_G32) return launch_one<D, KF, V_INT2_G32, WIDE, HT, ROT>(a, plan, m, stream);
+    if (vf == V_INT2_G32) return launch_one<D, KF, V_INT2_G32, WIDE, HT, ROT, SCORES>(a, plan, m, stream);
   }
   return cudaErrorInvalidValue;
 }
 
-template <int D, int KF, bool WIDE>
+template <int D, int KF, bool WIDE, bool SCORES>
 cudaError_t launch_vf(int vf, const DecodeArgs &a, const DecodePlan &plan, const DecodeMaps &m,
                       cudaStream_t stream) {
   if constexpr (KF != K_INT8_CHAN && KF != K_INT2_CHAN) {
-    if (a.rot) return launch_vf_h<D, KF, WIDE, 0, true>(vf, a, plan, m, stream);
+    if (a.rot) return launch_vf_h<D, KF, WIDE, 0, true, SCORES>(vf, a, plan, m, stream);
   }
-  return a.H == 8 ? launch_vf_h<D, KF, WIDE, 8, false>(vf, a, plan, m, stream)
-                  : launch_vf_h<D, KF, WIDE, 0, false>(vf, a, plan, m, stream);
+  return a.H == 8 ? launch_vf_h<D, KF, WIDE, 8, false, SCORES>(vf, a, plan, m, stream)
+                  : launch_vf_h<D, KF, WIDE, 0, false, SCORES>(vf, a, plan, m, stream);
 }
 
 }  // namespace detail
 
-template <int KF>
+template <int KF, bool SCORES>
 cudaError_t plan_decode_kf(int head_dim, int vf, int H, int G, int B, bool rot, DecodePlan *plan) {
   const bool wide = G > 4;
   if (head_dim == 128)
-    return wide ? detail::plan_vf<128, KF, true>(vf, H, B, rot, plan)
-                : detail::plan_vf<128, KF, false>(vf, H, B, rot, plan);
+    return wide ? detail::plan_vf<128, KF, true, SCORES>(vf, H, B, rot, plan)
+                : detail::plan_vf<128, KF, false, SCORES>(vf, H, B, rot, plan);
   if constexpr (KF != K_INT2_CHAN) {  // INT2 rows: head_dim 128
     if (head_dim == 64)
-      return wide ? detail::plan_vf<64, KF, true>(vf, H, B, rot, plan)
-                  : detail::plan_vf<64, KF, false>(vf, H, B, rot, plan);
+      return wide ? detail::plan_vf<64, KF, true, SCORES>(vf, H, B, rot, plan)
+                  : detail::plan_vf<64, KF, false, SCORES>(vf, H, B, rot, plan);
   }
   return cudaErrorInvalidValue;
 }
 
-template <int KF>
+template <int KF, bool SCORES>
 cudaError_t launch_decode_kf(int head_dim, int vf, const DecodeArgs &a, const DecodePlan &plan,
                              const DecodeMaps &m, cudaStream_t stream) {
   const bool wide = a.G > 4;
   if (head_dim == 128)
-    return wide ? detail::launch_vf<128, KF, true>(vf, a, plan, m, stream)
-                : detail::launch_vf<128, KF, false>(vf, a, plan, m, stream);
+    return wide ? detail::launch_vf<128, KF, true, SCORES>(vf, a, plan, m, stream)
+                : detail::launch_vf<128, KF, false, SCORES>(vf, a, plan, m, stream);
   if constexpr (KF != K_INT2_CHAN) {
     if (head_dim == 64)
-      return wide ? detail::launch_vf<64, KF, true>(vf, a, plan, m, stream)
-                  : detail::launch_vf<64, KF, false>(vf, a, plan, m, stream);
+      return wide ? detail::launch_vf<64, KF, true, SCORES>(vf, a, plan, m, stream)
+                  : detail::launch_vf<64, KF, false, SCORES>(vf, a, plan, m, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -70,7 +70,13 @@ int decode_format(const kvq_format *f, int *kf, int *vf) {
   return KVQ_OK;
 }
 
-cudaError_t plan_decode_uncached(int D, int kf, int vf, int H, int G, int B, bool rot, DecodePlan *plan) {
+cudaError_t plan_decode_uncached(int D, int kf, int vf, int H, int G, int B, bool rot, bool scores, DecodePlan *plan) {
+  if (scores) {
+    if (kf == K_INT8_TOK) return plan_decode_kf<K_INT8_TOK, true>(D, vf, H, G, B, rot, plan);
+    if (kf == K_FP8_TOK) return plan_decode_kf<K_FP8_TOK, true>(D, vf, H, G, B, rot, plan);
+    if (kf == K_INT4_TOK) return plan_decode_kf<K_INT4_TOK, true>(D, vf, H, G, B, rot, plan);
+    return cudaErrorInvalidValue;
+  }
   if (kf == K_INT8_TOK) return plan_decode_kf<K_INT8_TOK>(D, vf, H, G, B, rot, plan);
   if (kf == K_FP8_TOK) return plan_decode_kf<K_FP8_TOK>(D, vf, H, G, B, rot, plan);
   if (kf == K_INT8_CHAN) return plan_decode_kf<K_INT8_CHAN>(D, vf, H, G, B, rot, plan);
@@ -83,15 +89,17 @@ cudaError_t plan_decode_uncached(int D, int kf, int vf, int H, int G, int B, boo
 // kernel attributes, the SM count and the occupancy query stay off the
 // per-call path.  The map is bounded (cleared when full).
 struct PlanKey {
-  int dev, D, kf, vf, H, G, B, rot;
+  int dev, D, kf, vf, H, G, B, rot, scores;
   bool operator==(const PlanKey &o) const {
-    return dev == o.dev && D == o.D && kf == o.kf && vf == o.vf && H == o.H && G == o.G && B == o.B && rot == o.rot;
+    return dev == o.dev && D == o.D && kf == o.kf && vf == o.vf && H == o.H && G == o.G && B == o.B && rot == o.rot &&
+           scores == o.scores;
   }
 };
 struct PlanKeyHash {
   size_t operator()(const PlanKey &k) const {
     size_t h = 1469598103934665603ull;
-    for (int x : {k.dev, k.D, k.kf, k.vf, k.H, k.G, k.B, k.rot}) h = (h ^ static_cast<uint32_t>(x)) * 1099511628211ull;
+    for (int x : {k.dev, k.D, k.kf, k.vf, k.H, k.G, k.B, k.rot, k.scores})
+      h = (h ^ static_cast<uint32_t>(x)) * 1099511628211ull;
     return h;
   }
 };
@@ -99,11 +107,11 @@ constexpr size_t kMaxPlans = 1024;
 std::unordered_map<PlanKey, DecodePlan, PlanKeyHash> g_plans;
 std::mutex g_plan_mu;
 
-cudaError_t plan_decode(int D, int kf, int vf, int H, int G, int B, bool rot, DecodePlan *plan) {
+cudaError_t plan_decode(int D, int kf, int vf, int H, int G, int B, bool rot, DecodePlan *plan, bool scores = false) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const PlanKey key{dev, D, kf, vf, H, G, B, rot ? 1 : 0};
+  const PlanKey key{dev, D, kf, vf, H, G, B, rot ? 1 : 0, scores ? 1 : 0};
   {
     std::lock_guard<std::mutex> lk(g_plan_mu);
     auto it = g_plans.find(key);
@@ -113,7 +121,7 @@ cudaError_t plan_decode(int D, int kf, int vf, int H, int G, int B, bool rot, De
     }
   }
   DecodePlan p;
-  if ((e = plan_decode_uncached(D, kf, vf, H, G, B, rot, &p)) != cudaSuccess) return e;
+  if ((e = plan_decode_uncached(D, kf, vf, H, G, B, rot, scores, &p)) != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(g_plan_mu);
   if (g_plans.size() >= kMaxPlans) g_plans.clear();
   g_plans.emplace(key, p);
@@ -123,6 +131,12 @@ cudaError_t plan_decode(int D, int kf, int vf, int H, int G, int B, bool rot, De
 
 cudaError_t launch_decode(int D, int kf, int vf, const DecodeArgs &a, const DecodePlan &plan,
                           const DecodeMaps &m, cudaStream_t s) {
+  if (a.ws_z != nullptr) {
+    if (kf == K_INT8_TOK) return launch_decode_kf<K_INT8_TOK, true>(D, vf, a, plan, m, s);
+    if (kf == K_FP8_TOK) return launch_decode_kf<K_FP8_TOK, true>(D, vf, a, plan, m, s);
+    if (kf == K_INT4_TOK) return launch_decode_kf<K_INT4_TOK, true>(D, vf, a, plan, m, s);
+    return cudaErrorInvalidValue;
+  }
   if (kf == K_INT8_TOK) return launch_decode_kf<K_INT8_TOK>(D, vf, a, plan, m, s);
   if (kf == K_FP8_TOK) return launch_decode_kf<K_FP8_TOK>(D, vf, a, plan, m, s);
   if (kf == K_INT8_CHAN) return launch_decode_kf<K_INT8_CHAN>(D, vf, a, plan, m, s);
@@ -426,6 +440,13 @@ static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
   const int H = fmt->num_kv_heads, D = fmt->head_dim, G = num_q_heads / H;
   DecodePlan plan;
   if (plan_decode(D, kf, vf, H, G, batch, fmt->rotation != 0, &plan) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (weights != nullptr) {
+    // the same split as the plain decode's, on kernels of their own
+    DecodePlan own;
+    if (plan_decode(D, kf, vf, H, G, batch, fmt->rotation != 0, &own, true) != cudaSuccess) return KVQ_ERR_CUDA;
+    own.max_ctas = plan.max_ctas;
+    plan = own;
+  }
   const WsLayout wl = ws_layout(batch, H, D, plan.max_ctas);
   const WeighWs ww = weigh_ws(wl, batch, num_q_heads, max_context_len);
   if (workspace_bytes < (weights != nullptr ? ww.total : wl.total)) return KVQ_ERR_WORKSPACE;
@@ -494,6 +515,7 @@ static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
   w.weights = weights;
   w.stride = weights_stride;
   w.num_blocks = fmt->num_blocks;
+  w.most_blocks = blocks_ub;
   w.B = batch;
   w.H = H;
   w.G = G;

@@ -172,6 +172,7 @@ struct WeighArgs {
   const int32_t *tables, *ctx; // [B, max_blocks], [B]
   float *weights;              // [B, H, stride]
   int64_t stride, num_blocks;
+  int64_t most_blocks;         // that the contexts can have
   int B, H, G, max_blocks;
 };
 cudaError_t launch_weigh(const WeighArgs &a, int sms, cudaStream_t stream);
@@ -279,10 +280,11 @@ cudaError_t launch_prefix_attend(int head_dim, int kf, int vf, const PrefixArgs 
                                  cudaStream_t stream);
 cudaError_t launch_prefix_merge(int head_dim, const PrefixArgs &a, cudaStream_t stream);
 
-// Per-format entry points defined in the decode_k*.cu translation units.
-template <int KF>
+// Per-format entry points defined in the decode_k*.cu translation units, and in
+// decode_s*.cu for a decode that leaves its scores (per-token K).
+template <int KF, bool SCORES = false>
 cudaError_t plan_decode_kf(int head_dim, int vf, int H, int G, int B, bool rot, DecodePlan *plan);
-template <int KF>
+template <int KF, bool SCORES = false>
 cudaError_t launch_decode_kf(int head_dim, int vf, const DecodeArgs &a, const DecodePlan &plan,
                              const DecodeMaps &maps, cudaStream_t stream);
 
