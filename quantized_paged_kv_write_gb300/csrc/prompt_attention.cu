@@ -20,6 +20,7 @@
 #include <limits.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kvq_internal.h"
@@ -128,11 +129,11 @@ __device__ __forceinline__ Unit unit_at(const PromptArgs &a, int x) {
 // attention
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;                     // keys of a tile, rows of a row tile
-constexpr int kLoadWarp = 0, kMmaWarp = 1, kPlanWarp = 2, kSoftmaxWarp = 4;
+constexpr int kLoadWarp = 0, kMmaWarp = 1, kPlanWarp = 3, kSoftmaxWarp = 4;  // (two warps for the products)
 constexpr int kThreads = 12 * 32;
 // Registers a thread: 168 at launch; the four single-warp roles give theirs to
-// the softmax (128 * 72 + 256 * 216 = 384 * 168).
-constexpr int kFewRegs = 72, kManyRegs = 216;
+// the softmax (128 * 88 + 256 * 208 = 384 * 168).
+constexpr int kFewRegs = 88, kManyRegs = 208;
 constexpr float kRaise = 6.f;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -141,8 +142,9 @@ struct Smem {
   static constexpr uint32_t HALF = 128 * 128;           // 64 channels of 128 rows
   static constexpr uint32_t TILE = HALF * (D / 64);
   static constexpr int STAGES = D == 128 ? 2 : 4;       // places for tiles of K, and of V
-  static constexpr uint32_t q = 0;                      // [2] row tiles
-  static constexpr uint32_t k = q + 2 * TILE;
+  static constexpr int QS = 3;                          // and for row tiles: this unit's and one of the next
+  static constexpr uint32_t q = 0;
+  static constexpr uint32_t k = q + QS * TILE;
   static constexpr uint32_t v = k + STAGES * TILE;
   static constexpr uint32_t bars = v + STAGES * TILE;
   static constexpr uint32_t tmem = bars + 64 * 8;       // tensor memory address, then the abort flag
@@ -151,9 +153,16 @@ struct Smem {
   static_assert(bytes <= 227 * 1024, "shared memory");
 };
 
+// Tensor memory: two S, two O; P over S where they fill it, else beside them.
+template <int D>
+struct Tmem {
+  static constexpr bool BESIDE = D == 64;
+  static constexpr uint32_t s = 0, p = BESIDE ? 256 : 0, p_step = BESIDE ? 64 : 128, o = BESIDE ? 384 : 256;
+};
+
 enum Bar : int {
-  B_Q = 0, B_QFREE = 1, B_S = 2, B_P = 4, B_O = 6, B_OFREE = 8, B_UNIT = 10, B_UNITFREE = 12, B_KFULL = 14,
-  B_KFREE = 18, B_VFULL = 22, B_VFREE = 26, B_END = 30, B_COUNT = 31
+  B_Q = 0, B_QFREE = 3, B_S = 6, B_TAKEN = 8, B_P = 10, B_PFREE = 12, B_O = 14, B_OFREE = 16, B_UNIT = 18, B_UNITFREE = 20,
+  B_KFULL = 22, B_KFREE = 26, B_VFULL = 30, B_VFREE = 34, B_END = 38, B_COUNT = 40
 };
 
 // What the roles need to know of a unit: tokens t0 .. and the tiles of keys of
@@ -223,25 +232,14 @@ __device__ __forceinline__ void load_role(const PromptArgs &a, const CUtensorMap
   const int step = a.unit / 2;
   const uint32_t qbytes = step * a.G * D * 2;
   Units units(wait, base + L::units);
-  int st = 0;
-  uint32_t ph = 1;  // of the places for K and V
+  int st = 0, qs = 0;             // places for K and V, and for row tiles
+  uint32_t ph = 1, qp = 1;        // and their parities
   for (;;) {
     const uint4 u = units.next();
     if (static_cast<int>(u.x) < 0) break;
     const Work w(u, step);
-    wait(B_QFREE, (units.n & 1) ^ 1);
     units.done(lane);
     const bool go = lane == 0 && !*wait.abort;  // (after a wait that ran out nobody reads: no further copies)
-    if (go) {
-      uint64_t *bar = &wait.bars[B_Q];
-      const bool two = w.tiles[1] > 0;
-      mbar_arrive_expect_tx(bar, two ? 2 * qbytes : qbytes);
-#pragma unroll
-      for (int c = 0; c < D; c += 64) {
-        tma_load(base + L::q + c / 64 * L::HALF, qm, c, w.h * a.G, w.start + w.t0, bar);
-        if (two) tma_load(base + L::q + L::TILE + c / 64 * L::HALF, qm, c, w.h * a.G, w.start + w.t0 + step, bar);
-      }
-    }
     for (int j = 0; j < w.all; ++j) {
       wait(B_KFREE + st, ph);
       if (go) {
@@ -249,6 +247,24 @@ __device__ __forceinline__ void load_role(const PromptArgs &a, const CUtensorMap
 #pragma unroll
         for (int c = 0; c < D; c += 64)
           tma_load(base + L::k + st * L::TILE + c / 64 * L::HALF, km, c, w.h, w.start + j * kTile, &wait.bars[B_KFULL + st]);
+      }
+      if (j == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (w.tiles[i] == 0) continue;
+          wait(B_QFREE + qs, qp);
+          if (go) {
+            mbar_arrive_expect_tx(&wait.bars[B_Q + qs], qbytes);
+#pragma unroll
+            for (int c = 0; c < D; c += 64)
+              tma_load(base + L::q + qs * L::TILE + c / 64 * L::HALF, qm, c, w.h * a.G, w.start + w.t0 + i * step,
+                       &wait.bars[B_Q + qs]);
+          }
+          if (++qs == L::QS) {
+            qs = 0;
+            qp ^= 1;
+          }
+        }
       }
       wait(B_VFREE + st, ph);
       if (go) {
@@ -278,101 +294,139 @@ __device__ __forceinline__ void load_role(const PromptArgs &a, const CUtensorMap
       ph ^= 1;
     }
   }
+  for (int i = 0; i < L::QS; ++i) {
+    wait(B_QFREE + qs, qp);
+    if (++qs == L::QS) {
+      qs = 0;
+      qp ^= 1;
+    }
+  }
 }
 
-// The whole warp walks the steps and one elected lane issues, so that what the
-// products take stays in uniform registers.
+// The products of warpgroup i, a warp for each.  The whole warp walks the steps
+// and one elected lane issues, so that what the products take stays in uniform
+// registers.  Issuing takes as long as the products themselves, and the waits
+// between them several hundred cycles: with one warp for both warpgroups that time
+// was lost to the tensor core (16384 tokens 1380 us, now MEASURED).  The tiles of all units are one sequence: the next
+// S follows P V, or (P beside S) goes ahead of it, also from one unit to the next,
+// whose first S is there when the outputs of the one before are stored.
 template <int D>
 __device__ __forceinline__ void product_role(const PromptArgs &a, uint32_t base, const InlineWaiter &wait, uint32_t tmem_addr,
-                                             int lane) {
+                                             const int i, int lane) {
   using L = Smem<D>;
+  using M = Tmem<D>;
   constexpr uint32_t id_s = mma_idesc_bf16(128, kTile, false), id_o = mma_idesc_bf16(128, D, true);
   const bool leader = elect_one();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_addr, 0);
+  const uint32_t S = tmem + M::s + 128 * i, P = tmem + M::p + M::p_step * i, O = tmem + M::o + D * i;
   const uint64_t dq = mma_desc(base + L::q, 16, 1024), dk = mma_desc(base + L::k, 16, 1024),
                  dv = mma_desc(base + L::v, L::HALF, 1024);
   const int step = a.unit / 2;
   Units units(wait, base + L::units);
-  int ks = 0, vs = 0;            // places of the tiles of K and of V,
-  uint32_t kp = 0, vp = 0;       // and their parities
-  uint32_t np = 0, no = 0;       // bit i: parity of warpgroup i's steps, and of its units
+  int st = 0, qs = 0;                 // place of the tile of K and V, and of the next row tile,
+  uint32_t ph = 0, qp = 0;            // and their parities
+  uint32_t ns = 0, np = 0, no = 0;    // steps, P and units so far
+  // P V to be issued when P is there
+  bool any = false, first = false, last = false;
+  int v_st = 0, rows = 0;
+  uint32_t v_ph = 0;
+  auto output = [&]() {
+    if (!any) return;
+    any = false;
+    wait(B_VFULL + v_st, v_ph);
+    if (rows < kTile) {
+      // what lies behind the sequence may be anything, and 0 times it is not 0
+      // (each of the two warps does it: the other one's products read zeros)
+      const uint32_t to = base + L::v + v_st * L::TILE;
+      for (int x = rows * 8 + lane; x < kTile * 8; x += 32)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) sts128(to + c * L::HALF + 16 * x, 0u, 0u, 0u, 0u);
+      fence_proxy_async_shared();
+    }
+    if (first) wait(B_OFREE + i, (no++ & 1) ^ 1);
+    wait(B_P + i, np++ & 1);
+    __syncwarp();
+    tmem_fence_after();
+    if (leader) {
+      const uint64_t v = dv + v_st * (L::TILE / 16);
+#pragma unroll
+      for (int e = 0; e < kTile / 16; ++e) mma_f16_ts(O, P + 8 * e, v + e * (2048 / 16), id_o, !first || e > 0);
+      mma_commit(&wait.bars[B_VFREE + v_st]);
+      if constexpr (M::BESIDE) mma_commit(&wait.bars[B_PFREE + i]);
+      if (last) mma_commit(&wait.bars[B_O + i]);
+    }
+    __syncwarp();
+  };
   for (;;) {
     const uint4 u = units.next();
     if (static_cast<int>(u.x) < 0) break;
     const Work w(u, step);
-    wait(B_Q, units.n & 1);
     units.done(lane);
+    // the row tiles' places: the first warpgroup's, then the second's
+    int place[2];
+    uint32_t parity[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      place[k] = qs;
+      parity[k] = qp;
+      if (w.tiles[k] > 0 && ++qs == L::QS) {
+        qs = 0;
+        qp ^= 1;
+      }
+    }
+    const int tiles = i ? w.tiles[1] : w.tiles[0], q = i ? place[1] : place[0];
+    const uint32_t q_ph = i ? parity[1] : parity[0];
 #pragma unroll 1
-    for (int j = -1; j < w.all; ++j) {
+    for (int j = 0; j < w.all; ++j) {
+      if constexpr (!M::BESIDE) output();
+      if (j < tiles) {
+        if (j == 0) wait(B_Q + q, q_ph);
+        wait(B_KFULL + st, ph);
+        if constexpr (M::BESIDE) wait(B_TAKEN + i, (ns & 1) ^ 1);
+        ++ns;
+        __syncwarp();
+        tmem_fence_after();
+        if (leader) {
+          const uint64_t x = dq + q * (L::TILE / 16), k = dk + st * (L::TILE / 16);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bool other = i == 0 && j < w.tiles[1];  // the other warpgroup uses this tile after this one
-        if (j >= 0 && j < w.tiles[i]) {
-          wait(B_P + i, (np >> i) & 1);
-          np ^= 1u << i;
-          if (j == 0) {
-            wait(B_OFREE + i, ((no >> i) & 1) ^ 1);
-            no ^= 1u << i;
+          for (int e = 0; e < D / 16; ++e) {
+            const uint32_t off = ((e / 4) * L::HALF + (e % 4) * 32) / 16;
+            mma_f16_ss(S, x + off, k + off, id_s, e > 0);
           }
-          if (i == 0 || w.tiles[0] <= j) {
-            wait(B_VFULL + vs, vp);
-            const int rows = w.len - j * kTile;
-            if (rows < kTile) {
-              // what lies behind the sequence may be anything, and 0 times it is not 0
-              const uint32_t to = base + L::v + vs * L::TILE;
-              for (int x = rows * 8 + lane; x < kTile * 8; x += 32)
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) sts128(to + c * L::HALF + 16 * x, 0u, 0u, 0u, 0u);
-              fence_proxy_async_shared();
-            }
-          }
-          __syncwarp();
-          tmem_fence_after();
-          if (leader) {
-            const uint64_t v = dv + vs * (L::TILE / 16);
-            const uint32_t p = tmem + 128 * i, o = tmem + 256 + 128 * i;
-#pragma unroll
-            for (int e = 0; e < kTile / 16; ++e) mma_f16_ts(o, p + 8 * e, v + e * (2048 / 16), id_o, j > 0 || e > 0);
-            if (!other) mma_commit(&wait.bars[B_VFREE + vs]);
-            if (j + 1 == w.tiles[i]) mma_commit(&wait.bars[B_O + i]);
-          }
-          __syncwarp();
-          if (!other && ++vs == L::STAGES) {
-            vs = 0;
-            vp ^= 1;
-          }
+          mma_commit(&wait.bars[B_S + i]);
+          mma_commit(&wait.bars[B_KFREE + st]);
+          if (j + 1 == tiles) mma_commit(&wait.bars[B_QFREE + q]);
         }
-        if (j + 1 < w.tiles[i]) {
-          const bool more = i == 0 && j + 1 < w.tiles[1];
-          if (i == 0 || w.tiles[0] <= j + 1) wait(B_KFULL + ks, kp);
-          __syncwarp();
-          tmem_fence_after();
-          if (leader) {
-            const uint64_t q = dq + i * (L::TILE / 16), k = dk + ks * (L::TILE / 16);
-#pragma unroll
-            for (int e = 0; e < D / 16; ++e) {
-              const uint32_t off = ((e / 4) * L::HALF + (e % 4) * 32) / 16;
-              mma_f16_ss(tmem + 128 * i, q + off, k + off, id_s, e > 0);
-            }
-            mma_commit(&wait.bars[B_S + i]);
-            if (!more) {
-              mma_commit(&wait.bars[B_KFREE + ks]);
-              if (j + 2 == w.all) mma_commit(&wait.bars[B_QFREE]);
-            }
-          }
-          __syncwarp();
-          if (!more && ++ks == L::STAGES) {
-            ks = 0;
-            kp ^= 1;
-          }
+        __syncwarp();
+        if constexpr (M::BESIDE) output();
+        any = true;
+        first = j == 0;
+        last = j + 1 == tiles;
+        rows = w.len - j * kTile;
+        v_st = st;
+        v_ph = ph;
+      } else {
+        // a tile of the other warpgroup alone
+        if constexpr (M::BESIDE) output();
+        wait(B_KFULL + st, ph);
+        wait(B_VFULL + st, ph);
+        if (leader) {
+          mbar_arrive(&wait.bars[B_KFREE + st]);
+          mbar_arrive(&wait.bars[B_VFREE + st]);
         }
+        __syncwarp();
+      }
+      if (++st == L::STAGES) {
+        st = 0;
+        ph ^= 1;
       }
     }
   }
+  output();
   // nothing in flight when tensor memory is given back
-  if (leader) mma_commit(&wait.bars[B_END]);
+  if (leader) mma_commit(&wait.bars[B_END + i]);
   __syncwarp();
-  wait(B_END, 0);
+  wait(B_END + i, 0);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
@@ -393,7 +447,8 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base,
   using L = Smem<D>;
   const int wg = (threadIdx.x >> 7) - kSoftmaxWarp / 4, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
-  const uint32_t S = tmem + lanes + 128 * wg, O = tmem + lanes + 256 + 128 * wg;
+  using M = Tmem<D>;
+  const uint32_t S = tmem + lanes + M::s + 128 * wg, P = tmem + lanes + M::p + M::p_step * wg, O = tmem + lanes + M::o + D * wg;
   const int step = a.unit / 2, r = 32 * warp + lane, rt = r / a.G, g = r - rt * a.G;
   const int near = 32 * warp / a.G;  // the warp's first token
   const float c = rsqrtf(static_cast<float>(D)) * kLog2E;
@@ -412,7 +467,6 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base,
 #pragma unroll 1
     for (int j = 0; j < tiles; ++j) {
       wait(B_S + wg, ns & 1);
-      ++ns;
       __syncwarp();
       tmem_fence_after();
       uint32_t w0[32], w1[32], w2[32], w3[32];
@@ -424,6 +478,17 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base,
       tmem_wait_ld(w1);
       tmem_wait_ld(w2);
       tmem_wait_ld(w3);
+      if constexpr (M::BESIDE) {
+        // in registers: the next S may be written.  The P before it is free, and O
+        // is complete, once its product is.
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&wait.bars[B_TAKEN + wg]);
+        wait(B_PFREE + wg, (ns & 1) ^ 1);
+        __syncwarp();
+        tmem_fence_after();
+      }
+      ++ns;
       if (nearest < (j + 1) * kTile) {  // some row of the warp does not see the whole tile
         const int seen = limit - j * kTile;
 #pragma unroll
@@ -481,10 +546,10 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base,
         }
         tmem_st16(to, p);
       };
-      exponentials(w0, S);
-      exponentials(w1, S + 16);
-      exponentials(w2, S + 32);
-      exponentials(w3, S + 48);
+      exponentials(w0, P);
+      exponentials(w1, P + 16);
+      exponentials(w2, P + 32);
+      exponentials(w3, P + 48);
       l += (s0 + s1) + (s2 + s3);
       tmem_wait_st();
       tmem_fence_before();
@@ -540,10 +605,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t *const tm = reinterpret_cast<uint32_t *>(smem + L::tmem);
   if (warp == kLoadWarp) {
-    // arrivals per phase: 4 for a warpgroup's warps, 10 for all that read a unit, else 1
+    // arrivals per phase: 4 for a warpgroup's warps, 2 for the products' warps, 11
+    // for all that read a unit, else 1
     for (int i = lane; i < B_COUNT; i += 32) {
-      const bool four = (i >= B_P && i < B_P + 2) || (i >= B_OFREE && i < B_OFREE + 2);
-      mbar_init(&bars[i], four ? 4 : i >= B_UNITFREE && i < B_UNITFREE + 2 ? 10 : 1);
+      const bool four = (i >= B_TAKEN && i < B_TAKEN + 2) || (i >= B_P && i < B_P + 2) || (i >= B_OFREE && i < B_OFREE + 2);
+      const bool two = (i >= B_KFREE && i < B_KFREE + 4) || (i >= B_VFREE && i < B_VFREE + 4);
+      mbar_init(&bars[i], four ? 4 : two ? 2 : i >= B_UNITFREE && i < B_UNITFREE + 2 ? 11 : 1);
     }
     mbar_init_fence();
     if (lane == 0) {
@@ -568,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     fewer_registers<kFewRegs>();
     if (warp == kLoadWarp) load_role<D>(a, &qmap, &kmap, &vmap, base, wait, lane);
-    else if (warp == kMmaWarp) product_role<D>(a, base, wait, tmem, lane);
-    else if (warp == kPlanWarp) plan_role(a, base + L::units, wait, lane);
+    else if (warp < kPlanWarp) product_role<D>(a, base, wait, tmem, warp - kMmaWarp, lane);
+    else plan_role(a, base + L::units, wait, lane);
   }
   __syncwarp();
   tmem_fence_before();
