@@ -56,6 +56,9 @@ struct InlineWaiter {
   volatile uint32_t *abort;
   unsigned int *err;
   __device__ __forceinline__ void operator()(int bar, uint32_t parity) const {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(&bars[bar])), "r"(parity) : "memory");
+    if (ok) return;
     if (!mbar_suspend_wait(&bars[bar], parity)) mbar_long_wait(&bars[bar], parity, abort, err);
   }
 };

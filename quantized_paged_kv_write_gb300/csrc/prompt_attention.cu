@@ -162,7 +162,7 @@ struct Tmem {
 
 enum Bar : int {
   B_Q = 0, B_QFREE = 3, B_S = 6, B_TAKEN = 8, B_P = 10, B_PFREE = 12, B_O = 14, B_OFREE = 16, B_UNIT = 18, B_UNITFREE = 20,
-  B_KFULL = 22, B_KFREE = 26, B_VFULL = 30, B_VFREE = 34, B_END = 38, B_COUNT = 40
+  B_KFULL = 22, B_KFREE = 26, B_VFULL = 30, B_VFREE = 34, B_END = 38, B_TURN = 40, B_COUNT = 42
 };
 
 // What the roles need to know of a unit: tokens t0 .. and the tiles of keys of
@@ -329,10 +329,9 @@ __device__ __forceinline__ void product_role(const PromptArgs &a, uint32_t base,
   // P V to be issued when P is there
   bool any = false, first = false, last = false;
   int v_st = 0, rows = 0;
-  uint32_t v_ph = 0;
-  auto output = [&]() {
-    if (!any) return;
-    any = false;
+  uint32_t v_ph = 0, turns = 0;
+  // what it waits for
+  auto output_ready = [&]() {
     wait(B_VFULL + v_st, v_ph);
     if (rows < kTile) {
       // what lies behind the sequence may be anything, and 0 times it is not 0
@@ -345,17 +344,22 @@ __device__ __forceinline__ void product_role(const PromptArgs &a, uint32_t base,
     }
     if (first) wait(B_OFREE + i, (no++ & 1) ^ 1);
     wait(B_P + i, np++ & 1);
-    __syncwarp();
-    tmem_fence_after();
-    if (leader) {
-      const uint64_t v = dv + v_st * (L::TILE / 16);
+  };
+  auto issue_output = [&]() {  // (the leader)
+    const uint64_t v = dv + v_st * (L::TILE / 16);
 #pragma unroll
-      for (int e = 0; e < kTile / 16; ++e) mma_f16_ts(O, P + 8 * e, v + e * (2048 / 16), id_o, !first || e > 0);
-      mma_commit(&wait.bars[B_VFREE + v_st]);
-      if constexpr (M::BESIDE) mma_commit(&wait.bars[B_PFREE + i]);
-      if (last) mma_commit(&wait.bars[B_O + i]);
-    }
-    __syncwarp();
+    for (int e = 0; e < kTile / 16; ++e) mma_f16_ts(O, P + 8 * e, v + e * (2048 / 16), id_o, !first || e > 0);
+    mma_commit(&wait.bars[B_VFREE + v_st]);
+    if constexpr (M::BESIDE) mma_commit(&wait.bars[B_PFREE + i]);
+    if (last) mma_commit(&wait.bars[B_O + i]);
+  };
+  // P over S: the two warps issue in turns (left alone they fall into step, and the
+  // tensor core waits while both warpgroups take exponentials)
+  auto take_turn = [&]() {
+    if constexpr (!M::BESIDE) wait(B_TURN + i, (turns++ & 1) ^ (i == 0 ? 1 : 0));
+  };
+  auto pass_turn = [&]() {  // (the leader)
+    if constexpr (!M::BESIDE) mbar_arrive(&wait.bars[B_TURN + (i ^ 1)]);
   };
   for (;;) {
     const uint4 u = units.next();
@@ -378,15 +382,22 @@ __device__ __forceinline__ void product_role(const PromptArgs &a, uint32_t base,
     const uint32_t q_ph = i ? parity[1] : parity[0];
 #pragma unroll 1
     for (int j = 0; j < w.all; ++j) {
-      if constexpr (!M::BESIDE) output();
-      if (j < tiles) {
-        if (j == 0) wait(B_Q + q, q_ph);
-        wait(B_KFULL + st, ph);
-        if constexpr (M::BESIDE) wait(B_TAKEN + i, (ns & 1) ^ 1);
-        ++ns;
-        __syncwarp();
-        tmem_fence_after();
-        if (leader) {
+      const bool mine = j < tiles;  // (else a tile of the other warpgroup alone)
+      wait(B_KFULL + st, ph);
+      if (mine && j == 0) wait(B_Q + q, q_ph);
+      if constexpr (M::BESIDE) {
+        if (mine) wait(B_TAKEN + i, (ns++ & 1) ^ 1);
+      } else {
+        if (any) output_ready();
+        take_turn();
+      }
+      if (!mine) wait(B_VFULL + st, ph);
+      __syncwarp();
+      tmem_fence_after();
+      if (leader) {
+        if constexpr (!M::BESIDE)
+          if (any) issue_output();
+        if (mine) {
           const uint64_t x = dq + q * (L::TILE / 16), k = dk + st * (L::TILE / 16);
 #pragma unroll
           for (int e = 0; e < D / 16; ++e) {
@@ -396,33 +407,43 @@ __device__ __forceinline__ void product_role(const PromptArgs &a, uint32_t base,
           mma_commit(&wait.bars[B_S + i]);
           mma_commit(&wait.bars[B_KFREE + st]);
           if (j + 1 == tiles) mma_commit(&wait.bars[B_QFREE + q]);
-        }
-        __syncwarp();
-        if constexpr (M::BESIDE) output();
-        any = true;
-        first = j == 0;
-        last = j + 1 == tiles;
-        rows = w.len - j * kTile;
-        v_st = st;
-        v_ph = ph;
-      } else {
-        // a tile of the other warpgroup alone
-        if constexpr (M::BESIDE) output();
-        wait(B_KFULL + st, ph);
-        wait(B_VFULL + st, ph);
-        if (leader) {
+        } else {
           mbar_arrive(&wait.bars[B_KFREE + st]);
           mbar_arrive(&wait.bars[B_VFREE + st]);
         }
-        __syncwarp();
+        pass_turn();
       }
+      __syncwarp();
+      if constexpr (M::BESIDE) {
+        if (any) {
+          output_ready();
+          __syncwarp();
+          tmem_fence_after();
+          if (leader) issue_output();
+          __syncwarp();
+        }
+      }
+      any = mine;
+      first = j == 0;
+      last = j + 1 == tiles;
+      rows = w.len - j * kTile;
+      v_st = st;
+      v_ph = ph;
       if (++st == L::STAGES) {
         st = 0;
         ph ^= 1;
       }
     }
   }
-  output();
+  if (any) output_ready();
+  take_turn();
+  __syncwarp();
+  tmem_fence_after();
+  if (leader) {
+    if (any) issue_output();
+    pass_turn();
+  }
+  __syncwarp();
   // nothing in flight when tensor memory is given back
   if (leader) mma_commit(&wait.bars[B_END + i]);
   __syncwarp();
@@ -470,14 +491,15 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base,
       __syncwarp();
       tmem_fence_after();
       uint32_t w0[32], w1[32], w2[32], w3[32];
-      tmem_ld32(S, w0);
-      tmem_ld32(S + 32, w1);
-      tmem_ld32(S + 64, w2);
-      tmem_ld32(S + 96, w3);
-      tmem_wait_ld(w0);
-      tmem_wait_ld(w1);
-      tmem_wait_ld(w2);
-      tmem_wait_ld(w3);
+      float x0, x1, x2, x3;  // the row's largest
+      tmem_ld32_max(S, w0, x0);
+      tmem_ld32_max(S + 32, w1, x1);
+      tmem_ld32_max(S + 64, w2, x2);
+      tmem_ld32_max(S + 96, w3, x3);
+      tmem_wait_ld(w0, x0);
+      tmem_wait_ld(w1, x1);
+      tmem_wait_ld(w2, x2);
+      tmem_wait_ld(w3, x3);
       if constexpr (M::BESIDE) {
         // in registers: the next S may be written.  The P before it is free, and O
         // is complete, once its product is.
@@ -498,14 +520,14 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base,
           if (64 + e >= seen) w2[e] = 0xFF800000u;
           if (96 + e >= seen) w3[e] = 0xFF800000u;
         }
-      }
-      float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+        x0 = x1 = x2 = x3 = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        x0 = max3(x0, __uint_as_float(w0[e]), __uint_as_float(w0[e + 1]));
-        x1 = max3(x1, __uint_as_float(w1[e]), __uint_as_float(w1[e + 1]));
-        x2 = max3(x2, __uint_as_float(w2[e]), __uint_as_float(w2[e + 1]));
-        x3 = max3(x3, __uint_as_float(w3[e]), __uint_as_float(w3[e + 1]));
+        for (int e = 0; e < 32; e += 2) {
+          x0 = max3(x0, __uint_as_float(w0[e]), __uint_as_float(w0[e + 1]));
+          x1 = max3(x1, __uint_as_float(w1[e]), __uint_as_float(w1[e + 1]));
+          x2 = max3(x2, __uint_as_float(w2[e]), __uint_as_float(w2[e + 1]));
+          x3 = max3(x3, __uint_as_float(w3[e]), __uint_as_float(w3[e + 1]));
+        }
       }
       const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * c;
       // (each row for itself: what other rows of the warp hold changes nothing)
