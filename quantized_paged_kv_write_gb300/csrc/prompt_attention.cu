@@ -463,6 +463,24 @@ __device__ __forceinline__ void store_32(void *to, const uint32_t *r) {
                : "memory");
 }
 
+// Chunk c (8 words) of lane k of four to chunk k of lane c.
+__device__ __forceinline__ void transpose_chunks(uint32_t (&x)[32], int lane) {
+#pragma unroll
+  for (int s = 1; s < 4; s <<= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c & s) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint32_t &low = x[8 * c + e], &high = x[8 * (c + s) + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? low : high, s);
+        if (up) low = got; else high = got;
+      }
+    }
+  }
+}
+
 template <int D>
 __device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base, const InlineWaiter &wait, uint32_t tmem) {
   using L = Smem<D>;
@@ -583,21 +601,30 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base,
     ++no;
     __syncwarp();
     tmem_fence_after();
-    const int64_t row = static_cast<int64_t>(w.start + t) * a.Hq + w.h * a.G + g;
+    const int row = (w.start + t) * a.Hq + w.h * a.G + g;  // (below 2^30)
     const float inv = 1.f / l;
     const bool store = live && !*wait.abort;  // (after a wait that ran out the unit may be none)
+    // 64 channels at a time.  Four lanes trade their rows' 32-byte chunks, so that
+    // together they store whole lines: 32 lanes' stores to 32 rows took 2000 cycles a
+    // unit, in which no exponentials were taken.
 #pragma unroll
-    for (int cc = 0; cc < D / 32; ++cc) {
-      uint32_t o[32];
-      tmem_ld32(O + 32 * cc, o);
+    for (int cc = 0; cc < D / 64; ++cc) {
+      uint32_t o[32], x[32];
+      tmem_ld32(O + 64 * cc, o);
       tmem_wait_ld(o);
-      uint32_t b[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        b[e] = f32x2_to_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-      if (store) {
-        store_32(a.out + row * D + 32 * cc, b);
-        store_32(a.out + row * D + 32 * cc + 16, b + 8);
+        x[e] = f32x2_to_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+      tmem_ld32(O + 64 * cc + 32, o);
+      tmem_wait_ld(o);
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        x[16 + e] = f32x2_to_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+      transpose_chunks(x, lane);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int to = __shfl_sync(0xffffffffu, store ? row : -1, (lane & ~3) + k);
+        if (to >= 0) store_32(a.out + static_cast<int64_t>(to) * D + 64 * cc + 16 * (lane & 3), x + 8 * k);
       }
     }
     if (store && a.lse != nullptr) a.lse[row] = (mu + log2f(l)) * kLn2;
