@@ -916,7 +916,8 @@ int kvq_prompt_attention(const void *q_bf16, int64_t q_stride, const void *k_bf1
   PromptMaps m;
   if ((st = encode_rows_map(&m.q, q_bf16, num_tokens, num_q_heads, head_dim, q_stride, G, wl.unit / 2)) != KVQ_OK ||
       (st = encode_rows_map(&m.k, k_bf16, num_tokens, num_kv_heads, head_dim, k_stride, 1, 128)) != KVQ_OK ||
-      (st = encode_rows_map(&m.v, v_bf16, num_tokens, num_kv_heads, head_dim, v_stride, 1, 128)) != KVQ_OK)
+      (st = encode_rows_map(&m.v, v_bf16, num_tokens, num_kv_heads, head_dim, v_stride, 1, 128)) != KVQ_OK ||
+      (st = encode_rows_map(&m.out, out_bf16, num_tokens, num_q_heads, head_dim, qrow, G, wl.unit / 2)) != KVQ_OK)
     return st;
   int sms = 0;
   if ((st = sm_count(&sms)) != KVQ_OK) return st;

@@ -221,10 +221,10 @@ struct PromptArgs {
   int Hq, H, G;
   int unit, levels;            // tokens of a unit, tiles of max_seq
 };
-// Boxes of 64 channels: of a row tile's tokens and a kv head's query heads, and
-// of one head's tile of keys.
+// Boxes of 64 channels: of a row tile's tokens and a kv head's query heads (q,
+// out), and of one head's tile of keys.
 struct PromptMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, out;
 };
 cudaError_t launch_prompt_attention(int head_dim, const PromptArgs &a, const PromptMaps &maps, int sms,
                                     cudaStream_t stream);

@@ -142,11 +142,12 @@ struct Smem {
   static constexpr uint32_t HALF = 128 * 128;           // 64 channels of 128 rows
   static constexpr uint32_t TILE = HALF * (D / 64);
   static constexpr int STAGES = D == 128 ? 2 : 4;       // places for tiles of K, and of V
-  static constexpr int QS = 3;                          // and for row tiles: this unit's and one of the next
+  static constexpr int QS = 2;                          // and for row tiles
   static constexpr uint32_t q = 0;
   static constexpr uint32_t k = q + QS * TILE;
   static constexpr uint32_t v = k + STAGES * TILE;
-  static constexpr uint32_t bars = v + STAGES * TILE;
+  static constexpr uint32_t out = v + STAGES * TILE;    // [2] 64 channels of a warpgroup's outputs
+  static constexpr uint32_t bars = out + 2 * HALF;
   static constexpr uint32_t tmem = bars + 64 * 8;       // tensor memory address, then the abort flag
   static constexpr uint32_t units = tmem + 16;          // [2] {start, len, t0, h}; start -1: the end
   static constexpr uint32_t bytes = units + 32;
@@ -463,26 +464,17 @@ __device__ __forceinline__ void store_32(void *to, const uint32_t *r) {
                : "memory");
 }
 
-// Chunk c (8 words) of lane k of four to chunk k of lane c.
-__device__ __forceinline__ void transpose_chunks(uint32_t (&x)[32], int lane) {
-#pragma unroll
-  for (int s = 1; s < 4; s <<= 1) {
-    const bool up = lane & s;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (c & s) continue;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        uint32_t &low = x[8 * c + e], &high = x[8 * (c + s) + e];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? low : high, s);
-        if (up) low = got; else high = got;
-      }
-    }
-  }
+__device__ __forceinline__ void tma_store(uint32_t from, const CUtensorMap *map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(from)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
 template <int D>
-__device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base, const InlineWaiter &wait, uint32_t tmem) {
+__device__ __forceinline__ void softmax_role(const PromptArgs &a, const CUtensorMap *om, uint32_t base, const InlineWaiter &wait,
+                                             uint32_t tmem) {
   using L = Smem<D>;
   const int wg = (threadIdx.x >> 7) - kSoftmaxWarp / 4, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
@@ -493,13 +485,17 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base,
   const float c = rsqrtf(static_cast<float>(D)) * kLog2E;
   Units units(wait, base + L::units);
   uint32_t ns = 0, no = 0;  // steps and units of this warpgroup so far
-  for (;;) {
-    const uint4 u = units.next();
-    if (static_cast<int>(u.x) < 0) break;
+  const bool sender = (threadIdx.x & 127) == 0;  // of the warpgroup's outputs
+  auto meet = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
+  uint4 u = units.next();
+  while (static_cast<int>(u.x) >= 0) {
     const Work w(u, step);
     units.done(lane);
     const int tiles = wg ? w.tiles[1] : w.tiles[0], t = w.t0 + wg * step + rt;
-    if (tiles == 0) continue;
+    if (tiles == 0) {
+      u = units.next();
+      continue;
+    }
     const bool live = rt < step && t < w.len;
     const int limit = live ? t + 1 : INT_MAX, nearest = w.t0 + wg * step + near + 1;
     float mu = -INFINITY, l = 0.f;
@@ -596,17 +592,18 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base,
       __syncwarp();
       if (lane == 0) mbar_arrive(&wait.bars[B_P + wg]);
     }
-    // ---- the rows' outputs
+    // ---- the rows' outputs, 64 channels at a time through shared memory and the copy
+    // unit (stores of a lane for each row kept the warpgroup 1500 cycles longer from
+    // its next unit); the last rows of a sequence, which are fewer, one by one
+    u = units.next();
     wait(B_O + wg, no & 1);
     ++no;
     __syncwarp();
     tmem_fence_after();
-    const int row = (w.start + t) * a.Hq + w.h * a.G + g;  // (below 2^30)
     const float inv = 1.f / l;
-    const bool store = live && !*wait.abort;  // (after a wait that ran out the unit may be none)
-    // 64 channels at a time.  Four lanes trade their rows' 32-byte chunks, so that
-    // together they store whole lines: 32 lanes' stores to 32 rows took 2000 cycles a
-    // unit, in which no exponentials were taken.
+    const bool run_out = *wait.abort;  // (then the unit may be none)
+    const bool whole = w.t0 + (wg + 1) * step <= w.len, store = live && !run_out;
+    const int64_t row = static_cast<int64_t>(w.start + t) * a.Hq + w.h * a.G + g;
 #pragma unroll
     for (int cc = 0; cc < D / 64; ++cc) {
       uint32_t o[32], x[32];
@@ -620,18 +617,29 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, uint32_t base,
 #pragma unroll
       for (int e = 0; e < 16; ++e)
         x[16 + e] = f32x2_to_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-      transpose_chunks(x, lane);
+      if (cc + 1 == D / 64) {  // O is in registers
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&wait.bars[B_OFREE + wg]);
+      }
+      if (whole) {
+        // (the copy before has read its place)
+        if (sender) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        meet();
+        const uint32_t to = base + L::out + wg * L::HALF;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int to = __shfl_sync(0xffffffffu, store ? row : -1, (lane & ~3) + k);
-        if (to >= 0) store_32(a.out + static_cast<int64_t>(to) * D + 64 * cc + 16 * (lane & 3), x + 8 * k);
+        for (int e = 0; e < 8; ++e) sts128(to + 128 * r + 16 * (e ^ (r & 7)), x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        fence_proxy_async_shared();
+        meet();
+        if (sender && !run_out) tma_store(to, om, 64 * cc, w.h * a.G, w.start + w.t0 + wg * step);
+      } else if (store) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) store_32(a.out + row * D + 64 * cc + 16 * e, x + 8 * e);
       }
     }
     if (store && a.lse != nullptr) a.lse[row] = (mu + log2f(l)) * kLn2;
-    tmem_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&wait.bars[B_OFREE + wg]);
   }
+  if (sender) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 template <int N>
@@ -646,7 +654,8 @@ __device__ __forceinline__ void fewer_registers() {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                         const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PromptArgs a) {
+                         const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap,
+                         const __grid_constant__ PromptArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   using L = Smem<D>;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
@@ -666,6 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tensormap(&qmap);
       prefetch_tensormap(&kmap);
       prefetch_tensormap(&vmap);
+      prefetch_tensormap(&omap);
       *reinterpret_cast<volatile uint32_t *>(tm + 1) = 0;
       for (int i = 0; i < 2; ++i) sts128(base + L::units + 16 * i, 0xFFFFFFFFu, 0u, 0u, 0u);
     }
@@ -680,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const InlineWaiter wait = {bars, tm + 1, a.err};
   if (warp >= kSoftmaxWarp) {
     more_registers<kManyRegs>();
-    softmax_role<D>(a, base, wait, tmem);
+    softmax_role<D>(a, &omap, base, wait, tmem);
   } else {
     fewer_registers<kFewRegs>();
     if (warp == kLoadWarp) load_role<D>(a, &qmap, &kmap, &vmap, base, wait, lane);
@@ -711,7 +721,7 @@ static cudaError_t attend(const PromptArgs &a, const PromptMaps &m, int sms, cud
       return e;
     done.fetch_or(1ull << dev, std::memory_order_acq_rel);
   }
-  return launch_overlapped(kern, sms, kThreads, Smem<D>::bytes, stream, m.q, m.k, m.v, a);
+  return launch_overlapped(kern, sms, kThreads, Smem<D>::bytes, stream, m.q, m.k, m.v, m.out, a);
 }
 
 cudaError_t launch_prompt_attention(int head_dim, const PromptArgs &a, const PromptMaps &m, int sms, cudaStream_t stream) {
