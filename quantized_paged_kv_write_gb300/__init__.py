@@ -178,12 +178,12 @@ class CacheFormat:
     rotation_signs: Optional[tuple] = None
 
     def as_c(self) -> _Format:
-        rot = self.rotation_signs is not None
-        signs = (ctypes.c_uint32 * 4)(*(tuple(int(w) & 0xFFFFFFFF for w in self.rotation_signs) if rot
-                                        else (0, 0, 0, 0)))
-        return _Format(DTYPES[self.k_dtype], DTYPES[self.v_dtype], GRANS[self.k_gran], GRANS[self.v_gran],
-                       self.k_group, self.v_group, self.num_kv_heads, self.head_dim, self.block_size,
-                       1 if rot else 0, self.num_blocks, signs)
+        f = _Format(DTYPES[self.k_dtype], DTYPES[self.v_dtype], GRANS[self.k_gran], GRANS[self.v_gran],
+                    self.k_group, self.v_group, self.num_kv_heads, self.head_dim, self.block_size, 0, self.num_blocks)
+        if self.rotation_signs is not None:
+            f.rotation = 1
+            f.rotation_signs = (ctypes.c_uint32 * 4)(*(int(w) & 0xFFFFFFFF for w in self.rotation_signs))
+        return f
 
     def code_row_bytes(self, which: str) -> int:
         dt = self.k_dtype if which == "k" else self.v_dtype
@@ -626,14 +626,16 @@ def kvq_prefix_decode(q: torch.Tensor, fmt: CacheFormat, cache: dict, block_tabl
 def _rows(t: torch.Tensor, what: str) -> tuple:
     """Pointer and token stride of BF16 [N, heads, d] whose tokens may lie apart
     (a part of a projection's rows)."""
-    if isinstance(t, torch.Tensor) and t.dim() == 3:
-        n, heads, d = t.shape
-        if t.numel() and t.stride(2) == 1 and (heads == 1 or t.stride(1) == d) and (n == 1 or t.stride(0) >= heads * d):
-            return _ptr(t[0], torch.bfloat16, what), int(t.stride(0)) if n > 1 else heads * d
-        if not t.numel():
-            return _ptr(t, torch.bfloat16, what), max(heads * d, 8)
+    n, heads, d = t.shape
+    if t.is_contiguous():
+        return _ptr(t, torch.bfloat16, what), max(heads * d, 8)
+    if n == 1:
+        return _ptr(t[0], torch.bfloat16, what), heads * d
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d) or t.stride(0) < heads * d:
         raise ValueError(f"{what}: a token's heads must be contiguous")
-    return _ptr(t, torch.bfloat16, what), 0
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice() or t.dtype is not torch.bfloat16:
+        _ptr(t[0], torch.bfloat16, what)  # (raises)
+    return t.data_ptr(), t.stride(0)
 
 
 def kvq_prompt_attention_workspace_size(num_seqs: int, max_seq_len: int, num_q_heads: int, num_kv_heads: int) -> int:
@@ -711,10 +713,13 @@ def kvq_weigh_decode(q: torch.Tensor, fmt: CacheFormat, cache: dict, block_table
         out = _empty((bsz, hq, d), torch.float32, q.device, stream)
     elif tuple(out.shape) != (bsz, hq, d):
         raise ValueError("out must have the shape of q")
-    if workspace is None:
-        nbytes = kvq_weigh_decode_workspace_size(fmt, bsz, hq, max_context_len)
-        workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     cf = fmt.as_c()
+    if workspace is None:
+        need = ctypes.c_size_t(0)
+        st = lib.kvq_weigh_decode_workspace_size(ctypes.byref(cf), bsz, hq, int(max_context_len), ctypes.byref(need))
+        if st != KVQ_OK:
+            raise KvqError(st, "kvq_weigh_decode")
+        workspace = _empty(max(need.value, 256), torch.uint8, q.device, stream)
     caches, scales = _caches(cache)
     st = lib.kvq_weigh_decode(_ptr(q, torch.bfloat16, "q"), bsz, hq, ctypes.byref(cf), caches, scales,
                               _ptr(block_tables, torch.int32, "block_tables"), int(block_tables.shape[1]),
