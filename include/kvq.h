@@ -533,7 +533,8 @@ int kvq_weigh_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, con
  *                 write into a block whose count is not 1 is left as it is
  *   weights       [num_rows, num_kv_heads, max_positions] FP32 (updated)
  *   kept_lens     [num_rows] int32: min(n, k), or n where the row was left as it
- *                 is (written): the keep_lens of the kvq_release_blocks to follow
+ *                 is (written; no part of the lengths above): the keep_lens of the
+ *                 kvq_release_blocks to follow
  *   workspace     device buffer of at least kvq_evict_workspace_size() bytes,
  *                 256-byte aligned
  *

@@ -769,6 +769,12 @@ static int check_evict(int32_t num_rows, int32_t num_kv_heads, int32_t max_posit
   return num_rows > 8192 || num_kv_heads > 8 || max_positions > (1 << 30) ? KVQ_ERR_UNSUPPORTED : KVQ_OK;
 }
 
+// Whether two arrays of n entries share some.
+static bool overlap(const int32_t *a, const int32_t *b, int32_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b), bytes = 4 * static_cast<uintptr_t>(n);
+  return a != nullptr && b != nullptr && x < y + bytes && y < x + bytes;
+}
+
 int kvq_evict_workspace_size(int32_t num_rows, int32_t num_kv_heads, int32_t max_positions, size_t *bytes) {
   const int st = check_evict(num_rows, num_kv_heads, max_positions);
   if (st != KVQ_OK) return st;
@@ -800,6 +806,10 @@ int kvq_evict_tokens(const int32_t *keep_lens, const int32_t *recent_lens, const
       !aligned16(scales.v_scale) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return KVQ_ERR_INVALID_ARG;
   size_t list;
+  // written while other CTAs still read theirs
+  if (overlap(kept_lens, keep_lens, num_rows) || overlap(kept_lens, recent_lens, num_rows) ||
+      overlap(kept_lens, pinned_lens, num_rows) || overlap(kept_lens, context_lens, num_rows))
+    return KVQ_ERR_INVALID_ARG;
   if (workspace_bytes < evict_ws(num_rows, fmt->num_kv_heads, max_positions, &list)) return KVQ_ERR_WORKSPACE;
   EvictArgs a;
   if (error_word(&a.err) != cudaSuccess) return KVQ_ERR_CUDA;

@@ -142,6 +142,40 @@ def test_weights_captured_replayed_and_on_a_side_stream():
     assert torch.equal(got, want) and torch.equal(weights, once)
 
 
+def test_weights_of_two_calls_at_once():
+    """Two streams, each with its own workspace."""
+    ctx = [900, 30, 1200]
+    fmt, cache, oc, tables, gen = make("fp8", "v4", 8, 128, ctx, seed=8)
+    t, c = _i32(tables), _i32(ctx)
+    q = torch.randn((2, 3, 32, 128), generator=gen, device="cuda").to(torch.bfloat16)
+    weights = torch.zeros((2, 3, 8, 1200), device="cuda")
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    out = [None, None]
+    for _ in range(5):
+        for k in range(2):
+            out[k] = kvq.kvq_weigh_decode(q[k], fmt, cache, t, c, 1200, weights[k], stream=streams[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        once = torch.zeros((3, 8, 1200), device="cuda")
+        assert torch.equal(kvq.kvq_weigh_decode(q[k], fmt, cache, t, c, 1200, once), out[k])
+        five = torch.zeros_like(once)
+        for _ in range(5):
+            five += once
+        assert torch.equal(five, weights[k])
+
+
+def test_weights_of_eight_thousand_rows():
+    rng = np.random.default_rng(3)
+    ctx = [int(x) for x in rng.integers(0, 20, 8192) * (rng.random(8192) < 0.3)]
+    fmt, cache, oc, tables, gen = make("int8", "int8", 1, 64, ctx, seed=9)
+    q = torch.randn((len(ctx), 3, 64), generator=gen, device="cuda").to(torch.bfloat16)
+    weights = torch.zeros((len(ctx), 1, 20), device="cuda")
+    kvq.kvq_weigh_decode(q, fmt, cache, _i32(tables), _i32(ctx), 20, weights)
+    some = sorted(set(rng.integers(0, 8192, 300).tolist()) | {0, 8191})
+    check_weights(weights[some], np.zeros((len(some), 1, 20)), oc, q[some], tables[some], [ctx[i] for i in some], fmt)
+
+
 class Both:
     """The same cache and weights on the device and in the oracle."""
 
@@ -212,9 +246,10 @@ def test_ties_and_odd_weights(kind):
 
 
 @pytest.mark.parametrize("h,rows,length,kind", [(1, 1, 20000, "few"), (2, 3, 9001, "zero"), (4, 9, 8192, "rand"), (1, 70, 8192, "few"),
-                                                (8, 40, 8195, "few"), (2, 1, 33000, "rand"), (3, 1, 70001, "few")])
+                                                (8, 40, 8195, "few"), (2, 1, 33000, "rand"), (3, 1, 70001, "few"), (1, 1, 140003, "few"),
+                                                (7, 30, 16390, "few")])
 def test_long_rows_with_ties(h, rows, length, kind):
-    """One CTA, a cluster of two, four and eight for each (row, head), several steps of a CTA."""
+    """One CTA, a cluster of two, four and eight for each (row, head); the longest one's keys are not held."""
     rng = np.random.default_rng(length)
     w = np.zeros((rows, h, length), np.float32) if kind == "zero" else rng.integers(0, 4, (rows, h, length)).astype(np.float32)
     if kind == "rand":

@@ -175,6 +175,39 @@ def test_captured_and_replayed_with_other_lengths():
         check(q, k, v, o, out, lse, fill=7.0)
 
 
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace, and two graphs that share one in turn."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    x = [[_draw(gen, 2500, h, 128) for h in (16, 4, 4)] for _ in range(2)]
+    offsets = _i32([0, 1700, 2500])
+    want = [kvq.kvq_prompt_attention(*y, offsets, 1700) for y in x]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    for _ in range(4):
+        for k in range(2):
+            got[k] = kvq.kvq_prompt_attention(*x[k], offsets, 1700, stream=streams[k])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    ws = torch.empty(kvq.kvq_prompt_attention_workspace_size(2, 1700, 16, 4), dtype=torch.uint8, device="cuda")
+    out, graphs = [torch.zeros_like(want[0]) for _ in range(2)], [torch.cuda.CUDAGraph() for _ in range(2)]
+    torch.cuda.synchronize()
+    for k in range(2):
+        with torch.cuda.graph(graphs[k]):
+            kvq.kvq_prompt_attention(*x[k], offsets, 1700, out=out[k], workspace=ws)
+    for _ in range(3):
+        graphs[0].replay()
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+def test_a_bound_far_above_the_lengths():
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    q, k, v = (_draw(gen, 300, h, 64) for h in (8, 1, 1))
+    want, _ = attend(q, k, v, [0, 1, 300])
+    assert torch.equal(kvq.kvq_prompt_attention(q, k, v, _i32([0, 1, 300]), 1 << 24), want)
+
+
 def test_bad_offsets_write_nothing():
     gen = torch.Generator(device="cuda").manual_seed(7)
     q, k, v = (_draw(gen, 300, h, 64) for h in (2, 1, 1))
