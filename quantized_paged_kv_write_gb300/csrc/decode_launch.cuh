@@ -15,6 +15,7 @@ namespace detail {
 // 1 KB reserved per CTA).
 constexpr size_t kSmemPerCtaTarget = 112 * 1024;
 constexpr int kMaxStages = 6;
+constexpr int kReduceRows = 1024;  // rows of fewer take more warps
 
 template <int D, int KF, int VF, bool WIDE, int HT, bool ROT, bool SCORES>
 cudaError_t plan_one(int H, int B, DecodePlan *plan) {
@@ -72,8 +73,13 @@ cudaError_t launch_one(const DecodeArgs &a, const DecodePlan &plan, const Decode
     if (e != cudaSuccess) return e;
   }
   if (a.split_only) return cudaSuccess;
+  // few rows: a warp for every 32 channels (a rotated row and a tail need the whole
+  // row in one)
   const int warps = a.B * a.Hq;
-  decode_reduce_kernel<D><<<(warps + 7) / 8, 256, 0, stream>>>(a, a.ws_cum);
+  if (warps <= kReduceRows && !a.rot && a.res_k == nullptr)
+    decode_reduce_kernel<D, D / 32><<<(warps * (D / 32) + 7) / 8, 256, 0, stream>>>(a, a.ws_cum);
+  else
+    decode_reduce_kernel<D, 1><<<(warps + 7) / 8, 256, 0, stream>>>(a, a.ws_cum);
   return cudaGetLastError();
 }
 

@@ -1272,19 +1272,25 @@ __global__ void __maxnreg__(kDecodeMaxRegs)
 }
 
 // ---------------------------------------------------------------------------
-// split-reduce: one warp per (sequence, query head)
+// split-reduce: PARTS warps per (sequence, query head), each with its share of the
+// channels.  A channel's partials are added in one order whatever PARTS is, so the
+// results are the same bits; with few rows of many partials the loads' latency
+// bounds it, and more warps with more loads each hide it (D = 128, one warp and D / 32
+// of them: 32 rows of 60000 positions 112.6 and 49.4 us, 256 rows of 8000 14.9 and 9.8,
+// 1024 rows of 1000 6.5 and 6.1, 2048 rows of 4000 6.0 and 10.1).
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, int PARTS>
 __global__ void __launch_bounds__(256) decode_reduce_kernel(const DecodeArgs a, const int *__restrict__ cum) {
-  const int warp = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int unit = blockIdx.x * 8 + (threadIdx.x >> 5), warp = unit / PARTS;
   const int lane = threadIdx.x & 31;
   if (warp >= a.B * a.Hq) return;
   const int b = warp / a.Hq;
   const int hq = warp % a.Hq;
   const int h = hq / a.G;
   const int g = hq % a.G;
-  constexpr int CPL = D / 32;  // channels per lane
-  float *outp = a.out + static_cast<int64_t>(warp) * D + lane * CPL;
+  constexpr int CPL = D / 32 / PARTS;  // channels per lane
+  const int ch0 = (unit - warp * PARTS) * 32 * CPL + lane * CPL;
+  float *outp = a.out + static_cast<int64_t>(warp) * D + ch0;
   const int c0b = cum[b], c1b = cum[b + 1];
   float acc[CPL];
 #pragma unroll
@@ -1319,7 +1325,7 @@ __global__ void __launch_bounds__(256) decode_reduce_kernel(const DecodeArgs a, 
       // pass 2: weights per split (lane s), then the weighted sum of the
       // partial outputs with every lane on its channels, eight partials'
       // loads in flight at a time
-      constexpr int U = 8;
+      constexpr int U = CPL == 1 ? 16 : 8;
       for (int base = 0; base < ns; base += 32) {
         float w = 0.f;
         if (base + lane < ns) {
@@ -1342,7 +1348,7 @@ __global__ void __launch_bounds__(256) decode_reduce_kernel(const DecodeArgs a, 
             for (int q = 0; q < CPL; ++q) v[u][q] = 0.f;
             if (k0 + u < n) {
               const int64_t rec = (static_cast<int64_t>(b) + s0 + base + k0 + u) * a.H + h;
-              const float *col = a.ws_o + (rec * 8 + g) * D + lane * CPL;
+              const float *col = a.ws_o + (rec * 8 + g) * D + ch0;
               if constexpr (CPL == 4) {
                 const float4 x = *reinterpret_cast<const float4 *>(col);
                 v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
@@ -1369,7 +1375,7 @@ __global__ void __launch_bounds__(256) decode_reduce_kernel(const DecodeArgs a, 
       for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     }
   }
-  if (a.res_k != nullptr) {
+  if (PARTS == 1 && a.res_k != nullptr) {
     // per-channel K with a full-precision tail: the residual rows 0 .. nt - 1
     // hold positions [n - nt, n); merged into (mx, L, acc) token by token
     const int n = __ldg(a.ctx + b);
@@ -1401,11 +1407,11 @@ __global__ void __launch_bounds__(256) decode_reduce_kernel(const DecodeArgs a, 
     }
   }
   const float inv = (L > 0.f) ? 1.f / L : 0.f;
-  if (a.ws_norm != nullptr && lane == 0) a.ws_norm[warp] = make_float2(mx, inv);
+  if (a.ws_norm != nullptr && lane == 0 && ch0 == 0) a.ws_norm[warp] = make_float2(mx, inv);
   float o[CPL];
 #pragma unroll
   for (int k = 0; k < CPL; ++k) o[k] = acc[k] * inv;
-  if (a.rot) {
+  if (PARTS == 1 && a.rot) {
     // rotated cache: the merged output is in the rotated basis; return
     // sigma * (H o') / d.  This lane holds channels CPL lane .. + CPL - 1:
     // butterfly stages below CPL inside the lane, the others across lanes.
