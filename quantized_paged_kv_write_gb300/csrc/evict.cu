@@ -182,10 +182,21 @@ __global__ void __launch_bounds__(T, 1536 / T) evict_select_kernel(const EvictAr
   // every block of the row, and nobody else's among those to be written
   const int32_t *table = a.tables + static_cast<int64_t>(r) * a.max_blocks;
   bool bad = false, shared = false;
-  for (int i = tid; i < (n + kBlockSize - 1) / kBlockSize; i += T) {
-    const int id = __ldg(table + i);
-    if (id < 0 || id >= a.num_blocks) bad = true;
-    else if (a.refs != nullptr && i >= p / kBlockSize && i * kBlockSize < keep && __ldg(a.refs + id) != 1) shared = true;
+  // (eight of a thread in flight: one by one they took longer than the passes below)
+  constexpr int C = 8;
+  const int blocks = (n + kBlockSize - 1) / kBlockSize;
+#pragma unroll 1
+  for (int base = tid; base < blocks; base += C * T) {
+    int id[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) id[c] = base + c * T < blocks ? __ldg(table + base + c * T) : 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int i = base + c * T;
+      if (i >= blocks) break;
+      if (id[c] < 0 || id[c] >= a.num_blocks) bad = true;
+      else if (a.refs != nullptr && i >= p / kBlockSize && i * kBlockSize < keep) shared = shared || __ldg(a.refs + id[c]) != 1;
+    }
   }
   bad = __syncthreads_or(bad);
   shared = __syncthreads_or(shared);
@@ -444,57 +455,77 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
   }
 }
 
-// The last w tokens of a (row, head), as many at a time as a CTA's registers hold.
-// Where they overlap their new places, one CTA takes them in ascending order (a
-// place is below its token); else its CTAs share them.  Weights past k become 0.
+// The last w tokens of a (row, head) move down by s = n - k places.  A place is
+// written by the token s behind it and no other, so the tokens of one residue of s
+// are a chain of their own: the CTAs share the residues, and each takes its tokens
+// in ascending order, as many at a time as its registers hold (all are read before
+// any is written).  Weights past k become 0.
+// A CTA that has all residues, or whose residues have one token each, has
+// neighbouring tokens and needs no division (NEAR).
 constexpr int kShiftThreads = 256, kShiftPieces = 8;
+template <int LANES, bool NEAR>
+__device__ __forceinline__ void shift_tokens(const EvictArgs &a, const int32_t *table, float *weights, int h, int n, int k, int w,
+                                             int c0, int r) {
+  constexpr int TOKENS = kShiftThreads * kShiftPieces / LANES, SCALARS = (TOKENS + kShiftThreads - 1) / kShiftThreads;
+  const int tid = threadIdx.x, piece = tid % LANES, s = n - k;
+  const bool has = piece < (a.krow + a.vrow) / 16;
+  const int first = n - w, to = k - w;
+  // element e of this CTA's; those past its last get w
+  const int mine = NEAR ? (w <= s ? r : w) : (w - c0 + s - 1) / s * r;
+  auto token = [&](int e) {
+    if (e >= mine) return w;
+    if (NEAR) return c0 + e;
+    const int m = e / r;
+    const int64_t i = static_cast<int64_t>(m) * s + c0 + (e - m * r);
+    return i < w ? static_cast<int>(i) : w;
+  };
+#pragma unroll 1
+  for (int base = 0; base < mine; base += TOKENS) {
+    uint4 v[kShiftPieces];
+    Rest rest[SCALARS];
+#pragma unroll
+    for (int u = 0; u < kShiftPieces; ++u) {
+      const int i = token(base + (u * kShiftThreads + tid) / LANES);
+      if (has && i < w) v[u] = *piece_of(a, slot_of(a, table, h, first + i), piece);
+    }
+#pragma unroll
+    for (int u = 0; u < SCALARS; ++u) {
+      const int i = token(base + u * kShiftThreads + tid);
+      if (u * kShiftThreads + tid < TOKENS && i < w) rest[u] = load_rest(a, weights, slot_of(a, table, h, first + i), first + i);
+    }
+    if (w > s) __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kShiftPieces; ++u) {
+      const int i = token(base + (u * kShiftThreads + tid) / LANES);
+      if (has && i < w) *piece_of(a, slot_of(a, table, h, to + i), piece) = v[u];
+    }
+#pragma unroll
+    for (int u = 0; u < SCALARS; ++u) {
+      const int i = token(base + u * kShiftThreads + tid);
+      if (u * kShiftThreads + tid >= TOKENS || i >= w) continue;
+      store_rest(a, weights, slot_of(a, table, h, to + i), to + i, rest[u]);
+      if (first + i >= k) weights[first + i] = 0.f;  // (its reader clears it)
+    }
+    if (w > s) __syncthreads();
+  }
+}
+
 template <int LANES>
 __global__ void __launch_bounds__(kShiftThreads, 3) evict_shift_kernel(const EvictArgs a) {
-  constexpr int TOKENS = kShiftThreads * kShiftPieces / LANES, SCALARS = (TOKENS + kShiftThreads - 1) / kShiftThreads;
-  const int x = blockIdx.x, tid = threadIdx.x, piece = tid % LANES;
-  const bool has = piece < (a.krow + a.vrow) / 16;
+  const int x = blockIdx.x, y = blockIdx.y;
   grid_wait();  // the moves have read what is written here
   const EvictMeta meta = a.ws_meta[x];
   if (!meta.active) return;
   const int32_t *table = a.tables + static_cast<int64_t>(x / a.H) * a.max_blocks;
   const int n = __ldg(a.ctx + x / a.H), w = meta.recent, k = meta.keep, h = x % a.H;
-  const bool apart = n - k >= w;
-  const int ctas = apart ? gridDim.y : 1, y = blockIdx.y;
-  if (y >= ctas) return;
   float *weights = a.weights + static_cast<int64_t>(x) * a.stride;
-#pragma unroll 1
-  for (int64_t at = static_cast<int64_t>(y) * TOKENS; at < w; at += ctas * TOKENS) {
-    const int base = static_cast<int>(at);
-    uint4 v[kShiftPieces];
-    Rest rest[SCALARS];
-#pragma unroll
-    for (int u = 0; u < kShiftPieces; ++u) {
-      const int i = base + (u * kShiftThreads + tid) / LANES;
-      if (has && i < w) v[u] = *piece_of(a, slot_of(a, table, h, n - w + i), piece);
-    }
-#pragma unroll
-    for (int u = 0; u < SCALARS; ++u) {
-      const int i = base + u * kShiftThreads + tid;
-      if (u * kShiftThreads + tid < TOKENS && i < w) rest[u] = load_rest(a, weights, slot_of(a, table, h, n - w + i), n - w + i);
-    }
-    if (!apart) __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kShiftPieces; ++u) {
-      const int i = base + (u * kShiftThreads + tid) / LANES;
-      if (has && i < w) *piece_of(a, slot_of(a, table, h, k - w + i), piece) = v[u];
-    }
-#pragma unroll
-    for (int u = 0; u < SCALARS; ++u) {
-      const int i = base + u * kShiftThreads + tid;
-      if (u * kShiftThreads + tid < TOKENS && i < w) {
-        store_rest(a, weights, slot_of(a, table, h, k - w + i), k - w + i, rest[u]);
-        if (apart) weights[n - w + i] = 0.f;  // (its reader clears it)
-      }
-    }
-    if (!apart) __syncthreads();
-  }
-  const int end = apart ? n - w : n;
-  for (int64_t i = k + static_cast<int64_t>(y) * kShiftThreads + tid; i < end; i += ctas * kShiftThreads) weights[i] = 0.f;
+  // residues [c0, c0 + r) of the chains, of which there are no more than tokens
+  const int chains = min(n - k, w);
+  const int c0 = static_cast<int>(static_cast<int64_t>(chains) * y / gridDim.y);
+  const int r = static_cast<int>(static_cast<int64_t>(chains) * (y + 1) / gridDim.y) - c0;
+  if (r == n - k || w <= n - k) shift_tokens<LANES, true>(a, table, weights, h, n, k, w, c0, r);
+  else if (r > 0) shift_tokens<LANES, false>(a, table, weights, h, n, k, w, c0, r);
+  for (int64_t i = k + static_cast<int64_t>(y) * kShiftThreads + threadIdx.x; i < n - w; i += gridDim.y * kShiftThreads) weights[i] = 0.f;
 }
 
 template <int LANES>
@@ -504,9 +535,9 @@ cudaError_t move(const EvictArgs &a, int sms, cudaStream_t stream) {
   cudaError_t e = launch_overlapped(evict_move_kernel<LANES>, static_cast<int>(ctas < 1 ? 1 : ctas < 8 * sms ? ctas : 8 * sms),
                                     256, 0, stream, a);
   if (e != cudaSuccess) return e;
-  // CTAs for a (row, head): enough for all SMs, where its tokens can be shared
+  // CTAs for a (row, head): enough for all SMs
   const int share = static_cast<int>(4 * sms / heads);
-  return launch_overlapped(evict_shift_kernel<LANES>, dim3(static_cast<unsigned>(heads), share < 1 ? 1 : share > 16 ? 16 : share),
+  return launch_overlapped(evict_shift_kernel<LANES>, dim3(static_cast<unsigned>(heads), share < 1 ? 1 : share > 64 ? 64 : share),
                            kShiftThreads, 0, stream, a);
 }
 
