@@ -9,14 +9,41 @@
 // A unit of work is 2 x 128 rows of one kv head, row = (token, query head of the
 // group), against the sequence's keys in tiles of 128: each of two softmax
 // warpgroups (thread = row) has 128 rows, both use the tile's K and V.  Scores
-// S = Q K^T and outputs O += P V in tensor memory, P over S as the second
-// product's first operand.  The tensor core alternates between the warpgroups:
-// while one takes its exponentials, the other's P V and next S are computed.
+// S = Q K^T and outputs O += P V in tensor memory, P as the second product's first
+// operand there.  The tensor core alternates between the warpgroups: while one
+// takes its exponentials, the other's P V and next S are computed.
 //   t = S c - mu, c = log2(e) / sqrt(d); p = 2^t, l += p
 // mu, the reference, is the row's maximum in log2 units; it is raised (and O and
 // l follow) only when a score passes it by kRaise, so p stays below 2^kRaise.
 // p is rounded to BF16, the type of V (the product's operands have one type); l
-// sums the unrounded p.
+// sums the unrounded p.  Relative to 64 bits the outputs are off by 0.0020 to
+// 0.0022 (2-norm; library products in BF16 with FP32 softmax: 0.0016 to 0.0017).
+//
+// Why this shape.  4 d operations a (row, key) for 2 bytes of K and of V that 128
+// rows share: bound by the tensor core.  128 rows are what an instruction of one
+// SM takes; two row tiles make one's exponentials hide behind the other's products
+// (four would need twice the tensor memory).  A tile of the group's query heads
+// (128 / G tokens of them) instead of one head reads K and V once for all of them.
+// Units are handed out one at a time, those with the most keys first, by a counter:
+// the causal triangle and mixed lengths make them uneven.
+//
+// Measured (one GB300, 1906 TFLOP/s for a short product, 1699 for seconds of it):
+// head dimension 128, 16384 tokens of 32 heads on 8: 1205 us = 1.83 PFLOP/s of the
+// causal half, 23 prompts of up to 2049 tokens 213 us (142 at the product's
+// rate), 4 prompts of up to 4097 tokens of 64 on 8 297 us (232); head dimension
+// 64, 3 prompts of up to 5003 tokens of 24 on 8 118 us (49).  A step (128
+// rows x 128 keys x 2 warpgroups) takes ~2550 cycles where the products alone would
+// take 2048; S reads both operands from shared memory at 128 bytes a cycle, which
+// makes it 77 cycles for 64.  A unit's first scores, last outputs and hand-over cost
+// ~2500 cycles more, which short prompts feel.  Head dimension 64 has half the
+// products for the same exponentials: there the softmax's chain (load, maximum, 128
+// exponentials a thread, store: ~1150 cycles a warpgroup) bounds it, at 38 % of the
+// tensor core's cycles.
+//
+// Measured and dropped: waits that spin without suspending (1571 for 1381 us, 16384
+// tokens); one warp for both warpgroups' products (1380 for 1324); outputs stored by a
+// warpgroup of its own (1235 for 1207); three places for row tiles (no change);
+// exponents formed before the exponentials' turn, head dimension 64 (120 for 118).
 #include <limits.h>
 
 #include <atomic>
@@ -163,7 +190,8 @@ struct Tmem {
 
 enum Bar : int {
   B_Q = 0, B_QFREE = 3, B_S = 6, B_TAKEN = 8, B_P = 10, B_PFREE = 12, B_O = 14, B_OFREE = 16, B_UNIT = 18, B_UNITFREE = 20,
-  B_KFULL = 22, B_KFREE = 26, B_VFULL = 30, B_VFREE = 34, B_END = 38, B_TURN = 40, B_COUNT = 42
+  B_KFULL = 22, B_KFREE = 26, B_VFULL = 30, B_VFREE = 34, B_END = 38, B_TURN = 40, B_EXP = 42,
+  B_COUNT = 44
 };
 
 // What the roles need to know of a unit: tokens t0 .. and the tiles of keys of
@@ -308,9 +336,10 @@ __device__ __forceinline__ void load_role(const PromptArgs &a, const CUtensorMap
 // and one elected lane issues, so that what the products take stays in uniform
 // registers.  Issuing takes as long as the products themselves, and the waits
 // between them several hundred cycles: with one warp for both warpgroups that time
-// was lost to the tensor core (16384 tokens 1380 us, now MEASURED).  The tiles of all units are one sequence: the next
-// S follows P V, or (P beside S) goes ahead of it, also from one unit to the next,
-// whose first S is there when the outputs of the one before are stored.
+// was lost to the tensor core (16384 tokens: 1380 us; two warps 1324, with all waits
+// before the turn 1228).  The tiles of all units are one sequence: the next S follows
+// P V, or (P beside S) goes ahead of it, also from one unit to the next, whose first S
+// is there when the outputs of the one before are stored.
 template <int D>
 __device__ __forceinline__ void product_role(const PromptArgs &a, uint32_t base, const InlineWaiter &wait, uint32_t tmem_addr,
                                              const int i, int lane) {
@@ -486,6 +515,25 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, const CUtensor
   Units units(wait, base + L::units);
   uint32_t ns = 0, no = 0;  // steps and units of this warpgroup so far
   const bool sender = (threadIdx.x & 127) == 0;  // of the warpgroup's outputs
+  // P beside S: the warpgroups take their exponentials in turns, the second half of
+  // one's with the first of the other's (left alone both fall into step and the
+  // products wait meanwhile: 128 us for 118; a turn that ends with the last
+  // exponential 119).  P over S: the products' turns keep them apart.
+  uint32_t turns = 0;
+  auto take_turn = [&]() {
+    wait(B_EXP + wg, (turns++ & 1) ^ (wg == 0 ? 1 : 0));
+    __syncwarp();
+  };
+  auto pass_turn = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&wait.bars[B_EXP + (wg ^ 1)]);
+  };
+  auto pass_turns = [&](int n) {
+    for (int j = 0; M::BESIDE && j < n; ++j) {
+      take_turn();
+      pass_turn();
+    }
+  };
   auto meet = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
   uint4 u = units.next();
   while (static_cast<int>(u.x) >= 0) {
@@ -493,6 +541,7 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, const CUtensor
     units.done(lane);
     const int tiles = wg ? w.tiles[1] : w.tiles[0], t = w.t0 + wg * step + rt;
     if (tiles == 0) {
+      pass_turns(w.all);
       u = units.next();
       continue;
     }
@@ -582,8 +631,10 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, const CUtensor
         }
         tmem_st16(to, p);
       };
+      if constexpr (M::BESIDE) take_turn();
       exponentials(w0, P);
       exponentials(w1, P + 16);
+      if constexpr (M::BESIDE) pass_turn();
       exponentials(w2, P + 32);
       exponentials(w3, P + 48);
       l += (s0 + s1) + (s2 + s3);
@@ -592,6 +643,7 @@ __device__ __forceinline__ void softmax_role(const PromptArgs &a, const CUtensor
       __syncwarp();
       if (lane == 0) mbar_arrive(&wait.bars[B_P + wg]);
     }
+    pass_turns(w.all - tiles);
     // ---- the rows' outputs, 64 channels at a time through shared memory and the copy
     // unit (stores of a lane for each row kept the warpgroup 1500 cycles longer from
     // its next unit); the last rows of a sequence, which are fewer, one by one
@@ -666,7 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // arrivals per phase: 4 for a warpgroup's warps, 2 for the products' warps, 11
     // for all that read a unit, else 1
     for (int i = lane; i < B_COUNT; i += 32) {
-      const bool four = (i >= B_TAKEN && i < B_TAKEN + 2) || (i >= B_P && i < B_P + 2) || (i >= B_OFREE && i < B_OFREE + 2);
+      const bool four = (i >= B_TAKEN && i < B_TAKEN + 2) || (i >= B_P && i < B_P + 2) || (i >= B_OFREE && i < B_OFREE + 2) ||
+                        (i >= B_EXP && i < B_EXP + 2);
       const bool two = (i >= B_KFREE && i < B_KFREE + 4) || (i >= B_VFREE && i < B_VFREE + 4);
       mbar_init(&bars[i], four ? 4 : two ? 2 : i >= B_UNITFREE && i < B_UNITFREE + 2 ? 11 : 1);
     }
