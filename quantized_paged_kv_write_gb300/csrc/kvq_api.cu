@@ -403,13 +403,13 @@ constexpr int32_t kMaxRowBlocks = 1 << 27;
 
 // The decode entry points with a caller workspace; k_new / v_new non-null
 // fuse the write of each sequence's new token (kvq_write_decode).
-// `weights` non-null adds up attention weights (kvq_weigh_decode).
+// `weights_stride` >= 0 adds up attention weights (kvq_weigh_decode).
 static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, const kvq_format *fmt,
                       kvq_caches caches, kvq_scales scales, const int32_t *block_tables,
                       int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t max_context_len,
                       float *out, void *workspace, size_t workspace_bytes, kvq_stream_t stream,
                       const void *k_new, const void *v_new, const void *res_k = nullptr,
-                      const void *res_v = nullptr, float *weights = nullptr, int64_t weights_stride = 0) {
+                      const void *res_v = nullptr, float *weights = nullptr, int64_t weights_stride = -1) {
   int kf = 0, vf = 0;
   int st = check_decode_shape(fmt, batch, num_q_heads, &kf, &vf);
   if (st != KVQ_OK) return st;
@@ -418,7 +418,8 @@ static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
     if (kf != K_INT8_CHAN && kf != K_INT2_CHAN) return KVQ_ERR_UNSUPPORTED;  // the tail belongs to per-channel K
     if (!res_k || !res_v || !aligned16(res_k) || !aligned16(res_v)) return KVQ_ERR_INVALID_ARG;
   }
-  if (weights != nullptr && (kf == K_INT8_CHAN || kf == K_INT2_CHAN)) return KVQ_ERR_UNSUPPORTED;
+  const bool weigh = weights_stride >= 0;
+  if (weigh && (kf == K_INT8_CHAN || kf == K_INT2_CHAN)) return KVQ_ERR_UNSUPPORTED;
   const bool fused = k_new != nullptr || v_new != nullptr;
   if (fused) {
     if (kf == K_INT8_CHAN || kf == K_INT2_CHAN) return KVQ_ERR_UNSUPPORTED;  // per-channel K blocks take no appends
@@ -440,7 +441,7 @@ static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
   const int H = fmt->num_kv_heads, D = fmt->head_dim, G = num_q_heads / H;
   DecodePlan plan;
   if (plan_decode(D, kf, vf, H, G, batch, fmt->rotation != 0, &plan) != cudaSuccess) return KVQ_ERR_CUDA;
-  if (weights != nullptr) {
+  if (weigh) {
     // the same split as the plain decode's, on kernels of their own
     DecodePlan own;
     if (plan_decode(D, kf, vf, H, G, batch, fmt->rotation != 0, &own, true) != cudaSuccess) return KVQ_ERR_CUDA;
@@ -449,7 +450,7 @@ static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
   }
   const WsLayout wl = ws_layout(batch, H, D, plan.max_ctas);
   const WeighWs ww = weigh_ws(wl, batch, num_q_heads, max_context_len);
-  if (workspace_bytes < (weights != nullptr ? ww.total : wl.total)) return KVQ_ERR_WORKSPACE;
+  if (workspace_bytes < (weigh ? ww.total : wl.total)) return KVQ_ERR_WORKSPACE;
   unsigned int *err = nullptr;
   if (error_word(&err) != cudaSuccess) return KVQ_ERR_CUDA;
 
@@ -499,13 +500,13 @@ static int run_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, co
     a.ks_w = scales.k_scale;
     a.vs_w = scales.v_scale;
   }
-  if (weights != nullptr) {
+  if (weigh) {
     a.ws_z = reinterpret_cast<float *>(ws + ww.z_off);
     a.ws_norm = reinterpret_cast<float2 *>(ws + ww.norm_off);
   }
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (launch_decode(D, kf, vf, a, plan, maps, s) != cudaSuccess) return KVQ_ERR_CUDA;
-  if (weights == nullptr) return KVQ_OK;
+  if (!weigh) return KVQ_OK;
   WeighArgs w;
   w.z = a.ws_z;
   w.norm = a.ws_norm;
@@ -570,7 +571,9 @@ int kvq_weigh_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, con
                      int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t max_context_len,
                      float *weights, int64_t weights_stride, float *out, void *workspace, size_t workspace_bytes,
                      kvq_stream_t stream) {
-  if (!weights || (reinterpret_cast<uintptr_t>(weights) & 3u) || weights_stride < max_context_len)
+  // (arrays without entries may be null)
+  if (weights_stride < 0 || weights_stride < max_context_len || (reinterpret_cast<uintptr_t>(weights) & 3u) ||
+      (!weights && batch > 0 && weights_stride > 0))
     return KVQ_ERR_INVALID_ARG;
   return run_decode(q_bf16, batch, num_q_heads, fmt, caches, scales, block_tables, max_blocks_per_seq,
                     context_lens, max_context_len, out, workspace, workspace_bytes, stream, nullptr, nullptr,
@@ -797,7 +800,7 @@ int kvq_evict_tokens(const int32_t *keep_lens, const int32_t *recent_lens, const
   if (max_blocks_per_seq < 1) return KVQ_ERR_INVALID_ARG;
   if (!table_fits(num_rows, max_blocks_per_seq) || fmt->num_blocks >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   if (num_rows == 0) return KVQ_OK;
-  if (!keep_lens || !recent_lens || !context_lens || !block_tables || !weights || !kept_lens || !workspace ||
+  if (!keep_lens || !recent_lens || !context_lens || !block_tables || (!weights && max_positions > 0) || !kept_lens || !workspace ||
       !caches.k_cache || !caches.v_cache || !scales.k_scale || !scales.v_scale)
     return KVQ_ERR_INVALID_ARG;
   if (!aligned4(keep_lens) || !aligned4(recent_lens) || !aligned4(pinned_lens) || !aligned4(context_lens) ||
@@ -894,20 +897,17 @@ int kvq_prompt_attention(const void *q_bf16, int64_t q_stride, const void *k_bf1
   if (num_seqs == 0 || num_tokens == 0 || max_seq_len == 0) return KVQ_OK;
   if (!q_bf16 || !k_bf16 || !v_bf16 || !seq_offsets || !out_bf16 || !workspace) return KVQ_ERR_INVALID_ARG;
   if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) ||
-      (reinterpret_cast<uintptr_t>(out_bf16) & 31u) || !aligned4(seq_offsets) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+      (reinterpret_cast<uintptr_t>(out_bf16) & 31u) || !aligned4(seq_offsets) || !aligned4(lse) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return KVQ_ERR_INVALID_ARG;
   const int G = num_q_heads / num_kv_heads;
+  // (no sequence is longer than the tokens: a loose bound costs nothing)
+  max_seq_len = static_cast<int32_t>(std::min<int64_t>(max_seq_len, num_tokens));
   const PromptWs wl = prompt_ws(num_seqs, max_seq_len, G);
   if (workspace_bytes < wl.total) return KVQ_ERR_WORKSPACE;
   PromptArgs a;
   if (error_word(&a.err) != cudaSuccess) return KVQ_ERR_CUDA;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  a.q = static_cast<const uint16_t *>(q_bf16);
-  a.k = static_cast<const uint16_t *>(k_bf16);
-  a.v = static_cast<const uint16_t *>(v_bf16);
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
   a.offsets = seq_offsets;
   a.out = static_cast<uint16_t *>(out_bf16);
   a.lse = lse;

@@ -208,8 +208,6 @@ struct PromptHead {
   int next;                    // the first one that no CTA has taken
 };
 struct PromptArgs {
-  const uint16_t *q, *k, *v;   // BF16 [num_tokens, heads, D], tokens `stride` elements apart
-  int64_t q_stride, k_stride, v_stride;
   const int32_t *offsets;      // [num_seqs + 1]
   uint16_t *out;               // BF16 [num_tokens, Hq, D]
   float *lse;                  // [num_tokens, Hq] or null

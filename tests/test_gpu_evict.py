@@ -356,3 +356,33 @@ def test_a_budget_held_over_many_steps():
             for name, x in zip(("k_cache", "v_cache", "k_scale", "v_scale"), arrays):
                 assert np.array_equal(cache[name].cpu().numpy(), x), name
     assert int(pool["free_count"]) == nb - sum(-(-x // 16) for x in ctx.tolist())
+
+
+def test_no_rows_and_no_positions():
+    fmt, cache, oc, tables, gen = make("int8", "int8", 2, 64, [20, 5], seed=4)
+    q = torch.randn((2, 4, 64), generator=gen, device="cuda").to(torch.bfloat16)
+    none = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    assert kvq.kvq_weigh_decode(q[:0], fmt, cache, _i32(tables)[:0], _i32([]), 20, none(0, 2, 20)).shape == (0, 4, 64)
+    assert not kvq.kvq_weigh_decode(q, fmt, cache, _i32(tables), _i32([0, 0]), 0, none(2, 2, 0)).any()
+    args = (_i32(tables), fmt, cache)
+    assert kvq.kvq_evict_tokens(_i32([]), _i32([]), args[0][:0], fmt, cache, none(0, 2, 20), _i32([])).shape == (0,)
+    assert kvq.kvq_evict_tokens(_i32([3, 0]), _i32([0, 0]), *args, none(2, 2, 0), _i32([1, 1])).tolist() == [0, 0]
+    assert kvq.kvq_device_errors() == 0
+    assert kvq.kvq_evict_tokens(_i32([3, 0]), _i32([0, 5]), *args, none(2, 2, 0), _i32([1, 1])).tolist() == [0, 5]
+    assert kvq.kvq_device_errors() == kvq.DEVERR_CONTEXT_RANGE
+
+
+@pytest.mark.parametrize("rows,h,g,d", [(1, 8, 4, 128), (32, 8, 4, 128), (33, 8, 4, 128), (64, 8, 2, 64), (65, 8, 2, 64), (1, 1, 1, 64)])
+def test_few_and_many_rows_to_merge(rows, h, g, d):
+    """On either side of the rows that one warp each merges."""
+    rng = np.random.default_rng(rows)
+    ctx = [2500] + [int(x) for x in rng.integers(0, 200, rows - 1)]
+    fmt, cache, oc, tables, gen = make("fp8", "fp8", h, d, ctx, seed=rows)
+    q = torch.randn((rows, h * g, d), generator=gen, device="cuda").to(torch.bfloat16)
+    weights = torch.zeros((rows, h, 2500), device="cuda")
+    out = kvq.kvq_weigh_decode(q, fmt, cache, _i32(tables), _i32(ctx), 2500, weights)
+    assert torch.equal(out, kvq.kvq_paged_decode(q, fmt, cache, _i32(tables), _i32(ctx), 2500))
+    ref = oracle.paged_decode_fp64(oc, _bits(q), tables, np.array(ctx))
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert err.max() <= 2e-3 and (err <= 1e-2 * np.abs(ref))[np.abs(ref) >= 0.2].all()   # the decode's own bounds
+    check_weights(weights, np.zeros(weights.shape), oc, q, tables, ctx, fmt)

@@ -144,3 +144,12 @@ def test_the_binding_refuses_shapes():
                dict(recent_lens=i(2), pool=dict(ref_counts=i(5)))):
         with pytest.raises(ValueError):
             kvq.kvq_evict_tokens(i(2), i(2), i(2, 4), fmt, {}, f(2, 2, 64), **kw)
+
+
+def test_arrays_without_entries_may_be_null(lib):
+    assert weigh(lib, weights=None, batch=0) == 0
+    assert weigh(lib, weights=None, stride=0, longest=0) in (kvq.KVQ_ERR_CUDA, kvq.KVQ_ERR_WORKSPACE)   # without, with a GPU
+    assert weigh(lib, stride=-1, longest=-1) == kvq.KVQ_ERR_INVALID_ARG
+    assert weigh(lib, weights=None, stride=1, longest=0) == kvq.KVQ_ERR_INVALID_ARG
+    assert evict(lib, weights=None, positions=0) == kvq.KVQ_ERR_WORKSPACE
+    assert weigh(lib, _fmt(k_gran=2), stride=0, longest=0) == kvq.KVQ_ERR_UNSUPPORTED
