@@ -31,19 +31,20 @@
 // head dimension 128, 16384 tokens of 32 heads on 8: 1205 us = 1.83 PFLOP/s of the
 // causal half, 23 prompts of up to 2049 tokens 213 us (142 at the product's
 // rate), 4 prompts of up to 4097 tokens of 64 on 8 297 us (232); head dimension
-// 64, 3 prompts of up to 5003 tokens of 24 on 8 118 us (49).  A step (128
-// rows x 128 keys x 2 warpgroups) takes ~2550 cycles where the products alone would
-// take 2048; S reads both operands from shared memory at 128 bytes a cycle, which
-// makes it 77 cycles for 64.  A unit's first scores, last outputs and hand-over cost
-// ~2500 cycles more, which short prompts feel.  Head dimension 64 has half the
-// products for the same exponentials: there the softmax's chain (load, maximum, 128
-// exponentials a thread, store: ~1150 cycles a warpgroup) bounds it, at 38 % of the
-// tensor core's cycles.
+// 64, 3 prompts of up to 5003 tokens of 24 on 8 109 us (49).  A step (128
+// rows x 128 keys x 2 warpgroups) takes ~2550 cycles where the products alone take
+// 2048: the rest is the hand-over between products and softmax.  A unit's first
+// scores, last outputs and hand-over cost ~2500 cycles more, which short prompts feel.
+// Head dimension 64 has half the products for the same exponentials (a step's 1024
+// and 1150 cycles, each alone); a step takes ~2200: its parts, in a chain for either
+// warpgroup, overlap half.
 //
 // Measured and dropped: waits that spin without suspending (1571 for 1381 us, 16384
 // tokens); one warp for both warpgroups' products (1380 for 1324); outputs stored by a
 // warpgroup of its own (1235 for 1207); three places for row tiles (no change);
-// exponents formed before the exponentials' turn, head dimension 64 (120 for 118).
+// exponents formed before the exponentials' turn, head dimension 64 (120 for 118);
+// P handed over in halves there, so that P V overlaps the next exponentials (117.6
+// without turns, 130 with them, for 118).
 #include <limits.h>
 
 #include <atomic>
@@ -228,21 +229,37 @@ struct Units {
   }
 };
 
+// When a CTA takes its next unit.  Taken two ahead, the look-up is never waited for;
+// but where a CTA gets few units, those with the most keys first, some then have more
+// to do than others: there it is taken when the one before has kAhead tiles left to be
+// loaded (units of up to kShort tiles do not hide the look-up).  3 prompts of up to
+// 5003 tokens, head dimension 64, 5 units a CTA: 119 us two ahead, 108 late; 3 of 8000 of
+// 8 heads on 1, 5 a CTA: 140 and 102; 4 of up to 4097 of 64 on 8, 16 a CTA: 315 and 321;
+// the 23 of up to 2049, 19 a CTA: 216.5 and 219.5.
+constexpr int kAhead = 8, kShort = 2, kFewUnits = 12;
+__device__ __forceinline__ bool few_units(const PromptArgs &a) {
+  return a.ws_head->units <= kFewUnits * static_cast<int>(gridDim.x);
+}
+
 __device__ __forceinline__ void plan_role(const PromptArgs &a, uint32_t units, const InlineWaiter &wait, int lane) {
   const int total = a.ws_head->units;
+  const bool few = few_units(a);
+  int back = 2;
   for (int n = 0;; ++n) {
+    // the unit before last has been read, or (few) the last one nears its end
+    if (n >= back) wait(B_UNITFREE + ((n - back) & 1), ((n - back) >> 1) & 1);
     int x = 0;
     if (lane == 0) x = atomicAdd(&a.ws_head->next, 1);
     x = __shfl_sync(0xffffffffu, x, 0);
     const bool end = x >= total;
     Unit u = {-1, 0, 0, 0};
     if (!end) u = unit_at(a, x);
-    wait(B_UNITFREE + (n & 1), ((n >> 1) & 1) ^ 1);
     if (lane == 0) {
       sts128(units + 16 * (n & 1), u.start, u.len, u.t0, u.h);
       mbar_arrive(&wait.bars[B_UNIT + (n & 1)]);
     }
     if (end) return;
+    back = few && min(u.len, u.t0 + a.unit) > kShort * kTile ? 1 : 2;
   }
 }
 
@@ -260,6 +277,7 @@ __device__ __forceinline__ void load_role(const PromptArgs &a, const CUtensorMap
   using L = Smem<D>;
   const int step = a.unit / 2;
   const uint32_t qbytes = step * a.G * D * 2;
+  const int ahead = few_units(a) ? kAhead : INT_MAX;
   Units units(wait, base + L::units);
   int st = 0, qs = 0;             // places for K and V, and for row tiles
   uint32_t ph = 1, qp = 1;        // and their parities
@@ -267,9 +285,10 @@ __device__ __forceinline__ void load_role(const PromptArgs &a, const CUtensorMap
     const uint4 u = units.next();
     if (static_cast<int>(u.x) < 0) break;
     const Work w(u, step);
-    units.done(lane);
+    const int hand_back = max(0, w.all - ahead);
     const bool go = lane == 0 && !*wait.abort;  // (after a wait that ran out nobody reads: no further copies)
     for (int j = 0; j < w.all; ++j) {
+      if (j == hand_back) units.done(lane);
       wait(B_KFREE + st, ph);
       if (go) {
         mbar_arrive_expect_tx(&wait.bars[B_KFULL + st], L::TILE);
