@@ -584,16 +584,18 @@ cudaError_t select_with(const EvictArgs &a, int ctas, size_t bytes, cudaStream_t
 }
 
 cudaError_t select(const EvictArgs &a, int sms, cudaStream_t stream) {
-  const int64_t heads = static_cast<int64_t>(a.rows) * a.H;
-  // CTAs that hold all keys, and more where few rows leave SMs without work
+  // CTAs that hold all keys, and no more: where few rows leave SMs without work, more of
+  // them for a (row, head) still take longer (8 heads of 16384 positions: one 13 us,
+  // four 26; 32 heads of 32768: two 18, eight 54)
   int ctas = 1;
-  while (ctas < 8 && (a.stride > static_cast<int64_t>(ctas) * kHeld || (2 * ctas * heads <= 2 * sms && a.stride > 2048 * ctas)))
-    ctas *= 2;
+  while (ctas < 8 && a.stride > static_cast<int64_t>(ctas) * kHeld) ctas *= 2;
   const int64_t keys = (a.stride + ctas - 1) / ctas;
   if (keys > kHeld) return select_with<512, false, true>(a, ctas, 0, stream);
   const size_t bytes = 16 * (static_cast<size_t>(a.stride / 4 + 2 + ctas - 1) / ctas);  // vectors of any alignment
-  if (keys <= 8192)
-    return ctas == 1 ? select_with<256, true, false>(a, 1, bytes, stream) : select_with<256, true, true>(a, ctas, bytes, stream);
+  // Half as many threads for short rows, or where there are more of them than SMs hold
+  // (512 rows of 8192: 20.8 for 23.9 us, 400 of 4000 11.8 for 13.6; 8 of 8192 11.1 for 8.9)
+  if (keys <= 4096 || (keys <= 8192 && static_cast<int64_t>(a.rows) * a.H > 3 * sms))
+    return select_with<256, true, false>(a, 1, bytes, stream);
   return ctas == 1 ? select_with<512, true, false>(a, 1, bytes, stream) : select_with<512, true, true>(a, ctas, bytes, stream);
 }
 

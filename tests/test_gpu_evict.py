@@ -386,3 +386,14 @@ def test_few_and_many_rows_to_merge(rows, h, g, d):
     err = np.abs(out.double().cpu().numpy() - ref)
     assert err.max() <= 2e-3 and (err <= 1e-2 * np.abs(ref))[np.abs(ref) >= 0.2].all()   # the decode's own bounds
     check_weights(weights, np.zeros(weights.shape), oc, q, tables, ctx, fmt)
+
+
+@pytest.mark.parametrize("h,rows,length", [(8, 60, 8190), (8, 60, 4097), (8, 50, 4097), (2, 3, 4096), (1, 500, 8192), (1, 2, 40000), (2, 1, 16385)])
+def test_long_rows_among_few_and_many(h, rows, length):
+    """Either number of threads, on both sides of their bounds."""
+    rng = np.random.default_rng(length + rows)
+    w = (rng.random((rows, h, length)) ** 5).astype(np.float32)
+    w[:, :, ::7] = 0.25
+    ctx = [length] + [int(x) for x in rng.integers(0, 40, rows - 1)]
+    keep = [n // 3 for n in ctx]
+    Both("int8", "int8", h, 64, ctx, seed=8, weights=w).evict(keep, [n // 5 for n in keep], [n // 9 for n in keep])
