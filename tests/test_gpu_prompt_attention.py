@@ -232,3 +232,17 @@ def test_the_same_call_gives_the_same_bits():
     for _ in range(3):
         again = attend(q, k, v, offsets)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_sequence_gives_the_same_bits_in_any_batch(d):
+    """Among thousands of units, which are taken ahead, and alone, where few are taken late."""
+    lengths = [int(x) for x in np.random.default_rng(d).integers(1, 900, 60)] + [5000]
+    offsets = np.concatenate([[0], np.cumsum(lengths)]).tolist()
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    q, k, v = (_draw(gen, offsets[-1], h, d) for h in (64, 8, 8))
+    out, lse = attend(q, k, v, offsets)
+    for s in [0, 7, 33, 59, 60]:
+        a, b = offsets[s], offsets[s + 1]
+        alone = attend(q[a:b], k[a:b], v[a:b], [0, b - a])
+        assert torch.equal(alone[0], out[a:b]) and torch.equal(alone[1], lse[a:b])
