@@ -16,13 +16,13 @@
 // read: selection, the moves of the older tokens (into places that evicted ones
 // left), the shift of the last w (into places that moved ones left).  One kernel that
 // did all three for a (row, head) in turn took 298, 132 and 124 us where these take
-// 241, 110 and 68 (the three cases below): its passes wait for one another's latency
+// 241, 110 and 65 (the three cases below): its passes wait for one another's latency
 // with the whole SM.
 // 27 x 8 heads, 32768 tokens to 16384 (FP8): select 35 us, move 179, shift 17.  The
 // moves are of 256 bytes a token in two places, its scales and its weight 4 bytes each
 // in sectors of 32: 352 bytes of traffic for 268, near the memory's rate.
 // 256 x 8 heads, ~4160 tokens to 4096 (INT8), the last 256 shifted: 35, 10 and 53 us
-// (the shift's bytes alone: 42).  8 x 8 heads, 65536 to 8192 (INT4): 26, 27 and 9.
+// (the shift's bytes alone: 42).  8 x 8 heads, 65536 to 8192 (INT4): 24, 27 and 9.
 #include <atomic>
 #include <type_traits>
 
@@ -52,7 +52,7 @@ __device__ __forceinline__ unsigned order_of(float x) {
 // tokens a head, clusters of two) the reading pass takes 9000, a search of a
 // histogram 3000 to 3800 (three), the other two counts 3000 each, the lists 8500.
 constexpr int kBins = 2048;
-constexpr int kHeld = 16384;  // keys that a CTA holds at most: 64 KB, three CTAs an SM
+constexpr int kHeld = 16384;  // keys that 512 threads hold at most: 64 KB, three CTAs an SM (1024: twice that)
 
 __device__ __forceinline__ unsigned cluster_rank() {
   unsigned x;
@@ -250,13 +250,13 @@ __global__ void __launch_bounds__(T, 1536 / T) evict_select_kernel(const EvictAr
       }
       sync_all<CLUSTER>();
       // digits from the largest: the one in which the need-th lies
-      constexpr int PER = kBins / T;
+      constexpr int SEARCH = T < 512 ? T : 512, PER = kBins / SEARCH;  // (by the first 512 threads)
       static_assert(PER % 4 == 0, "whole vectors of bins");
       const int b0 = kBins - (tid + 1) * PER;
       unsigned bin[PER], own = 0;
 #pragma unroll
       for (int k = 0; k < PER; ++k) bin[k] = 0;
-      for (int j = 0; j < (CLUSTER ? ctas : 1); ++j)
+      for (int j = 0; j < (tid < SEARCH ? CLUSTER ? ctas : 1 : 0); ++j)
 #pragma unroll
         for (int k = 0; k < PER; k += 4) {
           const uint4 y = CLUSTER ? remote128(smem_u32(hist + b0 + k), j) : *reinterpret_cast<const uint4 *>(hist + b0 + k);
@@ -565,7 +565,8 @@ cudaError_t select_with(const EvictArgs &a, int ctas, size_t bytes, cudaStream_t
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   static std::atomic<unsigned long long> done{0};  // devices whose limit is raised
   if (HELD && !((done.load(std::memory_order_acquire) >> dev) & 1ull)) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * (kHeld / 4 + 2))) != cudaSuccess)
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  16 * ((T > 512 ? 2 : 1) * kHeld / 4 + 2))) != cudaSuccess)
       return e;
     done.fetch_or(1ull << dev, std::memory_order_acq_rel);
   }
@@ -589,12 +590,22 @@ cudaError_t select(const EvictArgs &a, int sms, cudaStream_t stream) {
   // four 26; 32 heads of 32768: two 18, eight 54)
   int ctas = 1;
   while (ctas < 8 && a.stride > static_cast<int64_t>(ctas) * kHeld) ctas *= 2;
+  // Where SMs would hold two or three of a cluster's CTAs, half as many of twice the
+  // threads and keys, if that is one an SM (64 heads of 65536: 31 and 25 us, 144 of 32768
+  // 26 and 21, 32 of 120000 48 and 27; not where there is an SM for each as it is:
+  // 32 of 60000 21 and 24)
+  const int64_t heads = static_cast<int64_t>(a.rows) * a.H;
+  const int half = ctas / 2;
+  if (half > 0 && a.stride <= int64_t{2} * half * kHeld && heads * ctas > sms && heads * half <= sms) {
+    const size_t bytes = 16 * (static_cast<size_t>(a.stride / 4 + 2 + half - 1) / half);
+    return half == 1 ? select_with<1024, true, false>(a, 1, bytes, stream) : select_with<1024, true, true>(a, half, bytes, stream);
+  }
   const int64_t keys = (a.stride + ctas - 1) / ctas;
   if (keys > kHeld) return select_with<512, false, true>(a, ctas, 0, stream);
   const size_t bytes = 16 * (static_cast<size_t>(a.stride / 4 + 2 + ctas - 1) / ctas);  // vectors of any alignment
   // Half as many threads for short rows, or where there are more of them than SMs hold
   // (512 rows of 8192: 20.8 for 23.9 us, 400 of 4000 11.8 for 13.6; 8 of 8192 11.1 for 8.9)
-  if (keys <= 4096 || (keys <= 8192 && static_cast<int64_t>(a.rows) * a.H > 3 * sms))
+  if (keys <= 4096 || (keys <= 8192 && heads > 3 * sms))
     return select_with<256, true, false>(a, 1, bytes, stream);
   return ctas == 1 ? select_with<512, true, false>(a, 1, bytes, stream) : select_with<512, true, true>(a, ctas, bytes, stream);
 }

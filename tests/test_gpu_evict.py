@@ -397,3 +397,14 @@ def test_long_rows_among_few_and_many(h, rows, length):
     ctx = [length] + [int(x) for x in rng.integers(0, 40, rows - 1)]
     keep = [n // 3 for n in ctx]
     Both("int8", "int8", h, 64, ctx, seed=8, weights=w).evict(keep, [n // 5 for n in keep], [n // 9 for n in keep])
+
+
+@pytest.mark.parametrize("h,rows,length", [(8, 18, 20001), (8, 18, 32768), (8, 8, 40003), (8, 8, 65536), (8, 4, 70002)])
+def test_long_rows_that_share_the_sms(h, rows, length):
+    """Selections by CTAs of 1024 threads, one and clusters of two and four."""
+    rng = np.random.default_rng(length)
+    w = rng.integers(0, 50, (rows, h, length)).astype(np.float32)
+    ctx = [int(x) for x in rng.integers(0, 60, rows)]
+    ctx[rows // 2] = length - 1
+    keep = [n // 2 for n in ctx]
+    Both("int8", "int8", h, 64, ctx, seed=9, weights=w, length=length).evict(keep, [n // 6 for n in keep], [n // 8 for n in keep])
