@@ -9,7 +9,7 @@
 // Why the scores and not K again: a token and kv head has 4 G bytes of scores,
 // written once and read once, against d bytes of codes and all of the decode's
 // products.  27 sequences of 32768 tokens, 32 heads on 8, FP8: the split takes
-// 309 us with the scores (286 without: 113 MB more), the weights 26 us (170 MB,
+// 309 us with the scores (278 without: 113 MB more), the weights 26 us (170 MB,
 // 6.4 TB/s) and the reduce 7.  What the decode reads bounds the call: 343 us where
 // its bytes and the weights' take 285.  The split with scores is a kernel of its
 // own: a run-time branch slowed the plain decode by up to 4.5 %.
