@@ -550,8 +550,9 @@ int kvq_weigh_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, con
  * A negative length or a context past max_positions or the table sets
  * KVQ_DEVERR_CONTEXT_RANGE, a block id outside [0, num_blocks) among the row's
  * KVQ_DEVERR_BLOCK_RANGE, a shared block KVQ_DEVERR_POOL_STATE; the row is left
- * as it is.  Blocks [p / 16, (k + 15) / 16) are written.  Rows must not share the
- * blocks that are written (ref_counts checks it).  num_rows <= 8192, max_positions
+ * as it is.  Blocks [p / 16, (k + 15) / 16) count as written whatever the weights,
+ * none of them where p = k.  Rows must not share the blocks that are written
+ * (ref_counts checks it).  num_rows <= 8192, max_positions
  * <= 2^30 and table sizes as kvq_assign_blocks; num_rows == 0 is a no-op.
  */
 int kvq_evict_workspace_size(int32_t num_rows, int32_t num_kv_heads, int32_t max_positions,

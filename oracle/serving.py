@@ -89,7 +89,7 @@ def evict_tokens(keep, recent, pinned, context_lens, tables, arrays, weights, re
         ids = [int(x) for x in tables[r, :-(-n // BLOCK)]]
         if any(x not in range(num_blocks) for x in ids):
             continue
-        if refs is not None and any(refs[x] != 1 for x in ids[p // BLOCK:-(-k // BLOCK)]):
+        if refs is not None and p < k and any(refs[x] != 1 for x in ids[p // BLOCK:-(-k // BLOCK)]):
             continue
         kept[r] = k
         for h in range(heads):

@@ -194,7 +194,9 @@ __global__ void __launch_bounds__(T, 1536 / T) evict_select_kernel(const EvictAr
     else each(of_weights, f);
   };
   for (int i = tid; i < kBins; i += T) hist[i] = 0;
-  // every block of the row, and nobody else's among those to be written
+  // every block of the row, and nobody else's among those to be written (none where
+  // all that stays is pinned)
+  const int written = p < keep ? keep : 0;
   const int32_t *table = a.tables + static_cast<int64_t>(r) * a.max_blocks;
   bool bad = false, shared = false;
   // (eight of a thread in flight: one by one they took longer than the passes below)
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(T, 1536 / T) evict_select_kernel(const EvictAr
       const int i = base + c * T;
       if (i >= blocks) break;
       if (id[c] < 0 || id[c] >= a.num_blocks) bad = true;
-      else if (a.refs != nullptr && i >= p / kBlockSize && i * kBlockSize < keep) shared = shared || __ldg(a.refs + id[c]) != 1;
+      else if (a.refs != nullptr && i >= p / kBlockSize && i * kBlockSize < written) shared = shared || __ldg(a.refs + id[c]) != 1;
     }
   }
   bad = __syncthreads_or(bad);
