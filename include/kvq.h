@@ -472,9 +472,10 @@ int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads,
  * sequence may hold anything.  Rows of out and lse outside every sequence are
  * left as they were.
  *
- * seq_offsets out of order or range set KVQ_DEVERR_GROUP_RANGE, and nothing is
- * written; a sequence longer than max_seq_len sets KVQ_DEVERR_CONTEXT_RANGE and
- * its rows are left as they were.  num_seqs <= 8192, num_tokens, max_seq_len and
+ * seq_offsets out of order or range set KVQ_DEVERR_GROUP_RANGE and nothing else,
+ * and nothing is written; a sequence longer than max_seq_len sets
+ * KVQ_DEVERR_CONTEXT_RANGE and its rows are left as they were.  num_seqs,
+ * num_tokens or max_seq_len of 0 is a no-op, which checks no offsets.  num_seqs <= 8192, num_tokens, max_seq_len and
  * strides <= 2^24, else KVQ_ERR_UNSUPPORTED; num_kv_heads 1 to 8, ratio 1 to 8,
  * head_dim 64 or 128, as in the cache.  Strides are multiples of 8.
  */

@@ -75,7 +75,6 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptA
   for (int s = threadIdx.x; s < a.num_seqs; s += kPlanThreads) {
     const int x = __ldg(a.offsets + s), y = __ldg(a.offsets + s + 1);
     order = order && x >= 0 && y >= x && y <= a.num_tokens;
-    if (y >= x && y - x > a.max_seq) set_error(a.err, KVQ_DEVERR_CONTEXT_RANGE);
   }
   for (int j = threadIdx.x; j <= a.levels; j += kPlanThreads) a.ws_level[j] = 0;
   const bool none = __syncthreads_or(!order);
@@ -87,15 +86,18 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptA
     }
     return;
   }
-  // how many sequences have j tiles
+  // how many sequences have j tiles (a sequence longer than announced: none)
   auto tiles = [&](int s, int *start, int *len) {
     const int x = __ldg(a.offsets + s), y = __ldg(a.offsets + s + 1);
     *start = x;
-    *len = y - x > a.max_seq ? 0 : y - x;
-    return (*len + a.unit - 1) / a.unit;
+    *len = y - x;
+    return *len > a.max_seq ? 0 : (*len + a.unit - 1) / a.unit;
   };
   int start, len;
-  for (int s = threadIdx.x; s < a.num_seqs; s += kPlanThreads) atomicAdd(a.ws_level + tiles(s, &start, &len), 1);
+  for (int s = threadIdx.x; s < a.num_seqs; s += kPlanThreads) {
+    atomicAdd(a.ws_level + tiles(s, &start, &len), 1);
+    if (len > a.max_seq) set_error(a.err, KVQ_DEVERR_CONTEXT_RANGE);
+  }
   __syncthreads();
   // from the top: sequences with more than j tiles (where those with j go), and
   // units before level j
