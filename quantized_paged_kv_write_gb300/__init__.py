@@ -287,6 +287,14 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _int32(x, what: str) -> int:
+    """A length or count for the C ABI's 32 bits (ctypes would keep the low ones)."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{what} does not fit in 32 bits: {x}")
+    return x
+
+
 def _caches(c: dict) -> tuple:
     return (_Caches(_ptr(c["k_cache"], torch.uint8, "k_cache"), _ptr(c["v_cache"], torch.uint8, "v_cache")),
             _Scales(_ptr(c["k_scale"], torch.float32, "k_scale"), _ptr(c["v_scale"], torch.float32, "v_scale")))
@@ -641,7 +649,8 @@ def _rows(t: torch.Tensor, what: str) -> tuple:
 def kvq_prompt_attention_workspace_size(num_seqs: int, max_seq_len: int, num_q_heads: int, num_kv_heads: int) -> int:
     lib = load_library()
     out = ctypes.c_size_t(0)
-    st = lib.kvq_prompt_attention_workspace_size(int(num_seqs), int(max_seq_len), int(num_q_heads), int(num_kv_heads),
+    st = lib.kvq_prompt_attention_workspace_size(_int32(num_seqs, "num_seqs"), _int32(max_seq_len, "max_seq_len"),
+                                                 _int32(num_q_heads, "num_q_heads"), _int32(num_kv_heads, "num_kv_heads"),
                                                  ctypes.byref(out))
     if st != KVQ_OK:
         raise KvqError(st, "kvq_prompt_attention_workspace_size")
@@ -663,7 +672,8 @@ def kvq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_
     hkv = int(k.shape[1])
     if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
         raise ValueError("seq_offsets must be [S + 1]")
-    seqs = int(seq_offsets.shape[0]) - 1
+    seqs = _int32(seq_offsets.shape[0] - 1, "the number of sequences")
+    max_seq_len = _int32(max_seq_len, "max_seq_len")
     if out is None:
         out = _empty((n, hq, d), torch.bfloat16, q.device, stream)
     elif tuple(out.shape) != (n, hq, d):
@@ -675,7 +685,7 @@ def kvq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_
         workspace = _empty(max(nbytes, 256), torch.uint8, q.device, stream)
     (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
     st = lib.kvq_prompt_attention(qp, qs, kp, ks, vp, vs, _ptr(seq_offsets, torch.int32, "seq_offsets"), seqs, n,
-                                  int(max_seq_len), hq, hkv, d, _ptr(out, torch.bfloat16, "out"),
+                                  max_seq_len, hq, hkv, d, _ptr(out, torch.bfloat16, "out"),
                                   None if lse is None else _ptr(lse, torch.float32, "lse"),
                                   _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream))
     if st != KVQ_OK:
@@ -687,8 +697,8 @@ def kvq_weigh_decode_workspace_size(fmt: CacheFormat, batch: int, num_q_heads: i
     lib = load_library()
     out = ctypes.c_size_t(0)
     cf = fmt.as_c()
-    st = lib.kvq_weigh_decode_workspace_size(ctypes.byref(cf), int(batch), int(num_q_heads), int(max_context_len),
-                                             ctypes.byref(out))
+    st = lib.kvq_weigh_decode_workspace_size(ctypes.byref(cf), _int32(batch, "batch"), _int32(num_q_heads, "num_q_heads"),
+                                             _int32(max_context_len, "max_context_len"), ctypes.byref(out))
     if st != KVQ_OK:
         raise KvqError(st, "kvq_weigh_decode_workspace_size")
     return int(out.value)
@@ -709,6 +719,7 @@ def kvq_weigh_decode(q: torch.Tensor, fmt: CacheFormat, cache: dict, block_table
         raise ValueError("block_tables must be [B, max_blocks] and context_lens [B]")
     if weights.dim() != 3 or tuple(weights.shape[:2]) != (bsz, fmt.num_kv_heads):
         raise ValueError("weights must be [B, H_kv, positions]")
+    width, max_context_len = _int32(block_tables.shape[1], "max_blocks"), _int32(max_context_len, "max_context_len")
     if out is None:
         out = _empty((bsz, hq, d), torch.float32, q.device, stream)
     elif tuple(out.shape) != (bsz, hq, d):
@@ -716,14 +727,14 @@ def kvq_weigh_decode(q: torch.Tensor, fmt: CacheFormat, cache: dict, block_table
     cf = fmt.as_c()
     if workspace is None:
         need = ctypes.c_size_t(0)
-        st = lib.kvq_weigh_decode_workspace_size(ctypes.byref(cf), bsz, hq, int(max_context_len), ctypes.byref(need))
+        st = lib.kvq_weigh_decode_workspace_size(ctypes.byref(cf), bsz, hq, max_context_len, ctypes.byref(need))
         if st != KVQ_OK:
             raise KvqError(st, "kvq_weigh_decode")
         workspace = _empty(max(need.value, 256), torch.uint8, q.device, stream)
     caches, scales = _caches(cache)
     st = lib.kvq_weigh_decode(_ptr(q, torch.bfloat16, "q"), bsz, hq, ctypes.byref(cf), caches, scales,
-                              _ptr(block_tables, torch.int32, "block_tables"), int(block_tables.shape[1]),
-                              _ptr(context_lens, torch.int32, "context_lens"), int(max_context_len),
+                              _ptr(block_tables, torch.int32, "block_tables"), width,
+                              _ptr(context_lens, torch.int32, "context_lens"), max_context_len,
                               _ptr(weights, torch.float32, "weights"), int(weights.shape[2]),
                               _ptr(out, torch.float32, "out"), _ptr(workspace, torch.uint8, "workspace"),
                               int(workspace.numel()), _stream(stream))
@@ -735,7 +746,8 @@ def kvq_weigh_decode(q: torch.Tensor, fmt: CacheFormat, cache: dict, block_table
 def kvq_evict_workspace_size(num_rows: int, num_kv_heads: int, max_positions: int) -> int:
     lib = load_library()
     out = ctypes.c_size_t(0)
-    st = lib.kvq_evict_workspace_size(int(num_rows), int(num_kv_heads), int(max_positions), ctypes.byref(out))
+    st = lib.kvq_evict_workspace_size(_int32(num_rows, "num_rows"), _int32(num_kv_heads, "num_kv_heads"),
+                                      _int32(max_positions, "max_positions"), ctypes.byref(out))
     if st != KVQ_OK:
         raise KvqError(st, "kvq_evict_workspace_size")
     return int(out.value)
@@ -752,7 +764,7 @@ def kvq_evict_tokens(keep_lens: torch.Tensor, context_lens: torch.Tensor, block_
     pool's counts show blocks that other rows use.  Returns kept_lens int32 [R],
     what kvq_release_blocks takes to give the freed blocks back."""
     lib = load_library()
-    rows = int(keep_lens.shape[0])
+    rows = _int32(keep_lens.shape[0], "the number of rows")
     for t, what in ((keep_lens, "keep_lens"), (recent_lens, "recent_lens"), (pinned_lens, "pinned_lens"),
                     (context_lens, "context_lens"), (kept_lens, "kept_lens")):
         if t is not None and t.shape != (rows,):
@@ -761,7 +773,7 @@ def kvq_evict_tokens(keep_lens: torch.Tensor, context_lens: torch.Tensor, block_
         raise ValueError("block_tables must be [R, max_blocks]")
     if weights.dim() != 3 or tuple(weights.shape[:2]) != (rows, fmt.num_kv_heads):
         raise ValueError("weights must be [R, H_kv, positions]")
-    positions = int(weights.shape[2])
+    width, positions = _int32(block_tables.shape[1], "max_blocks"), _int32(weights.shape[2], "positions")
     refs = None
     if pool is not None:
         if int(pool["ref_counts"].numel()) != fmt.num_blocks:
@@ -777,7 +789,7 @@ def kvq_evict_tokens(keep_lens: torch.Tensor, context_lens: torch.Tensor, block_
     st = lib.kvq_evict_tokens(_ptr(keep_lens, torch.int32, "keep_lens"), _ptr(recent_lens, torch.int32, "recent_lens"),
                               None if pinned_lens is None else _ptr(pinned_lens, torch.int32, "pinned_lens"), rows,
                               _ptr(context_lens, torch.int32, "context_lens"),
-                              _ptr(block_tables, torch.int32, "block_tables"), int(block_tables.shape[1]),
+                              _ptr(block_tables, torch.int32, "block_tables"), width,
                               ctypes.byref(cf), caches, scales, refs, _ptr(weights, torch.float32, "weights"), positions,
                               _ptr(kept_lens, torch.int32, "kept_lens"), _ptr(workspace, torch.uint8, "workspace"),
                               int(workspace.numel()), _stream(stream))
