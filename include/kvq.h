@@ -467,9 +467,10 @@ int kvq_prefix_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads,
  * sequence up to its own; query head h reads kv head h / (num_q_heads /
  * num_kv_heads).  Products of BF16 operands accumulate in FP32; scores, softmax
  * statistics and partial outputs are FP32; a probability is rounded to BF16 once
- * (relative to its row's largest so far) and the output once.  A sequence's
- * values must be finite; tokens of other sequences and rows outside every
- * sequence may hold anything.  Rows of out and lse outside every sequence are
+ * (relative to a reference that may lie up to a factor 2^6 below its row's largest
+ * so far) and the output once.  A sequence's values must be finite, and its scores
+ * finite in FP32; tokens of other sequences and rows outside every sequence may
+ * hold anything.  out and lse must not overlap the inputs.  Rows of out and lse outside every sequence are
  * left as they were.
  *
  * seq_offsets out of order or range set KVQ_DEVERR_GROUP_RANGE and nothing else,
@@ -508,6 +509,12 @@ int kvq_prompt_attention(const void *q_bf16, int64_t q_stride, const void *k_bf1
  * add nothing.  A token's weight starts at what its entry holds when the token
  * is appended: 0 after an eviction; a row that begins anew, or whose last tokens
  * were taken back without an eviction, has its entries cleared by the caller.
+ * Weights come from decode steps alone: what a prompt's tokens attend to
+ * (kvq_prompt_attention) adds nothing, so an eviction right behind a prompt finds
+ * equal weights and keeps the lowest positions.
+ * The workspace holds 4 bytes a query head for each of batch * max_context_len
+ * positions, however short the contexts are: give the longest context, not the
+ * model's limit (256 rows, 32 heads and a bound of 131072: 4.3 GB).
  */
 int kvq_weigh_decode_workspace_size(const kvq_format *fmt, int32_t batch, int32_t num_q_heads,
                                     int32_t max_context_len, size_t *bytes);
@@ -538,6 +545,11 @@ int kvq_weigh_decode(const void *q_bf16, int32_t batch, int32_t num_q_heads, con
  *                 kvq_release_blocks to follow
  *   workspace     device buffer of at least kvq_evict_workspace_size() bytes,
  *                 256-byte aligned
+ *
+ * Time and workspace follow max_positions, not the lengths in context_lens, which
+ * the host does not see: keep weights about as wide as the longest row (256 rows of
+ * ~4160 tokens and 8 heads: 103 us and 34 MB with weights 4160 wide, 188 us and
+ * 268 MB with 32768, 1.26 ms and 1.1 GB with 131072).
  *
  * Each kv head keeps, besides those p and w, the k - w - p heaviest of the tokens
  * [p, n - w): by weight, ties to the lower position; NaN counts as the heaviest.

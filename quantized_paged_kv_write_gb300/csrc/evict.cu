@@ -22,7 +22,8 @@
 // moves are of 256 bytes a token in two places, its scales and its weight 4 bytes each
 // in sectors of 32: 352 bytes of traffic for 268, near the memory's rate.
 // 256 x 8 heads, ~4160 tokens to 4096 (INT8), the last 256 shifted: 35, 10 and 53 us
-// (the shift's bytes alone: 42).  8 x 8 heads, 65536 to 8192 (INT4): 24, 27 and 9.
+// (the shift's bytes alone: 42).  8 x 8 heads, 65536 to 8192 (INT4): 24, 27 and 9; of
+// the moves' 27 the sectors alone take ~15, of the shift's 9 the bytes 2.
 #include <atomic>
 #include <type_traits>
 
@@ -587,9 +588,12 @@ cudaError_t select_with(const EvictArgs &a, int ctas, size_t bytes, cudaStream_t
 }
 
 cudaError_t select(const EvictArgs &a, int sms, cudaStream_t stream) {
-  // CTAs that hold all keys, and no more: where few rows leave SMs without work, more of
+  // CTAs that hold the keys of a row as long as the weights are wide (the host does not
+  // see the rows' lengths), and no more: where few rows leave SMs without work, more of
   // them for a (row, head) still take longer (8 heads of 16384 positions: one 13 us,
-  // four 26; 32 heads of 32768: two 18, eight 54)
+  // four 26; 32 heads of 32768: two 18, eight 54).  Weights much wider than the rows
+  // cost the same surplus (256 x 8 heads of ~4160 tokens, the three kernels: 103 us
+  // with 4160 positions, 104 with 8192, 117 with 16384, 188 with 32768, 1260 with 131072)
   int ctas = 1;
   while (ctas < 8 && a.stride > static_cast<int64_t>(ctas) * kHeld) ctas *= 2;
   // Where SMs would hold two or three of a cluster's CTAs, half as many of twice the

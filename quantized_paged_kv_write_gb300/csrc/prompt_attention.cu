@@ -16,25 +16,29 @@
 // mu, the reference, is the row's maximum in log2 units; it is raised (and O and
 // l follow) only when a score passes it by kRaise, so p stays below 2^kRaise.
 // p is rounded to BF16, the type of V (the product's operands have one type); l
-// sums the unrounded p.  Relative to 64 bits the outputs are off by 0.0020 to
-// 0.0022 (2-norm; library products in BF16 with FP32 softmax: 0.0016 to 0.0017).
+// sums the unrounded p.  Relative to 64 bits the outputs are off by 0.0018 to
+// 0.0021 (2-norm; all in FP32 and rounded once: 0.0015 to 0.0016).
 //
 // Why this shape.  4 d operations a (row, key) for 2 bytes of K and of V that 128
 // rows share: bound by the tensor core.  128 rows are what an instruction of one
 // SM takes; two row tiles make one's exponentials hide behind the other's products
-// (four would need twice the tensor memory).  A tile of the group's query heads
+// (four would need twice the tensor memory with keys in tiles of 128; in tiles of 64,
+// with P over S, four would fit for head dimension 64: not built).  A tile of the group's query heads
 // (128 / G tokens of them) instead of one head reads K and V once for all of them.
 // Units are handed out one at a time, those with the most keys first, by a counter:
 // the causal triangle and mixed lengths make them uneven.
 //
-// Measured (one GB300, 1906 TFLOP/s for a short product, 1699 for seconds of it):
-// head dimension 128, 16384 tokens of 32 heads on 8: 1205 us = 1.83 PFLOP/s of the
-// causal half, 23 prompts of up to 2049 tokens 213 us (142 at the product's
-// rate), 4 prompts of up to 4097 tokens of 64 on 8 297 us (232); head dimension
-// 64, 3 prompts of up to 5003 tokens of 24 on 8 109 us (49).  A step (128
+// Measured (one GB300, 1906 TFLOP/s for a short product, 1699 for seconds of it; a few
+// calls after a rest): head dimension 128, 16384 tokens of 32 heads on 8: 1207 us =
+// 1.82 PFLOP/s of the causal half, 23 prompts of up to 2049 tokens 219 us (142 at
+// the product's rate), 4 prompts of up to 4097 tokens of 64 on 8 290 us (232); head
+// dimension 64, 3 prompts of up to 5003 tokens of 24 on 8 104 us (49).  Calls for
+// seconds meet the power limit: 1385, 231, 322 and 104 us.  A step (128
 // rows x 128 keys x 2 warpgroups) takes ~2550 cycles where the products alone take
 // 2048: the rest is the hand-over between products and softmax.  A unit's first
-// scores, last outputs and hand-over cost ~2500 cycles more, which short prompts feel.
+// scores, last outputs and hand-over cost ~2500 cycles more, which short prompts feel
+// (steps and unit ends make ~175 of the 23 prompts' 219 us; where the rest goes, the
+// plan, look-ups, the last CTAs, has not been taken apart).
 // Head dimension 64 has half the products for the same exponentials (a step's 1024
 // and 1150 cycles, each alone); a step takes ~2200: its parts, in a chain for either
 // warpgroup, overlap half.
