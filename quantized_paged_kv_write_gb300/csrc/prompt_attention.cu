@@ -29,15 +29,15 @@
 // the causal triangle and mixed lengths make them uneven.
 //
 // Measured (one GB300, 1906 TFLOP/s for a short product, 1699 for seconds of it; a few
-// calls after a rest): head dimension 128, 16384 tokens of 32 heads on 8: 1207 us =
-// 1.82 PFLOP/s of the causal half, 23 prompts of up to 2049 tokens 219 us (142 at
+// calls after a rest): head dimension 128, 16384 tokens of 32 heads on 8: 1199 us =
+// 1.83 PFLOP/s of the causal half, 23 prompts of up to 2049 tokens 218 us (142 at
 // the product's rate), 4 prompts of up to 4097 tokens of 64 on 8 290 us (232); head
-// dimension 64, 3 prompts of up to 5003 tokens of 24 on 8 104 us (49).  Calls for
-// seconds meet the power limit: 1385, 231, 322 and 104 us.  A step (128
+// dimension 64, 3 prompts of up to 5003 tokens of 24 on 8 105 us (49).  Calls for
+// seconds meet the power limit: 1336 to 1389, 236, 314 to 322 and 104 us.  A step (128
 // rows x 128 keys x 2 warpgroups) takes ~2550 cycles where the products alone take
 // 2048: the rest is the hand-over between products and softmax.  A unit's first
 // scores, last outputs and hand-over cost ~2500 cycles more, which short prompts feel
-// (steps and unit ends make ~175 of the 23 prompts' 219 us; where the rest goes, the
+// (steps and unit ends make ~175 of the 23 prompts' 218 us; where the rest goes, the
 // plan, look-ups, the last CTAs, has not been taken apart).
 // Head dimension 64 has half the products for the same exponentials (a step's 1024
 // and 1150 cycles, each alone); a step takes ~2200: its parts, in a chain for either
